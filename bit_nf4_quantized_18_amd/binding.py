@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(PKG, "libqlora_nf4.so")
 QLORA_BF16, QLORA_F32, QLORA_F16 = 0, 1, 2
 MAX_RANK = 128
 BLOCK, DQ_GROUP = 64, 256
+INT8_MAX_COLS, INT8_MAX_K = 1 << 22, 131008  # QLORA_INT8_MAX_COLS, QLORA_INT8_MAX_K
 
 STATUS = {0: "QLORA_OK", -1: "QLORA_ERR_NULL", -2: "QLORA_ERR_SHAPE", -3: "QLORA_ERR_ALIGN",
           -4: "QLORA_ERR_UNSUPPORTED", -5: "QLORA_ERR_WORKSPACE", -6: "QLORA_ERR_HIP"}
@@ -29,7 +30,9 @@ EXPORTS = ("qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd", "ql
            "qlora_requantize", "qlora_linear_dropout_workspace_bytes", "qlora_linear_fwd_dropout",
            "qlora_linear_bwd_dropout", "qlora_dropout_mask", "qlora_linear_fwd_f16", "qlora_linear_bwd_f16",
            "qlora_linear_fwd_grouped_f16", "qlora_linear_bwd_grouped_f16", "qlora_linear_fwd_dropout_f16",
-           "qlora_linear_bwd_dropout_f16", "qlora_linear_fwd_noalloc")
+           "qlora_linear_bwd_dropout_f16", "qlora_linear_fwd_noalloc", "qlora_int8_quantize",
+           "qlora_int8_dequantize", "qlora_rmsnorm_int8", "qlora_int8_linear_fwd",
+           "qlora_int8_linear_workspace_bytes", "qlora_grad_norm", "qlora_grad_clip", "qlora_grad_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 16 << 20  # QLORA_NOALLOC_SCRATCH_BYTES
 
 CODEBOOK_NF4 = 0   # normal-quantile levels
@@ -106,6 +109,22 @@ def load():
     lib.qlora_linear_bwd_dropout.restype = i32
     lib.qlora_dropout_mask.argtypes = [ctypes.c_uint64, ctypes.c_uint64, i64, f32, vp, vp]
     lib.qlora_dropout_mask.restype = i32
+    lib.qlora_int8_quantize.argtypes = [vp, i32, i64, i64, vp, i64, vp, vp]
+    lib.qlora_int8_quantize.restype = i32
+    lib.qlora_int8_dequantize.argtypes = [vp, i64, vp, i64, i64, i32, vp, vp]
+    lib.qlora_int8_dequantize.restype = i32
+    lib.qlora_rmsnorm_int8.argtypes = [vp, vp, vp, i32, i32, i64, i64, f32, vp, vp, i64, vp, vp]
+    lib.qlora_rmsnorm_int8.restype = i32
+    lib.qlora_int8_linear_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.qlora_int8_linear_workspace_bytes.restype = sz
+    lib.qlora_int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, sz, vp]
+    lib.qlora_int8_linear_fwd.restype = i32
+    lib.qlora_grad_workspace_bytes.argtypes = [vp, i32]
+    lib.qlora_grad_workspace_bytes.restype = sz
+    lib.qlora_grad_norm.argtypes = [vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.qlora_grad_norm.restype = i32
+    lib.qlora_grad_clip.argtypes = [vp, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.qlora_grad_clip.restype = i32
     # the fp16 compute calls share their bf16 counterparts' signatures
     for name in ("grouped", "dropout"):
         for d in ("fwd", "bwd"):
@@ -607,6 +626,282 @@ def linear_bwd_grouped(q: PackedNF4, parts, x, dy, a, b, alpha: float, h=None, n
             _stream())
     _check(st, "qlora_linear_bwd_grouped")
     return dx, da, db
+
+
+# ---------------------------------------------------------------- 8-bit rows
+# A merged weight quantized by output channel, activations by token, and their
+# product in 8-bit integers. These calls run once a token or more, so their
+# checks read each attribute of a tensor once.
+_DTYPE = None
+
+
+def _dtype_codes():
+    """torch dtype -> element code of the 16- and 32-bit types the row and gradient calls take."""
+    global _DTYPE
+    if _DTYPE is None:
+        import torch
+
+        _DTYPE = {torch.bfloat16: QLORA_BF16, torch.float32: QLORA_F32, torch.float16: QLORA_F16}
+    return _DTYPE
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on ``dev``'s current stream, with ``dev`` current."""
+    import torch
+
+    if dev.type != "cuda":
+        raise ValueError(f"expected tensors on the GPU, got {dev}")
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+@dataclasses.dataclass
+class PackedInt8:
+    """8-bit rows on the device: n rows of k values, value = code * scale of
+    its row. Rows of codes are padded with zeros to a multiple of 64."""
+    n: int
+    k: int
+    codes: "object"  # int8 [n, ld], ld % 64 == 0, ld >= k, zeros behind the k codes
+    scale: "object"  # float32 [n]
+
+
+def _need_rows(t, name):
+    """dtype code of a contiguous 2-D (rows, cols >= 1) tensor of a 16- or 32-bit type."""
+    code = _dtype_codes().get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be 2-D (rows, cols >= 1), got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return code
+
+
+def _need_int8(q, name, dev):
+    """ld of the 8-bit rows ``q``, whose buffers are checked against n and k."""
+    import torch
+
+    codes, scale = q.codes, q.scale
+    if codes.device != dev or scale.device != dev:
+        raise ValueError(f"{name}: codes and scale must be on {dev}")
+    if codes.dtype != torch.int8 or scale.dtype != torch.float32:
+        raise TypeError(f"{name}: codes must be int8 and scale float32")
+    shape = codes.shape
+    if len(shape) != 2 or shape[0] != q.n or shape[1] % 64 or not 1 <= q.k <= shape[1]:
+        raise ValueError(f"{name}: codes must be ({q.n}, ld) with ld a multiple of 64 and at least k = {q.k}, "
+                         f"got {tuple(shape)}")
+    if scale.dim() != 1 or scale.shape[0] != q.n:
+        raise ValueError(f"{name}: scale must have shape ({q.n},), got {tuple(scale.shape)}")
+    if not codes.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"{name}: codes and scale must be contiguous")
+    return shape[1]
+
+
+def _int8_out(out, n, k, dev):
+    import torch
+
+    if out is None:
+        ld = -(-k // 64) * 64
+        if ld > INT8_MAX_COLS:
+            raise ValueError(f"rows of {k} values are longer than {INT8_MAX_COLS}")
+        return PackedInt8(n, k, torch.empty((n, ld), dtype=torch.int8, device=dev),
+                          torch.empty(n, dtype=torch.float32, device=dev)), ld
+    if out.n != n or out.k != k:
+        raise ValueError(f"out holds {out.n} rows of {out.k} values, expected {n} of {k}")
+    return out, _need_int8(out, "out", dev)
+
+
+def quantize_int8(x, out=None) -> PackedInt8:
+    """8-bit rows of x (rows, cols; bf16, fp16 or float32): a weight by output
+    channel or activations by token (qlora_int8_quantize). ``out`` may be a
+    PackedInt8 of the same sizes."""
+    code = _need_rows(x, "x")
+    dev = x.device
+    n, k = x.shape
+    q, ld = _int8_out(out, n, k, dev)
+    _check(_launch(dev, load().qlora_int8_quantize, x.data_ptr(), code, n, k, q.codes.data_ptr(), ld,
+                   q.scale.data_ptr()), "qlora_int8_quantize")
+    return q
+
+
+def dequantize_int8(q: PackedInt8, dtype=None, out=None):
+    """The values of 8-bit rows as (n, k) of ``dtype`` (bf16 by default)."""
+    import torch
+
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = _dtype_codes().get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    dev = q.codes.device
+    ld = _need_int8(q, "q", dev)
+    if out is None:
+        out = torch.empty((q.n, q.k), dtype=dtype, device=dev)
+    else:
+        _need(out, "out", (q.n, q.k), (dtype,), dev)
+    _check(_launch(dev, load().qlora_int8_dequantize, q.codes.data_ptr(), ld, q.scale.data_ptr(), q.n, q.k, code,
+                   out.data_ptr()), "qlora_int8_dequantize")
+    return out
+
+
+def rmsnorm_int8(x, gain, eps: float = 1e-6, residual=None, residual_out=None, out=None):
+    """Root-mean-square norm of h = x + residual into 8-bit rows
+    (qlora_rmsnorm_int8). x: (rows, cols) bf16, fp16 or float32; residual: the
+    same, or None; gain: (cols,) of x's type or float32. Returns (PackedInt8,
+    h in x's type, or None without a residual). ``residual_out`` may be
+    preallocated, or be ``residual`` or ``x`` itself (in place); ``out`` may be
+    a PackedInt8 of x's sizes."""
+    import torch
+
+    code = _need_rows(x, "x")
+    dev, shape, dtype = x.device, x.shape, x.dtype
+    n, k = shape
+    if gain.dtype != dtype and gain.dtype != torch.float32:
+        raise TypeError(f"gain has dtype {gain.dtype}, expected {dtype} or torch.float32")
+    if gain.device != dev or gain.dim() != 1 or gain.shape[0] != k or not gain.is_contiguous():
+        raise ValueError(f"gain must be a contiguous ({k},) tensor on {dev}")
+    rp = op = None
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out is given without a residual")
+    else:
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+            if t.dtype != dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+            if t.shape != shape or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)} on {dev}")
+        rp, op = residual.data_ptr(), residual_out.data_ptr()
+    q, ld = _int8_out(out, n, k, dev)
+    _check(_launch(dev, load().qlora_rmsnorm_int8, x.data_ptr(), rp, gain.data_ptr(), code,
+                   code if gain.dtype == dtype else QLORA_F32, n, k, eps, op, q.codes.data_ptr(), ld,
+                   q.scale.data_ptr()), "qlora_rmsnorm_int8")
+    return q, residual_out
+
+
+def int8_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Workspace bytes of int8_linear_fwd for m tokens and an (n, k) weight."""
+    return int(load().qlora_int8_linear_workspace_bytes(m, n, -(-k // 64) * 64))
+
+
+def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None, ws=None):
+    """Y = X W^T of 8-bit rows: q the weight by channel (n, k), x the input by
+    token (m, k). Returns (m, n) of ``dtype`` (bf16, fp16 or float32; bf16 by
+    default). ``out`` and ``ws`` (uint8 workspace) may be preallocated."""
+    import torch
+
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = _dtype_codes().get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    dev = q.codes.device
+    ld = _need_int8(q, "q", dev)
+    if x.k != q.k:
+        raise ValueError(f"x holds rows of {x.k} values, the weight rows of {q.k}")
+    if _need_int8(x, "x", dev) != ld:
+        raise ValueError("the rows of x and of the weight must be padded to the same length")
+    m, n = x.n, q.n
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=dev)
+    else:
+        _need(out, "out", (m, n), (dtype,), dev)
+    lib = load()
+    _need_ws(ws, dev)
+    if ws is None:
+        nbytes = lib.qlora_int8_linear_workspace_bytes(m, n, ld)
+        wp = None
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            wp = ws.data_ptr()
+    else:
+        wp, nbytes = ws.data_ptr(), ws.numel()
+    _check(_launch(dev, lib.qlora_int8_linear_fwd, q.codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
+                   x.scale.data_ptr(), m, code, out.data_ptr(), wp, nbytes), "qlora_int8_linear_fwd")
+    return out
+
+
+# ---------------------------------------------------------------- gradients
+class GradList:
+    """Gradients (contiguous tensors of one type on one GPU) checked once, for
+    grad_norm and grad_clip calls of every step on the same buffers. Addresses
+    and lengths are read again at every call; a tensor must keep its type,
+    device and contiguity."""
+
+    def __init__(self, grads):
+        grads = tuple(grads)
+        self.dtype = self.device = None
+        if grads:
+            self.dtype, self.device = grads[0].dtype, grads[0].device
+            self.code = _dtype_codes().get(self.dtype)
+            if self.code is None:
+                raise TypeError(f"gradients must be bfloat16, float16 or float32, got {self.dtype}")
+        for i, g in enumerate(grads):
+            if g.dtype != self.dtype:
+                raise TypeError(f"gradient {i} has dtype {g.dtype}, the first {self.dtype}")
+            if g.device != self.device:
+                raise ValueError(f"gradient {i} is on {g.device}, the first on {self.device}")
+            if not g.is_contiguous():
+                raise ValueError(f"gradient {i} must be contiguous")
+        self.grads = grads
+        self.sizes = [g.numel() for g in grads]
+        self.total = sum(self.sizes)
+        self._numel = (ctypes.c_int64 * max(len(grads), 1))(*self.sizes)
+        self._at = ctypes.c_void_p * max(len(grads), 1)
+        self.ws_bytes = int(load().qlora_grad_workspace_bytes(self._numel, len(grads)))
+        if self.total and not self.ws_bytes:
+            raise ValueError("too many gradients or elements for one call")
+
+    def _pointers(self):
+        if [g.numel() for g in self.grads] != self.sizes:
+            raise ValueError("a gradient changed its length since the list was made")
+        return self._at(*[g.data_ptr() for g in self.grads])
+
+
+def _grad_call(grads, norm, ws, device):
+    import torch
+
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    dev = g.device
+    if dev is None:
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
+        raise ValueError(f"norm must be one float32 on {dev}")
+    _need_ws(ws, dev)
+    if ws is None:
+        ws = torch.empty(max(g.ws_bytes, 1), dtype=torch.uint8, device=dev)
+    return g, dev, norm, ws
+
+
+def grad_norm(grads, norm=None, ws=None):
+    """The norm of all elements of ``grads`` (a list of tensors, or a GradList)
+    as one float32 on the GPU (qlora_grad_norm). ``norm`` and ``ws`` (uint8,
+    GradList.ws_bytes) may be preallocated."""
+    g, dev, norm, ws = _grad_call(grads, norm, ws, None)
+    n = len(g.grads)
+    _check(_launch(dev, load().qlora_grad_norm, g._pointers(), g._numel, n, g.code if n else QLORA_F32,
+                   norm.data_ptr(), ws.data_ptr(), ws.numel()), "qlora_grad_norm")
+    return norm
+
+
+def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
+    """Scale ``grads`` (a list of tensors, or a GradList) by min(1, max_norm /
+    (norm + 1e-6)), in place, or packed one behind the other into ``out`` (1-D,
+    their type and total length). Returns the norm before clipping as one
+    float32 on the GPU (qlora_grad_clip)."""
+    g, dev, norm, ws = _grad_call(grads, norm, ws, None if out is None else out.device)
+    n = len(g.grads)
+    op = None
+    if out is not None:
+        if n:
+            _need(out, "out", (g.total,), (g.dtype,), dev)
+        op = out.data_ptr() if g.total else None
+    _check(_launch(dev, load().qlora_grad_clip, g._pointers(), g._numel, n, g.code if n else QLORA_F32,
+                   float(max_norm), op, norm.data_ptr(), ws.data_ptr(), ws.numel()), "qlora_grad_clip")
+    return norm
 
 
 # ---------------------------------------------------------------- storage

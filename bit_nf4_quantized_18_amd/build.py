@@ -20,10 +20,10 @@ ARCH = "gfx950"
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"-I{INCLUDE}", f"-I{CSRC}", "-Wall", "-Wno-unused-function"]
-# Packed-fp32 instructions are kept out of every device build; the quantizer
-# and merge units are also built without floating-point contraction because
-# their outputs (codes, scale codes, dequantized and merged values) are
-# bit-exact.
+# Packed-fp32 instructions are kept out of every device build; the quantizer,
+# merge and 8-bit units are also built without floating-point contraction
+# because their outputs (codes, scale codes, dequantized and merged values,
+# 8-bit products) are bit-exact.
 DEVICE = ["-x", "hip", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-fno-gpu-rdc", "-munsafe-fp-atomics"]
 SOURCES = {
@@ -37,6 +37,9 @@ SOURCES = {
     "gemv_mfma.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "gemm_kernels.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "noalloc.hip": DEVICE,
+    "int8_rows.hip": DEVICE + ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt"],
+    "int8_gemm.hip": DEVICE + ["-ffp-contract=off"],
+    "grad_clip.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
 }
 
 

@@ -1,6 +1,10 @@
 // C ABI: argument validation, workspace layout and kernel dispatch.
+#include <float.h>
 #include <stddef.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <new>
 
 #include "internal.h"
 
@@ -646,6 +650,165 @@ qlora_status qlora_linear_bwd_f16(const qlora_nf4_weight* w, const uint16_t* x, 
                                   uint16_t* dx, float* da, float* db, void* ws, size_t ws_bytes, hipStream_t stream) {
   return linear_bwd_impl(w, nullptr, x, dy, m, a, b, r, r, alpha, h_saved, dx, da, db, ws, ws_bytes, stream, nullptr,
                          true);
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit rows and their product
+// ---------------------------------------------------------------------------
+static bool known_dtype(int t) { return t == QLORA_BF16 || t == QLORA_F32 || t == QLORA_F16; }
+
+static bool int8_rows_ok(int64_t rows, int64_t cols, int64_t ld) {
+  return rows >= 0 && rows < (INT64_C(1) << 31) && cols >= 1 && ld >= cols && ld % 64 == 0 &&
+         ld <= QLORA_INT8_MAX_COLS;
+}
+
+qlora_status qlora_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, int64_t ld,
+                                 float* scale, hipStream_t stream) {
+  if (!known_dtype(dtype)) return QLORA_ERR_UNSUPPORTED;
+  if (!int8_rows_ok(rows, cols, ld)) return QLORA_ERR_SHAPE;
+  if (rows == 0) return QLORA_OK;
+  if (x == nullptr || codes == nullptr || scale == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return QLORA_ERR_ALIGN;
+  return hip_status(qlora::launch_int8_quantize(x, dtype, rows, cols, codes, ld, scale, stream));
+}
+
+qlora_status qlora_int8_dequantize(const int8_t* codes, int64_t ld, const float* scale, int64_t rows, int64_t cols,
+                                   int dtype, void* out, hipStream_t stream) {
+  if (!known_dtype(dtype)) return QLORA_ERR_UNSUPPORTED;
+  if (!int8_rows_ok(rows, cols, ld)) return QLORA_ERR_SHAPE;
+  if (rows == 0) return QLORA_OK;
+  if (codes == nullptr || scale == nullptr || out == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scale) || !aligned16(out)) return QLORA_ERR_ALIGN;
+  return hip_status(qlora::launch_int8_dequantize(codes, ld, scale, rows, cols, dtype, out, stream));
+}
+
+qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void* gain, int dtype, int gain_dtype,
+                                int64_t rows, int64_t cols, float eps, void* residual_out, int8_t* codes, int64_t ld,
+                                float* scale, hipStream_t stream) {
+  if (!known_dtype(dtype) || (gain_dtype != dtype && gain_dtype != QLORA_F32)) return QLORA_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f && eps <= FLT_MAX)) return QLORA_ERR_UNSUPPORTED;  // NaN fails the test
+  if (!int8_rows_ok(rows, cols, ld)) return QLORA_ERR_SHAPE;
+  if (rows == 0) return QLORA_OK;
+  if (x == nullptr || gain == nullptr || codes == nullptr || scale == nullptr) return QLORA_ERR_NULL;
+  if (residual != nullptr && residual_out == nullptr) return QLORA_ERR_NULL;
+  if (residual == nullptr) residual_out = nullptr;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(residual_out) || !aligned16(codes) ||
+      !aligned16(scale))
+    return QLORA_ERR_ALIGN;
+  return hip_status(qlora::launch_rmsnorm_int8(x, residual, gain, dtype, gain_dtype == QLORA_F32, rows, cols, eps,
+                                               residual_out, codes, ld, scale, stream));
+}
+
+static bool int8_linear_ok(int64_t m, int64_t n, int64_t k) {
+  return m >= 0 && m < (INT64_C(1) << 31) && n >= 1 && n <= (INT64_C(1) << 22) && k >= 64 && k % 64 == 0 &&
+         k <= QLORA_INT8_MAX_K;
+}
+
+size_t qlora_int8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (!int8_linear_ok(m, n, k) || m == 0) return 0;
+  return qlora::int8_linear_ws_bytes(m, n, k);
+}
+
+qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
+                                   const float* x_scale, int64_t m, int out_dtype, void* y, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  if (!known_dtype(out_dtype)) return QLORA_ERR_UNSUPPORTED;
+  if (!int8_linear_ok(m, n, k)) return QLORA_ERR_SHAPE;
+  if (m == 0) return QLORA_OK;
+  if (w == nullptr || w_scale == nullptr || x == nullptr || x_scale == nullptr || y == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(w) || !aligned16(w_scale) || !aligned16(x) || !aligned16(x_scale) || !aligned16(y))
+    return QLORA_ERR_ALIGN;
+  const size_t need = qlora::int8_linear_ws_bytes(m, n, k);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
+  return hip_status(qlora::launch_int8_linear(w, w_scale, n, k, x, x_scale, m, out_dtype, y, ws, stream));
+}
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping
+// ---------------------------------------------------------------------------
+static int dtype_bytes(int t) { return t == QLORA_F32 ? 4 : 2; }
+
+// The lengths are in range; *total is their sum.
+static bool grad_sizes_ok(const int64_t* numel, int count, int64_t* total) {
+  if (count < 0 || count > QLORA_MAX_GRADS || (count > 0 && numel == nullptr)) return false;
+  constexpr int64_t kMost = INT64_C(1) << 40;
+  int64_t sum = 0;
+  for (int i = 0; i < count; ++i) {
+    if (numel[i] < 0 || numel[i] > kMost) return false;
+    sum += numel[i];
+    if (sum > kMost) return false;
+  }
+  *total = sum;
+  return true;
+}
+
+static qlora_status check_grads(const void* const* grads, const int64_t* numel, int count, int dtype, const float* norm,
+                                const void* ws, size_t ws_bytes, int64_t* total) {
+  if (!known_dtype(dtype)) return QLORA_ERR_UNSUPPORTED;
+  if (count > 0 && (grads == nullptr || numel == nullptr)) return QLORA_ERR_NULL;
+  if (!grad_sizes_ok(numel, count, total)) return QLORA_ERR_SHAPE;
+  if (norm == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(norm)) return QLORA_ERR_ALIGN;
+  const uintptr_t mask = static_cast<uintptr_t>(dtype_bytes(dtype) - 1);
+  for (int i = 0; i < count; ++i) {
+    if (numel[i] == 0) continue;
+    if (grads[i] == nullptr) return QLORA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(grads[i]) & mask) != 0) return QLORA_ERR_ALIGN;
+  }
+  const size_t need = qlora::grad_ws_bytes(numel, count);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+size_t qlora_grad_workspace_bytes(const int64_t* numel, int count) {
+  int64_t total = 0;
+  return grad_sizes_ok(numel, count, &total) ? qlora::grad_ws_bytes(numel, count) : 0;
+}
+
+qlora_status qlora_grad_norm(const void* const* grads, const int64_t* numel, int count, int dtype, float* norm,
+                             void* ws, size_t ws_bytes, hipStream_t stream) {
+  int64_t total = 0;
+  const qlora_status st = check_grads(grads, numel, count, dtype, norm, ws, ws_bytes, &total);
+  if (st != QLORA_OK) return st;
+  return hip_status(qlora::launch_grad_clip(grads, numel, count, dtype, false, 0.0f, nullptr, norm, ws, stream));
+}
+
+qlora_status qlora_grad_clip(void* const* grads, const int64_t* numel, int count, int dtype, float max_norm, void* out,
+                             float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!(max_norm >= 0.0f)) return QLORA_ERR_UNSUPPORTED;  // NaN fails the test
+  int64_t total = 0;
+  const qlora_status st = check_grads(grads, numel, count, dtype, norm, ws, ws_bytes, &total);
+  if (st != QLORA_OK) return st;
+  const uintptr_t size = static_cast<uintptr_t>(dtype_bytes(dtype));
+  if (out != nullptr) {
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), o1 = o0 + static_cast<uintptr_t>(total) * size;
+    if ((o0 & (size - 1)) != 0) return QLORA_ERR_ALIGN;
+    for (int i = 0; i < count; ++i) {
+      const uintptr_t g0 = reinterpret_cast<uintptr_t>(grads[i]), g1 = g0 + static_cast<uintptr_t>(numel[i]) * size;
+      if (numel[i] > 0 && g0 < o1 && o0 < g1) return QLORA_ERR_UNSUPPORTED;
+    }
+  } else if (count > 1) {
+    // in place: two tensors on the same memory would be scaled twice, in a race
+    struct Range {
+      uintptr_t at, end;
+    };
+    Range* r = new (std::nothrow) Range[static_cast<size_t>(count)];
+    if (r == nullptr) return QLORA_ERR_WORKSPACE;
+    int used = 0;
+    for (int i = 0; i < count; ++i) {
+      const uintptr_t g0 = reinterpret_cast<uintptr_t>(grads[i]);
+      if (numel[i] > 0) r[used++] = Range{g0, g0 + static_cast<uintptr_t>(numel[i]) * size};
+    }
+    std::sort(r, r + used, [](const Range& a, const Range& b) { return a.at < b.at; });
+    bool apart = true;
+    for (int i = 1; i < used; ++i) apart = apart && r[i - 1].end <= r[i].at;
+    delete[] r;
+    if (!apart) return QLORA_ERR_UNSUPPORTED;
+  }
+  return hip_status(qlora::launch_grad_clip(const_cast<const void* const*>(grads), numel, count, dtype, true, max_norm,
+                                            out, norm, ws, stream));
 }
 
 }  // extern "C"

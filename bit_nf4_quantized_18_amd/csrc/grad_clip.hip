@@ -1,0 +1,178 @@
+// The global norm of a list of gradients, and clipping by it.
+//
+// norm = sqrt(sum over all tensors of g^2); out = g min(1, max_norm / (norm +
+// 1e-6)). The factor depends on every element, so the gradients are read
+// twice and written once: bound by memory. Squares are summed in 64 bits (two
+// more instructions an element, far under the memory's rate), so no square
+// over- or underflows, and in a fixed order, so results repeat bit for bit.
+//
+// The tensors are cut into chunks. The list reaches the first kernel by value,
+// kTensors a launch (a launch's arguments end at 4 KB): it sums the squares of
+// its chunks and leaves in the workspace one partial sum a workgroup and one
+// record a chunk (address, place in the output, length). The second kernel
+// takes all records of all launches: every workgroup forms the norm from the
+// partial sums in the same order, then scales its chunks.
+#include "elem.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kTensors = 180;
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 1024;  // workgroups of a launch
+
+struct Slice {
+  const void* at[kTensors];
+  int64_t off[kTensors + 1];  // elements in front of tensor i in the list
+  int32_t first[kTensors];    // its first chunk, counted over all launches
+};
+static_assert(sizeof(Slice) <= 3900, "kernel arguments end at 4 KB");
+
+struct Record {
+  const void* at;
+  int64_t off;
+  int64_t len;
+};
+
+// Sum over the workgroup in a fixed order, in every thread.
+__device__ __forceinline__ double reduce_sum(double v) {
+  __shared__ double sums[kThreads / 64];
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int i = 0; i < kThreads / 64; ++i) v += sums[i];
+  return v;
+}
+
+template <int kType>
+__global__ __launch_bounds__(kThreads) void square_sum_kernel(Slice l, int tensors, int chunk0, int chunk1,
+                                                              int64_t chunk, double* partial, Record* records) {
+  typedef Elem<kType> G;
+  double sum = 0.0;
+  for (int c = chunk0 + blockIdx.x; c < chunk1; c += gridDim.x) {
+    int t = 0;  // the last tensor that starts at or in front of chunk c
+    for (int i = 1; i < tensors; ++i) t = l.first[i] <= c ? i : t;
+    const int64_t begin = (c - l.first[t]) * chunk, size = l.off[t + 1] - l.off[t];
+    const int64_t len = size - begin < chunk ? size - begin : chunk;
+    const typename G::T* p = static_cast<const typename G::T*>(l.at[t]) + begin;
+    if (records != nullptr && threadIdx.x == 0) records[c] = Record{p, l.off[t] + begin, len};
+    for (int64_t j = threadIdx.x; j < len; j += kThreads) {
+      const double v = static_cast<double>(G::get(p[j]));
+      sum += v * v;
+    }
+  }
+  sum = reduce_sum(sum);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+// clip = false: only the norm (one workgroup). out null: in place.
+template <int kType>
+__global__ __launch_bounds__(kThreads) void scale_kernel(const double* partial, int partials, const Record* records,
+                                                         int chunks, bool clip, float max_norm, void* out,
+                                                         float* norm_out) {
+  typedef Elem<kType> G;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
+  const double norm = sqrt(reduce_sum(sum));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
+  if (!clip) return;
+  float f = 1.0f;
+  const double ratio = static_cast<double>(max_norm) / (norm + 1e-6);
+  if (!(ratio >= 1.0) && !__builtin_isinf(max_norm)) f = static_cast<float>(ratio);  // a NaN norm: NaN
+  if (out == nullptr && f == 1.0f) return;
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const Record r = records[c];
+    const typename G::T* p = static_cast<const typename G::T*>(r.at);
+    typename G::T* o = out == nullptr ? const_cast<typename G::T*>(p) : static_cast<typename G::T*>(out) + r.off;
+    for (int64_t j = threadIdx.x; j < r.len; j += kThreads) o[j] = G::put(G::get(p[j]) * f);
+  }
+}
+
+// Chunk length and what follows from it.
+struct Plan {
+  int64_t chunk;
+  int chunks;    // of all tensors
+  int partials;  // workgroups of all first launches
+};
+
+int64_t chunks_of(int64_t numel, int64_t chunk) { return (numel + chunk - 1) / chunk; }
+
+Plan plan_for(const int64_t* numel, int count) {
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) total += numel[i];
+  Plan p{};
+  p.chunk = 16384;
+  while (total / p.chunk > (1 << 20)) p.chunk *= 2;  // chunks are numbered in 32 bits
+  int64_t chunks = 0, in_slice = 0;
+  int tensors = 0;
+  for (int i = 0; i < count; ++i) {
+    if (numel[i] == 0) continue;
+    const int64_t c = chunks_of(numel[i], p.chunk);
+    chunks += c;
+    in_slice += c;
+    if (++tensors == kTensors) {
+      p.partials += static_cast<int>(in_slice < kMaxBlocks ? in_slice : kMaxBlocks);
+      tensors = 0;
+      in_slice = 0;
+    }
+  }
+  if (tensors > 0) p.partials += static_cast<int>(in_slice < kMaxBlocks ? in_slice : kMaxBlocks);
+  p.chunks = static_cast<int>(chunks);
+  return p;
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+template <int kType>
+hipError_t launch_t(const void* const* grads, const int64_t* numel, int count, bool clip, float max_norm, void* out,
+                    float* norm, void* ws, hipStream_t s) {
+  const Plan p = plan_for(numel, count);
+  double* partial = static_cast<double*>(ws);
+  Record* records = reinterpret_cast<Record*>(static_cast<char*>(ws) + up256(p.partials * 8));
+  Slice l{};
+  int tensors = 0, chunk0 = 0, chunk1 = 0, partials = 0;
+  int64_t off = 0;
+  for (int i = 0; i <= count; ++i) {
+    if (i < count && numel[i] > 0) {
+      l.at[tensors] = grads[i];
+      l.off[tensors] = off;
+      l.first[tensors] = chunk1;
+      off += numel[i];
+      chunk1 += static_cast<int>(chunks_of(numel[i], p.chunk));
+      l.off[++tensors] = off;
+    }
+    if (tensors == kTensors || (i == count && tensors > 0)) {
+      const int blocks = chunk1 - chunk0 < kMaxBlocks ? chunk1 - chunk0 : kMaxBlocks;
+      hipLaunchKernelGGL((square_sum_kernel<kType>), dim3(blocks), dim3(kThreads), 0, s, l, tensors, chunk0, chunk1,
+                         p.chunk, partial + partials, clip ? records : nullptr);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      partials += blocks;
+      chunk0 = chunk1;
+      tensors = 0;
+    }
+  }
+  int blocks = clip ? (p.chunks < 2 * kMaxBlocks ? p.chunks : 2 * kMaxBlocks) : 1;
+  if (blocks < 1) blocks = 1;
+  hipLaunchKernelGGL((scale_kernel<kType>), dim3(blocks), dim3(kThreads), 0, s, partial, partials, records, p.chunks,
+                     clip, max_norm, out, norm);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t grad_ws_bytes(const int64_t* numel, int count) {
+  const Plan p = plan_for(numel, count);
+  return static_cast<size_t>(up256(p.partials * 8) + up256(static_cast<int64_t>(p.chunks) * sizeof(Record)));
+}
+
+hipError_t launch_grad_clip(const void* const* grads, const int64_t* numel, int count, int dtype, bool clip,
+                            float max_norm, void* out, float* norm, void* ws, hipStream_t s) {
+  auto fn = dtype == QLORA_F32 ? launch_t<QLORA_F32> : dtype == QLORA_F16 ? launch_t<QLORA_F16> : launch_t<QLORA_BF16>;
+  return fn(grads, numel, count, clip, max_norm, out, norm, ws, s);
+}
+
+}  // namespace qlora

@@ -193,4 +193,25 @@ qlora_status linear_fwd_scratch(const qlora_nf4_weight* w, const uint16_t* x, in
                                 const uint16_t* b, int r, float alpha, uint16_t* y, float* h_out, void* scratch,
                                 size_t scratch_bytes, hipStream_t stream);
 
+// 8-bit rows. dtype arguments are QLORA_BF16, QLORA_F32 or QLORA_F16.
+hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, int64_t ld,
+                                float* scale, hipStream_t s);
+hipError_t launch_int8_dequantize(const int8_t* codes, int64_t ld, const float* scale, int64_t rows, int64_t cols,
+                                  int dtype, void* out, hipStream_t s);
+// residual and residual_out are both null or both given.
+hipError_t launch_rmsnorm_int8(const void* x, const void* residual, const void* gain, int dtype, bool gain_f32,
+                               int64_t rows, int64_t cols, float eps, void* residual_out, int8_t* codes, int64_t ld,
+                               float* scale, hipStream_t s);
+
+// The 8-bit product; ws holds int8_linear_ws_bytes(m, n, k) bytes.
+size_t int8_linear_ws_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
+                              const float* x_scale, int64_t m, int out_dtype, void* y, void* ws, hipStream_t s);
+
+// Global norm of a list of tensors and (clip) their scaling: out null writes
+// in place. total is the sum of numel; ws holds grad_ws_bytes(numel, count).
+size_t grad_ws_bytes(const int64_t* numel, int count);
+hipError_t launch_grad_clip(const void* const* grads, const int64_t* numel, int count, int dtype, bool clip,
+                            float max_norm, void* out, float* norm, void* ws, hipStream_t s);
+
 }  // namespace qlora

@@ -402,6 +402,123 @@ qlora_status qlora_requantize(const qlora_nf4_weight* w, const uint16_t* a, cons
                               uint8_t* codes, uint8_t* scale_codes, float* group_scale,
                               float* absmax, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit serving of a merged layer. A merged weight (qlora_merge) is quantized
+ * once by output channel, the layer's input by token, and the product of the
+ * two is taken in 8-bit integers.
+ *
+ * 8-bit rows: `rows` rows of `cols` values are held as int8 codes, row i at
+ * codes + i ld (ld % 64 == 0, ld >= cols; the ld - cols codes behind a row's
+ * values are zeros, so the product contracts over whole rows of ld codes), and
+ * one float32 scale a row; the value is code * scale[i]. With a_i the row's
+ * largest magnitude: scale[i] = fl32(a_i / 127), code = 127 x / a_i rounded to
+ * the nearest integer in exact arithmetic, ties to even, so |code| <= 127. A
+ * row of zeros has scale 0 and codes 0. A row that holds a NaN or an infinity
+ * has scale NaN and codes 0: it comes back from every use as NaN.
+ * ------------------------------------------------------------------------- */
+
+#define QLORA_INT8_MAX_COLS (1 << 22) /* largest ld the row calls take              */
+#define QLORA_INT8_MAX_K 131008       /* largest contraction of the 8-bit product:  */
+                                      /* k 128^2 stays below 2^31 for any codes     */
+
+/* Quantize rows to 8 bit: a weight by channel, activations by token.
+ *   x       : rows x cols of `dtype` (QLORA_BF16, QLORA_F16 or QLORA_F32).
+ *   codes   : rows x ld int8, written whole (zeros behind the cols values).
+ *   scale   : rows float32.
+ *   rows 0 .. 2^31 - 1 (0: nothing is done); cols >= 1.
+ * Bit-exact with the CPU oracle. Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtype) / HIP. */
+qlora_status qlora_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes,
+                                 int64_t ld, float* scale, hipStream_t stream);
+
+/* The values of 8-bit rows: out (rows x cols of `dtype`) = code * scale, one
+ * float32 product rounded to nearest even into `dtype`. Sizes and errors as
+ * qlora_int8_quantize. */
+qlora_status qlora_int8_dequantize(const int8_t* codes, int64_t ld, const float* scale, int64_t rows,
+                                   int64_t cols, int dtype, void* out, hipStream_t stream);
+
+/* Root-mean-square norm with the residual's addition in front of it and 8-bit
+ * rows behind it, as a decoder layer has them in front of q/k/v and gate/up:
+ *   h = x + residual (float32; h = x without a residual),
+ *   y = h gain / sqrt(mean(h^2) + eps), quantized as qlora_int8_quantize's rows.
+ * With v = fl32(h gain) and a = max |v| over the row, the codes are 127 v / a
+ * rounded as above (the norm's factor cancels) and scale = fl32(a / (127
+ * sqrt(mean(h^2) + eps))), where the sum of squares is kept in 64 bits. A row
+ * with a NaN or an infinity in h or v has scale NaN and codes 0.
+ *   x, residual : rows x cols of `dtype`; residual may be NULL.
+ *   gain        : cols values of `gain_dtype`: `dtype` or QLORA_F32.
+ *   eps         : finite, >= 0.
+ *   residual_out: rows x cols of `dtype`, h rounded to nearest even; required
+ *                 with a residual, ignored without. May be `residual` or `x`
+ *                 itself (in place).
+ *   codes, ld, scale: the 8-bit rows written.
+ * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtypes, eps) / HIP. */
+qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void* gain, int dtype,
+                                int gain_dtype, int64_t rows, int64_t cols, float eps,
+                                void* residual_out, int8_t* codes, int64_t ld, float* scale,
+                                hipStream_t stream);
+
+/* The 8-bit product Y[i][j] = (fl32(sum_q x[i][q] w[j][q]) * x_scale[i]) *
+ * w_scale[j], rounded to nearest even into `out_dtype`. The sums are exact
+ * 32-bit integers, so Y does not depend on how the work is split: a token's
+ * row is bit-identical at every m.
+ *   w, w_scale : 8-bit rows of the weight (n x k, one scale a channel).
+ *   x, x_scale : 8-bit rows of the input (m x k, one scale a token). k is the
+ *                row length ld of both: k % 64 == 0, 64 .. QLORA_INT8_MAX_K.
+ *   n          : 1 .. 2^22, n k <= 2^40; m 0 .. 2^31 - 1 (0: nothing is done).
+ *   out_dtype  : QLORA_BF16, QLORA_F16 or QLORA_F32; y is m x n.
+ *   ws         : qlora_int8_linear_workspace_bytes(m, n, k) bytes (may be NULL
+ *                when that is 0). Calls that may overlap need one each.
+ * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (out_dtype) / WORKSPACE / HIP. */
+qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_t n, int64_t k,
+                                   const int8_t* x, const float* x_scale, int64_t m, int out_dtype,
+                                   void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes for qlora_int8_linear_fwd; 0 for invalid sizes and where the
+ * call needs none. Host only, no GPU use. */
+size_t qlora_int8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/* ---------------------------------------------------------------------------
+ * The global norm of a training step's adapter gradients (the dA and dB of
+ * every layer's backward) and clipping by it.
+ *   grads : count device pointers, in a host array that is read during the
+ *           call; tensor i holds numel[i] >= 0 elements of `dtype`
+ *           (QLORA_F32, QLORA_BF16 or QLORA_F16) and is aligned to its
+ *           element size (16 bytes are not needed here).
+ *   count : 0 .. QLORA_MAX_GRADS; their elements are at most 2^40 in total.
+ *   norm  : one float32, sqrt of the sum of all squares; the squares are
+ *           summed in 64 bits in a fixed order, so they do not overflow and
+ *           two calls on the same values and lengths agree bit for bit. 0
+ *           without elements; NaN or infinity where an element is.
+ *   ws    : qlora_grad_workspace_bytes(numel, count) bytes.
+ * ------------------------------------------------------------------------- */
+
+#define QLORA_MAX_GRADS (1 << 20) /* most tensors in one call */
+
+/* Errors: NULL / ALIGN / SHAPE (count or a length out of range) / UNSUPPORTED
+ * (dtype) / WORKSPACE / HIP. */
+qlora_status qlora_grad_norm(const void* const* grads, const int64_t* numel, int count, int dtype,
+                             float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* norm as qlora_grad_norm, then every element times min(1, max_norm / (norm +
+ * 1e-6)), that factor computed in 64 bits and rounded once to float32, the
+ * product rounded to nearest even into `dtype`. A NaN norm makes every element
+ * NaN; an infinite norm gives the factor 0 (elements that are infinite become
+ * NaN).
+ *   max_norm : >= 0 (infinity: nothing is scaled).
+ *   out      : NULL writes in place; otherwise one buffer of the tensors'
+ *              total length that takes them packed one behind the other in
+ *              list order (`dtype`, aligned to the element size).
+ * Tensors that overlap each other (in place) or the output are refused.
+ * Errors: as qlora_grad_norm; UNSUPPORTED also for a NaN or negative max_norm
+ * and for overlapping buffers. */
+qlora_status qlora_grad_clip(void* const* grads, const int64_t* numel, int count, int dtype,
+                             float max_norm, void* out, float* norm, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* Workspace bytes for the two calls above; 0 for invalid arguments. Host
+ * only, no GPU use. */
+size_t qlora_grad_workspace_bytes(const int64_t* numel, int count);
+
 /* Static, NUL-terminated description of a status (any int: values that are
  * no qlora_status get a generic text). Host only. */
 const char* qlora_status_string(int status);
