@@ -35,4 +35,25 @@ struct Elem<QLORA_F32> {
   static __device__ __forceinline__ T put(float f) { return f; }
 };
 
+// 16 bytes at any element's address: global memory takes them in one access
+// whatever the alignment.
+struct __attribute__((packed, aligned(2))) Any16 {
+  u32x4 v;
+};
+__device__ __forceinline__ u32x4 ld16_any(const void* p) { return static_cast<const Any16*>(p)->v; }
+__device__ __forceinline__ void st16_any(void* p, u32x4 v) { static_cast<Any16*>(p)->v = v; }
+
+// Four float32 as elements, in the words [0, sizeof(T)) of a store.
+template <int kType>
+__device__ __forceinline__ void put4(uint32_t* w, const float* f) {
+  typedef Elem<kType> E;
+  if constexpr (kType == QLORA_F32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(f[e]);
+  } else {
+    w[0] = E::put(f[0]) | static_cast<uint32_t>(E::put(f[1])) << 16;
+    w[1] = E::put(f[2]) | static_cast<uint32_t>(E::put(f[3])) << 16;
+  }
+}
+
 }  // namespace qlora
