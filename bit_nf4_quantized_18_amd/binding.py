@@ -630,31 +630,41 @@ def linear_bwd_grouped(q: PackedNF4, parts, x, dy, a, b, alpha: float, h=None, n
 
 # ---------------------------------------------------------------- 8-bit rows
 # A merged weight quantized by output channel, activations by token, and their
-# product in 8-bit integers. These calls run once a token or more, so their
-# checks read each attribute of a tensor once.
-_DTYPE = None
+# product in 8-bit integers. At decode these calls take less time on the GPU
+# than their issue on the host, so they look torch and the library up once and
+# read each attribute of a tensor once.
+_torch = None      # the torch module, after _init()
+_DTYPE = None      # torch dtype -> element code of the 16- and 32-bit types
+_raw_stream = None  # device index -> the current stream's handle
+_device_now = None  # the current device's index
 
 
-def _dtype_codes():
-    """torch dtype -> element code of the 16- and 32-bit types the row and gradient calls take."""
-    global _DTYPE
-    if _DTYPE is None:
-        import torch
-
-        _DTYPE = {torch.bfloat16: QLORA_BF16, torch.float32: QLORA_F32, torch.float16: QLORA_F16}
-    return _DTYPE
-
-
-def _launch(dev, fn, *args):
-    """fn(*args, stream) on ``dev``'s current stream, with ``dev`` current."""
+def _init():
+    global _torch, _DTYPE, _raw_stream, _device_now
     import torch
 
-    if dev.type != "cuda":
-        raise ValueError(f"expected tensors on the GPU, got {dev}")
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _DTYPE = {torch.bfloat16: QLORA_BF16, torch.float32: QLORA_F32, torch.float16: QLORA_F16}
+    # torch's own accessors behind torch.cuda.current_stream() and
+    # current_device(), without the stream object these make
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
+    load()
+
+
+def _launch(where, index, *args):
+    """The library's function ``where`` with args and the current stream of
+    GPU ``index``, that GPU being current; raises on a status."""
+    if index < 0:
+        raise ValueError("expected tensors on the GPU")
+    if index == _device_now():
+        status = getattr(_LIB, where)(*args, _raw_stream(index))
+    else:
+        with _torch.cuda.device(index):
+            status = getattr(_LIB, where)(*args, _raw_stream(index))
+    if status:
+        raise QloraError(status, where)
 
 
 @dataclasses.dataclass
@@ -667,81 +677,88 @@ class PackedInt8:
     scale: "object"  # float32 [n]
 
 
-def _need_rows(t, name):
-    """dtype code of a contiguous 2-D (rows, cols >= 1) tensor of a 16- or 32-bit type."""
-    code = _dtype_codes().get(t.dtype)
+def _need_rows(x, name):
+    """(dtype code, rows, cols, GPU index) of a contiguous 2-D tensor of a 16-
+    or 32-bit type with one column at least (-1: not on a GPU)."""
+    if _torch is None:
+        _init()
+    code = _DTYPE.get(x.dtype)
     if code is None:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{name} must be 2-D (rows, cols >= 1), got shape {tuple(t.shape)}")
-    if not t.is_contiguous():
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    shape = x.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be 2-D (rows, cols >= 1), got shape {tuple(shape)}")
+    if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return code
+    return code, shape[0], shape[1], x.get_device()
 
 
-def _need_int8(q, name, dev):
+def _need_int8(q, name, index):
     """ld of the 8-bit rows ``q``, whose buffers are checked against n and k."""
-    import torch
-
+    if _torch is None:
+        _init()
     codes, scale = q.codes, q.scale
-    if codes.device != dev or scale.device != dev:
-        raise ValueError(f"{name}: codes and scale must be on {dev}")
-    if codes.dtype != torch.int8 or scale.dtype != torch.float32:
+    if codes.dtype is not _torch.int8 or scale.dtype is not _torch.float32:
         raise TypeError(f"{name}: codes must be int8 and scale float32")
     shape = codes.shape
     if len(shape) != 2 or shape[0] != q.n or shape[1] % 64 or not 1 <= q.k <= shape[1]:
         raise ValueError(f"{name}: codes must be ({q.n}, ld) with ld a multiple of 64 and at least k = {q.k}, "
                          f"got {tuple(shape)}")
-    if scale.dim() != 1 or scale.shape[0] != q.n:
+    if scale.shape != (q.n,):
         raise ValueError(f"{name}: scale must have shape ({q.n},), got {tuple(scale.shape)}")
+    if codes.get_device() != index or scale.get_device() != index:
+        raise ValueError(f"{name}: codes and scale must be on one GPU, the call's")
     if not codes.is_contiguous() or not scale.is_contiguous():
         raise ValueError(f"{name}: codes and scale must be contiguous")
     return shape[1]
 
 
-def _int8_out(out, n, k, dev):
-    import torch
+def _int8_out(out, n, k, like, index):
+    """(PackedInt8 of n rows of k values on ``like``'s device, its ld): new, or ``out`` checked."""
+    if out is not None:
+        if out.n != n or out.k != k:
+            raise ValueError(f"out holds {out.n} rows of {out.k} values, expected {n} of {k}")
+        return out, _need_int8(out, "out", index)
+    ld = -(-k // 64) * 64
+    if ld > INT8_MAX_COLS:
+        raise ValueError(f"rows of {k} values are longer than {INT8_MAX_COLS}")
+    return PackedInt8(n, k, like.new_empty((n, ld), dtype=_torch.int8),
+                      like.new_empty((n,), dtype=_torch.float32)), ld
 
-    if out is None:
-        ld = -(-k // 64) * 64
-        if ld > INT8_MAX_COLS:
-            raise ValueError(f"rows of {k} values are longer than {INT8_MAX_COLS}")
-        return PackedInt8(n, k, torch.empty((n, ld), dtype=torch.int8, device=dev),
-                          torch.empty(n, dtype=torch.float32, device=dev)), ld
-    if out.n != n or out.k != k:
-        raise ValueError(f"out holds {out.n} rows of {out.k} values, expected {n} of {k}")
-    return out, _need_int8(out, "out", dev)
+
+def _out_dtype(dtype):
+    """(torch dtype, its code); None is bfloat16."""
+    if _torch is None:
+        _init()
+    if dtype is None:
+        dtype = _torch.bfloat16
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    return dtype, code
 
 
 def quantize_int8(x, out=None) -> PackedInt8:
     """8-bit rows of x (rows, cols; bf16, fp16 or float32): a weight by output
     channel or activations by token (qlora_int8_quantize). ``out`` may be a
     PackedInt8 of the same sizes."""
-    code = _need_rows(x, "x")
-    dev = x.device
-    n, k = x.shape
-    q, ld = _int8_out(out, n, k, dev)
-    _check(_launch(dev, load().qlora_int8_quantize, x.data_ptr(), code, n, k, q.codes.data_ptr(), ld,
-                   q.scale.data_ptr()), "qlora_int8_quantize")
+    code, n, k, index = _need_rows(x, "x")
+    q, ld = _int8_out(out, n, k, x, index)
+    _launch("qlora_int8_quantize", index, x.data_ptr(), code, n, k, q.codes.data_ptr(), ld, q.scale.data_ptr())
     return q
 
 
 def dequantize_int8(q: PackedInt8, dtype=None, out=None):
     """The values of 8-bit rows as (n, k) of ``dtype`` (bf16 by default)."""
-    import torch
-
-    dtype = torch.bfloat16 if dtype is None else dtype
-    code = _dtype_codes().get(dtype)
-    if code is None:
-        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    dev = q.codes.device
-    ld = _need_int8(q, "q", dev)
+    dtype, code = _out_dtype(dtype)
+    codes = q.codes
+    index = codes.get_device()
+    ld = _need_int8(q, "q", index)
     if out is None:
-        out = torch.empty((q.n, q.k), dtype=dtype, device=dev)
+        out = codes.new_empty((q.n, q.k), dtype=dtype)
     else:
-        _need(out, "out", (q.n, q.k), (dtype,), dev)
-    _check(_launch(dev, load().qlora_int8_dequantize, q.codes.data_ptr(), ld, q.scale.data_ptr(), q.n, q.k, code,
-                   out.data_ptr()), "qlora_int8_dequantize")
+        _need(out, "out", (q.n, q.k), (dtype,), codes.device)
+    _launch("qlora_int8_dequantize", index, codes.data_ptr(), ld, q.scale.data_ptr(), q.n, q.k, code, out.data_ptr())
     return out
 
 
@@ -752,33 +769,35 @@ def rmsnorm_int8(x, gain, eps: float = 1e-6, residual=None, residual_out=None, o
     h in x's type, or None without a residual). ``residual_out`` may be
     preallocated, or be ``residual`` or ``x`` itself (in place); ``out`` may be
     a PackedInt8 of x's sizes."""
-    import torch
-
-    code = _need_rows(x, "x")
-    dev, shape, dtype = x.device, x.shape, x.dtype
-    n, k = shape
-    if gain.dtype != dtype and gain.dtype != torch.float32:
+    code, n, k, index = _need_rows(x, "x")
+    dtype = x.dtype
+    gain_code = code if gain.dtype is dtype else QLORA_F32
+    if gain_code != code and gain.dtype is not _torch.float32:
         raise TypeError(f"gain has dtype {gain.dtype}, expected {dtype} or torch.float32")
-    if gain.device != dev or gain.dim() != 1 or gain.shape[0] != k or not gain.is_contiguous():
-        raise ValueError(f"gain must be a contiguous ({k},) tensor on {dev}")
+    if gain.shape != (k,) or gain.get_device() != index or not gain.is_contiguous():
+        raise ValueError(f"gain must be a contiguous ({k},) tensor on x's device")
     rp = op = None
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out is given without a residual")
     else:
+        _need_like(residual, "residual", x, index)
         if residual_out is None:
-            residual_out = torch.empty_like(x)
-        for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-            if t.dtype != dtype:
-                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-            if t.shape != shape or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)} on {dev}")
+            residual_out = x.new_empty((n, k))
+        else:
+            _need_like(residual_out, "residual_out", x, index)
         rp, op = residual.data_ptr(), residual_out.data_ptr()
-    q, ld = _int8_out(out, n, k, dev)
-    _check(_launch(dev, load().qlora_rmsnorm_int8, x.data_ptr(), rp, gain.data_ptr(), code,
-                   code if gain.dtype == dtype else QLORA_F32, n, k, eps, op, q.codes.data_ptr(), ld,
-                   q.scale.data_ptr()), "qlora_rmsnorm_int8")
+    q, ld = _int8_out(out, n, k, x, index)
+    _launch("qlora_rmsnorm_int8", index, x.data_ptr(), rp, gain.data_ptr(), code, gain_code, n, k, eps, op,
+            q.codes.data_ptr(), ld, q.scale.data_ptr())
     return q, residual_out
+
+
+def _need_like(t, name, x, index):
+    if t.dtype is not x.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
+    if t.shape != x.shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(x.shape)} on x's device")
 
 
 def int8_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -790,35 +809,30 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None, ws=None)
     """Y = X W^T of 8-bit rows: q the weight by channel (n, k), x the input by
     token (m, k). Returns (m, n) of ``dtype`` (bf16, fp16 or float32; bf16 by
     default). ``out`` and ``ws`` (uint8 workspace) may be preallocated."""
-    import torch
-
-    dtype = torch.bfloat16 if dtype is None else dtype
-    code = _dtype_codes().get(dtype)
-    if code is None:
-        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    dev = q.codes.device
-    ld = _need_int8(q, "q", dev)
+    dtype, code = _out_dtype(dtype)
+    codes = q.codes
+    index = codes.get_device()
+    ld = _need_int8(q, "q", index)
     if x.k != q.k:
         raise ValueError(f"x holds rows of {x.k} values, the weight rows of {q.k}")
-    if _need_int8(x, "x", dev) != ld:
+    if _need_int8(x, "x", index) != ld:
         raise ValueError("the rows of x and of the weight must be padded to the same length")
     m, n = x.n, q.n
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=dev)
+        out = codes.new_empty((m, n), dtype=dtype)
     else:
-        _need(out, "out", (m, n), (dtype,), dev)
-    lib = load()
-    _need_ws(ws, dev)
-    if ws is None:
-        nbytes = lib.qlora_int8_linear_workspace_bytes(m, n, ld)
-        wp = None
-        if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            wp = ws.data_ptr()
-    else:
+        _need(out, "out", (m, n), (dtype,), codes.device)
+    wp = None
+    if ws is not None:
+        _need_ws(ws, codes.device)
         wp, nbytes = ws.data_ptr(), ws.numel()
-    _check(_launch(dev, lib.qlora_int8_linear_fwd, q.codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
-                   x.scale.data_ptr(), m, code, out.data_ptr(), wp, nbytes), "qlora_int8_linear_fwd")
+    else:
+        nbytes = _LIB.qlora_int8_linear_workspace_bytes(m, n, ld)
+        if nbytes:
+            ws = codes.new_empty((nbytes,), dtype=_torch.uint8)
+            wp = ws.data_ptr()
+    _launch("qlora_int8_linear_fwd", index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
+            x.scale.data_ptr(), m, code, out.data_ptr(), wp, nbytes)
     return out
 
 
@@ -830,18 +844,19 @@ class GradList:
     device and contiguity."""
 
     def __init__(self, grads):
+        if _torch is None:
+            _init()
         grads = tuple(grads)
-        self.dtype = self.device = None
-        if grads:
-            self.dtype, self.device = grads[0].dtype, grads[0].device
-            self.code = _dtype_codes().get(self.dtype)
-            if self.code is None:
-                raise TypeError(f"gradients must be bfloat16, float16 or float32, got {self.dtype}")
+        self.dtype = grads[0].dtype if grads else None
+        self.code = _DTYPE.get(self.dtype) if grads else QLORA_F32
+        self.index = grads[0].get_device() if grads else None
+        if self.code is None:
+            raise TypeError(f"gradients must be bfloat16, float16 or float32, got {self.dtype}")
         for i, g in enumerate(grads):
-            if g.dtype != self.dtype:
+            if g.dtype is not self.dtype:
                 raise TypeError(f"gradient {i} has dtype {g.dtype}, the first {self.dtype}")
-            if g.device != self.device:
-                raise ValueError(f"gradient {i} is on {g.device}, the first on {self.device}")
+            if g.get_device() != self.index:
+                raise ValueError(f"gradient {i} is on {g.device}, the first on {grads[0].device}")
             if not g.is_contiguous():
                 raise ValueError(f"gradient {i} must be contiguous")
         self.grads = grads
@@ -849,41 +864,39 @@ class GradList:
         self.total = sum(self.sizes)
         self._numel = (ctypes.c_int64 * max(len(grads), 1))(*self.sizes)
         self._at = ctypes.c_void_p * max(len(grads), 1)
-        self.ws_bytes = int(load().qlora_grad_workspace_bytes(self._numel, len(grads)))
+        self.ws_bytes = int(_LIB.qlora_grad_workspace_bytes(self._numel, len(grads)))
         if self.total and not self.ws_bytes:
             raise ValueError("too many gradients or elements for one call")
 
     def _pointers(self):
-        if [g.numel() for g in self.grads] != self.sizes:
+        tensor = _torch.Tensor
+        if list(map(tensor.numel, self.grads)) != self.sizes:
             raise ValueError("a gradient changed its length since the list was made")
-        return self._at(*[g.data_ptr() for g in self.grads])
+        return self._at(*map(tensor.data_ptr, self.grads))
 
 
-def _grad_call(grads, norm, ws, device):
-    import torch
-
-    g = grads if isinstance(grads, GradList) else GradList(grads)
-    dev = g.device
-    if dev is None:
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+def _grad_buffers(g, index, norm, ws):
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
-        raise ValueError(f"norm must be one float32 on {dev}")
-    _need_ws(ws, dev)
+        norm = _torch.empty((), dtype=_torch.float32, device=f"cuda:{index}") if not g.grads else \
+            g.grads[0].new_empty((), dtype=_torch.float32)
+    elif norm.dtype is not _torch.float32 or norm.numel() != 1 or norm.get_device() != index:
+        raise ValueError("norm must be one float32 on the gradients' device")
     if ws is None:
-        ws = torch.empty(max(g.ws_bytes, 1), dtype=torch.uint8, device=dev)
-    return g, dev, norm, ws
+        ws = norm.new_empty((g.ws_bytes,), dtype=_torch.uint8)
+    else:
+        _need_ws(ws, norm.device)
+    return norm, ws
 
 
 def grad_norm(grads, norm=None, ws=None):
     """The norm of all elements of ``grads`` (a list of tensors, or a GradList)
     as one float32 on the GPU (qlora_grad_norm). ``norm`` and ``ws`` (uint8,
     GradList.ws_bytes) may be preallocated."""
-    g, dev, norm, ws = _grad_call(grads, norm, ws, None)
-    n = len(g.grads)
-    _check(_launch(dev, load().qlora_grad_norm, g._pointers(), g._numel, n, g.code if n else QLORA_F32,
-                   norm.data_ptr(), ws.data_ptr(), ws.numel()), "qlora_grad_norm")
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    index = g.index if g.grads else _device_now()
+    norm, ws = _grad_buffers(g, index, norm, ws)
+    _launch("qlora_grad_norm", index, g._pointers(), g._numel, len(g.grads), g.code, norm.data_ptr(), ws.data_ptr(),
+            ws.numel())
     return norm
 
 
@@ -892,15 +905,15 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
     (norm + 1e-6)), in place, or packed one behind the other into ``out`` (1-D,
     their type and total length). Returns the norm before clipping as one
     float32 on the GPU (qlora_grad_clip)."""
-    g, dev, norm, ws = _grad_call(grads, norm, ws, None if out is None else out.device)
-    n = len(g.grads)
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    index = g.index if g.grads else _device_now()
     op = None
-    if out is not None:
-        if n:
-            _need(out, "out", (g.total,), (g.dtype,), dev)
+    if out is not None and g.grads:
+        _need(out, "out", (g.total,), (g.dtype,), g.grads[0].device)
         op = out.data_ptr() if g.total else None
-    _check(_launch(dev, load().qlora_grad_clip, g._pointers(), g._numel, n, g.code if n else QLORA_F32,
-                   float(max_norm), op, norm.data_ptr(), ws.data_ptr(), ws.numel()), "qlora_grad_clip")
+    norm, ws = _grad_buffers(g, index, norm, ws)
+    _launch("qlora_grad_clip", index, g._pointers(), g._numel, len(g.grads), g.code, max_norm, op, norm.data_ptr(),
+            ws.data_ptr(), ws.numel())
     return norm
 
 
