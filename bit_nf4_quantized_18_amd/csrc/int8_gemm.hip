@@ -31,14 +31,8 @@ struct LinearArgs {
 // ---------------------------------------------------------------------------
 // Tiles through LDS.
 // ---------------------------------------------------------------------------
-constexpr int kBK = 64;     // contraction codes a step: one MFMA deep
-constexpr int kStages = 4;  // LDS ring
+constexpr int kUnit = 128;  // contraction codes of a stage: a whole cache line of a row
 constexpr int kXcds = 8;
-
-template <int BM, int BN>
-constexpr int stage_bytes() {
-  return (BM + BN) * kBK;
-}
 
 // 16 neighbouring outputs of one token: (acc sx) sw, each rounded once, the
 // first `left` of them stored.
@@ -73,22 +67,23 @@ __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t src, int8_t* dst,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)dst, 16, off, 0, 0, 0);
 }
 
-// Chunk order of a quad of rows (see below).
-__device__ __forceinline__ int quad_key(int q) { return ((q << 1) & 3) ^ ((q >> 1) * 3); }
-
-template <int BM, int BN, int WM, int WN, int kType>
+// S: stages of the LDS ring.
+template <int BM, int BN, int WM, int WN, int S, int kType>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave: tokens, channels
-  constexpr int LX = BM / 16 / kWaves, LW = BN / 16 / kWaves;  // 1 KB loads of a wave a stage
+  constexpr int LX = BM / 8 / kWaves, LW = BN / 8 / kWaves;  // 1 KB copies of a wave a stage
   constexpr int kLoads = LX + LW;
-  static_assert(TN % 4 == 0 && LX >= 1 && LW >= 1 && kWaves % 4 == 0, "tile shape");
+  constexpr int kBytes = (BM + BN) * kUnit;
+  static_assert(TN % 4 == 0 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && S >= 2 && S <= 4, "tile shape");
   typedef typename Elem<kType>::T T;
 
-  __shared__ __attribute__((aligned(1024))) int8_t s0[stage_bytes<BM, BN>()];
-  __shared__ __attribute__((aligned(1024))) int8_t s1[stage_bytes<BM, BN>()];
-  __shared__ __attribute__((aligned(1024))) int8_t s2[stage_bytes<BM, BN>()];
-  __shared__ __attribute__((aligned(1024))) int8_t s3[stage_bytes<BM, BN>()];
+  // one array a stage: the compiler can then tell a copy into one stage from
+  // the reads of another, and waits for none of them by itself
+  __shared__ __attribute__((aligned(1024))) int8_t s0[kBytes];
+  __shared__ __attribute__((aligned(1024))) int8_t s1[kBytes];
+  __shared__ __attribute__((aligned(1024))) int8_t s2[S > 2 ? kBytes : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t s3[S > 3 ? kBytes : 16];
 
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -105,89 +100,108 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   const int64_t m0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(b0 + in % rows)) * BM;
   const int64_t n0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(in / rows)) * BN;
 
-  const int nk = static_cast<int>(g.k / kBK);
+  const int units = static_cast<int>((g.k + kUnit - 1) / kUnit), whole = static_cast<int>(g.k / kUnit);
   const int mrows = static_cast<int>(g.m - m0 < BM ? g.m - m0 : BM), nrows = static_cast<int>(g.n - n0 < BN ? g.n - n0 : BN);
+  // Ranges of the tile's own rows: the last unit of a contraction that is no
+  // multiple of 128 reads past its rows, into the next row or, past the last
+  // one, into zeros; neither is multiplied.
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.k, mrows * g.k);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + n0 * g.k, nrows * g.k);
 
-  // Load l of a wave fills block l kWaves + wave: 16 rows of 64 bytes, lane l
-  // the 16 bytes at row l / 4, place l % 4.
-  const int lr = lane >> 2, lc = lane & 3;
+  // Copy l of a wave fills block l kWaves + wave of a stage: 8 rows of 128
+  // bytes, lane l the 16 bytes at row l / 8, place l % 8. A row's chunk c
+  // stands at place c ^ key(row). The 16 lanes that read one chunk column
+  // then fall on 16 different 16-byte columns of the banks, both as 16
+  // neighbouring lanes and as four quads of lanes out of two columns.
+  const int lr = lane >> 3, lc = lane & 7;
   int xo[LX], wo[LW];
 #pragma unroll
   for (int l = 0; l < LX; ++l) {
-    const int row = 16 * (l * kWaves + wave) + lr;
-    xo[l] = static_cast<int>((row < mrows ? row : mrows - 1) * g.k) + 16 * (lc ^ quad_key(lr >> 2));
+    const int row = 8 * (l * kWaves + wave) + lr;
+    xo[l] = static_cast<int>((row < mrows ? row : mrows - 1) * g.k) + 16 * (lc ^ ((row >> 1) & 7));
   }
 #pragma unroll
   for (int l = 0; l < LW; ++l) {
-    const int row = 16 * (l * kWaves + wave) + lr;
-    wo[l] = static_cast<int>((row < nrows ? row : nrows - 1) * g.k) + 16 * (lc ^ quad_key(wave & 3));
+    const int row = 8 * (l * kWaves + wave) + lr;
+    wo[l] = static_cast<int>((row < nrows ? row : nrows - 1) * g.k) +
+            16 * (lc ^ (2 * ((row >> 4) & 3) + ((row >> 1) & 1)));
   }
-  auto copy = [&](int8_t* stage, int kt) {
-    const int q = (kt < nk ? kt : nk - 1) * kBK;
+  auto copy = [&](int8_t* stage, int u) {
+    const int q = (u < units ? u : units - 1) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LX; ++l)
-      copy_1k(xr, stage + (l * kWaves + wave) * 1024, xo[l] + q);
+    for (int l = 0; l < LX; ++l) copy_1k(xr, stage + (l * kWaves + wave) * 1024, xo[l] + q);
 #pragma unroll
-    for (int l = 0; l < LW; ++l)
-      copy_1k(wr, stage + BM * kBK + (l * kWaves + wave) * 1024, wo[l] + q);
+    for (int l = 0; l < LW; ++l) copy_1k(wr, stage + BM * kUnit + (l * kWaves + wave) * 1024, wo[l] + q);
   };
-  const int xa = (wm * TM * 16 + i) * kBK + 16 * (h ^ quad_key(i >> 2));
-  const int wa = BM * kBK + (wn * TN * 16 + 16 * (i >> 2) + (i & 3)) * kBK + 16 * (h ^ quad_key(i >> 2));
+  // Fragments of the stage's first or second 64 codes. Token tile t reads rows
+  // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,
+  // which leaves a lane with runs of 16 neighbouring channels. Both keys are
+  // i / 2.
+  const int xa = (wm * TM * 16 + i) * kUnit;
+  const int wa = BM * kUnit + (wn * TN * 16 + 16 * (i >> 2) + (i & 3)) * kUnit;
+  const int place[2] = {16 * (h ^ (i >> 1)), 16 * ((4 + h) ^ (i >> 1))};
   u32x4 fx[2][TM], fw[2][TN];
-  auto read = [&](const int8_t* stage, int set) {
+  auto read = [&](const int8_t* stage, int half) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t) fw[set][t] = ld16(stage + wa + (t >> 2) * (64 * kBK) + (t & 3) * (4 * kBK));
+    for (int t = 0; t < TN; ++t)
+      fw[half][t] = ld16(stage + wa + place[half] + (t >> 2) * (64 * kUnit) + (t & 3) * (4 * kUnit));
 #pragma unroll
-    for (int t = 0; t < TM; ++t) fx[set][t] = ld16(stage + xa + t * (16 * kBK));
+    for (int t = 0; t < TM; ++t) fx[half][t] = ld16(stage + xa + place[half] + t * (16 * kUnit));
   };
   i32x4 acc[TM][TN];
 #pragma unroll
   for (int a = 0; a < TM; ++a)
 #pragma unroll
     for (int b = 0; b < TN; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
-  auto multiply = [&](int set) {
+  auto multiply = [&](int half) {
 #pragma unroll
     for (int a = 0; a < TM; ++a)
 #pragma unroll
-      for (int b = 0; b < TN; ++b) acc[a][b] = mma8(fw[set][b], fx[set][a], acc[a][b]);
+      for (int b = 0; b < TN; ++b) acc[a][b] = mma8(fw[half][b], fx[half][a], acc[a][b]);
   };
-  // Step kt: its fragments are in set; the next stage has to be whole, then
-  // its fragments are read and this step's stage is filled again while the
-  // matrix cores run.
-  auto step = [&](int kt, int set, int8_t* mine, const int8_t* next) {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this step's fragments have left the stage
-    wait_vmcnt<(kStages - 2) * kLoads>();
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    read(next, set ^ 1);
-    copy(mine, kt + kStages);
-    multiply(set);
+  // Unit u, whose first half's fragments are in registers: its second half is
+  // read while the first is multiplied; then the next unit has to be whole,
+  // its first half is read and this unit's stage filled again while the second
+  // is multiplied. One barrier a unit.
+  auto unit = [&](int u, int8_t* mine, const int8_t* next) {
+    read(mine, 1);
+    multiply(0);
 #pragma unroll
     for (int j = 0; j < TM + TN; ++j) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                        // LDS read
-      if (j % 2 == 0 && j / 2 < kLoads) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // copy
-      __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);      // MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                    // LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);  // MFMA
     }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the fragments have left this unit's stage
+    wait_vmcnt<(S - 2) * kLoads>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(next, 0);
+    copy(mine, u + S);
+    multiply(1);
+#pragma unroll
+    for (int j = 0; j < TM + TN; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (j < kLoads) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // copy
+      __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  copy(s0, 0);
-  copy(s1, 1);
-  copy(s2, 2);
-  copy(s3, 3);
-  wait_vmcnt<(kStages - 1) * kLoads>();
+  int8_t* const ring[4] = {s0, s1, S > 2 ? s2 : s0, S > 3 ? s3 : s0};
+#pragma unroll
+  for (int u = 0; u < S; ++u) copy(ring[u], u);
+  wait_vmcnt<(S - 1) * kLoads>();
   __builtin_amdgcn_s_barrier();
   read(s0, 0);
-  int kt = 0;
-  for (; kt + 4 <= nk; kt += 4) {
-    step(kt, 0, s0, s1);
-    step(kt + 1, 1, s1, s2);
-    step(kt + 2, 0, s2, s3);
-    step(kt + 3, 1, s3, s0);
+  int u = 0;
+  for (; u + S <= whole; u += S) {
+#pragma unroll
+    for (int j = 0; j < S; ++j) unit(u + j, ring[j], ring[(j + 1) % S]);
   }
-  if (kt < nk) step(kt, 0, s0, s1);
-  if (kt + 1 < nk) step(kt + 1, 1, s1, s2);
-  if (kt + 2 < nk) step(kt + 2, 0, s2, s3);
+#pragma unroll
+  for (int j = 0; j < S - 1; ++j)
+    if (u + j < whole) unit(u + j, ring[j], ring[(j + 1) % S]);
+  if (whole < units) multiply(0);
   wait_vmcnt<0>();  // no copy may be in flight when the workgroup's LDS is given on
 
   // Lane: tokens 16 a + i, channels 64 (b / 4) + 16 h + 4 (b % 4) + v: runs of
@@ -207,13 +221,113 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int S>
 hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
   const int tiles_m = static_cast<int>((g.m + BM - 1) / BM), tiles_n = static_cast<int>((g.n + BN - 1) / BN);
-  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, QLORA_F32>
-              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, QLORA_F16>
-                                       : tile_kernel<BM, BN, WM, WN, QLORA_BF16>;
+  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, S, QLORA_F32>
+              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, S, QLORA_F16>
+                                       : tile_kernel<BM, BN, WM, WN, S, QLORA_BF16>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(64 * WM * WN), 0, s, g, tiles_m, tiles_n);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the weight is streamed once, bound by memory. A workgroup of 16
+// waves takes 16 channels; its waves split the contraction, each reading its
+// runs of the 16 rows straight into registers, all loads in flight at once,
+// and add their integer sums through LDS.
+// ---------------------------------------------------------------------------
+constexpr int kDecodeWaves = 8;
+constexpr int kDecodeBlocks = 256;
+
+// J: 64-code steps of a wave a pass; TT: tiles of 16 tokens. kOne: one pass
+// covers the contraction, so the tokens stay in registers while the workgroup
+// goes through its channels, and the next weight rows are on their way while
+// the sums of the last ones are added.
+template <int J, int TT, bool kOne, int kType>
+__global__ __launch_bounds__(64 * kDecodeWaves) void decode_kernel(LinearArgs g, int groups) {
+  __shared__ int part[2][kDecodeWaves][TT * 256];
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int steps = static_cast<int>(g.k / 64);
+  const int8_t* xp[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xp[t] = g.x + (16 * t + i < g.m ? 16 * t + i : g.m - 1) * g.k + 16 * h;
+  // Step j of this wave in the pass at `base`; past the end the last step is
+  // read again and multiplied by zeros.
+  auto at = [&](int base, int j) {
+    const int s = base + wave * J + j;
+    return 64 * (s < steps ? s : steps - 1);
+  };
+  u32x4 wf[J], xf[TT][J];
+  auto read_w = [&](int group, int base) {
+    const int64_t n = static_cast<int64_t>(group) * 16 + i;
+    const int8_t* wp = g.w + (n < g.n ? n : g.n - 1) * g.k + 16 * h;
+#pragma unroll
+    for (int j = 0; j < J; ++j) wf[j] = ld16(wp + at(base, j));
+  };
+  auto read_x = [&](int base) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        xf[t][j] = ld16(xp[t] + at(base, j));
+        if (base + wave * J + j >= steps) xf[t][j] = u32x4{0, 0, 0, 0};
+      }
+  };
+  read_w(blockIdx.x, 0);
+  read_x(0);
+  int turn = 0;
+  for (int group = blockIdx.x; group < groups; group += gridDim.x, turn ^= 1) {
+    i32x4 acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+    auto multiply = [&] {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] = mma8(wf[j], xf[t][j], acc[t]);
+    };
+    if (kOne) {
+      multiply();
+      const int next = group + gridDim.x;
+      if (next < groups) read_w(next, 0);
+    } else {
+      for (int base = 0; base < steps; base += kDecodeWaves * J) {
+        if (base > 0 || group != static_cast<int>(blockIdx.x)) {
+          read_w(group, base);
+          read_x(base);
+        }
+        multiply();
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) *reinterpret_cast<i32x4*>(&part[turn][wave][t * 256 + 4 * lane]) = acc[t];
+    __syncthreads();  // the other turn's sums have been read by all in front of this
+    // output e: token e / 16, channel e % 16
+    const int64_t n = static_cast<int64_t>(group) * 16 + (tid & 15);
+#pragma unroll
+    for (int e = tid; e < TT * 256; e += 64 * kDecodeWaves) {
+      const int64_t m = e >> 4;
+      if (m >= g.m || n >= g.n) continue;
+      const int from = (e >> 8) * 256 + 4 * (((e >> 4) & 15) + 16 * ((e & 15) >> 2)) + (e & 3);
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < kDecodeWaves; ++w) sum += part[turn][w][from];
+      static_cast<typename Elem<kType>::T*>(g.y)[m * g.n + n] =
+          Elem<kType>::put((static_cast<float>(sum) * g.sx[m]) * g.sw[n]);
+    }
+  }
+}
+
+template <int J, int TT, bool kOne>
+hipError_t launch_decode(const LinearArgs& g, int out_dtype, hipStream_t s) {
+  const int groups = static_cast<int>((g.n + 15) / 16);
+  const int blocks = kOne && groups > kDecodeBlocks ? kDecodeBlocks : groups;
+  auto kern = out_dtype == QLORA_F32   ? decode_kernel<J, TT, kOne, QLORA_F32>
+              : out_dtype == QLORA_F16 ? decode_kernel<J, TT, kOne, QLORA_F16>
+                                       : decode_kernel<J, TT, kOne, QLORA_BF16>;
+  hipLaunchKernelGGL(kern, dim3(blocks), dim3(64 * kDecodeWaves), 0, s, g, groups);
   return hipGetLastError();
 }
 
@@ -262,7 +376,17 @@ size_t int8_linear_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
 hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
                               const float* x_scale, int64_t m, int out_dtype, void* y, void*, hipStream_t s) {
   const LinearArgs g{w, w_scale, x, x_scale, y, m, n, k};
-  if (m > 256) return launch_tiles<256, 256, 2, 4>(g, out_dtype, s);
+  if (m <= 16) {
+    if (k <= 2048) return launch_decode<4, 1, true>(g, out_dtype, s);
+    if (k <= 4096) return launch_decode<8, 1, true>(g, out_dtype, s);
+    return launch_decode<4, 1, false>(g, out_dtype, s);
+  }
+  if (m <= 32) {
+    if (k <= 2048) return launch_decode<4, 2, true>(g, out_dtype, s);
+    if (k <= 4096) return launch_decode<8, 2, true>(g, out_dtype, s);
+    return launch_decode<4, 2, false>(g, out_dtype, s);
+  }
+  if (m > 32) return launch_tiles<256, 256, 2, 4, 2>(g, out_dtype, s);
   const int64_t tiles = ((m + kTM - 1) / kTM) * ((n + kTN - 1) / kTN);
   auto kern = out_dtype == QLORA_F32   ? linear_kernel<QLORA_F32>
               : out_dtype == QLORA_F16 ? linear_kernel<QLORA_F16>
