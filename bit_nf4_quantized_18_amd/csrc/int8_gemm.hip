@@ -67,23 +67,33 @@ __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t src, int8_t* dst,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)dst, 16, off, 0, 0, 0);
 }
 
-// S: stages of the LDS ring.
-template <int BM, int BN, int WM, int WN, int S, int kType>
+// P: parts of the LDS ring. A unit of 128 codes is two parts, the tokens' and
+// the channels'; the ring holds P / 2 units, and with an odd P the tokens' part
+// of one more, so that half of the codes have a unit's time more to arrive.
+template <int BM, int BN, int WM, int WN, int P, int kType>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave: tokens, channels
   constexpr int LX = BM / 8 / kWaves, LW = BN / 8 / kWaves;  // 1 KB copies of a wave a stage
   constexpr int kLoads = LX + LW;
-  constexpr int kBytes = (BM + BN) * kUnit;
-  static_assert(TN % 4 == 0 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && S >= 2 && S <= 4, "tile shape");
+  constexpr int S = P / 2;        // units that the ring holds whole
+  constexpr bool kOdd = P % 2 != 0;
+  constexpr int kTurn = kOdd ? P : S;  // units after which parts lie in the same places again
+  static_assert(TN % 4 == 0 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
+  static_assert(P >= 4 && P <= 8 && (!kOdd || BM == BN), "ring");
   typedef typename Elem<kType>::T T;
 
-  // one array a stage: the compiler can then tell a copy into one stage from
-  // the reads of another, and waits for none of them by itself
-  __shared__ __attribute__((aligned(1024))) int8_t s0[kBytes];
-  __shared__ __attribute__((aligned(1024))) int8_t s1[kBytes];
-  __shared__ __attribute__((aligned(1024))) int8_t s2[S > 2 ? kBytes : 16];
-  __shared__ __attribute__((aligned(1024))) int8_t s3[S > 3 ? kBytes : 16];
+  // one array a part: the compiler can then tell a copy into one part from the
+  // reads of another, and waits for none of them by itself
+  __shared__ __attribute__((aligned(1024))) int8_t p0[BM * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p1[BN * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p2[BM * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p3[BN * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p4[P > 4 ? BM * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p5[P > 5 ? BN * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p6[P > 6 ? BM * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p7[P > 7 ? BN * kUnit : 16];
+  int8_t* const ring[8] = {p0, p1, p2, p3, p4, p5, p6, p7};
 
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -126,27 +136,30 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
     wo[l] = static_cast<int>((row < nrows ? row : nrows - 1) * g.k) +
             16 * (lc ^ (2 * ((row >> 4) & 3) + ((row >> 1) & 1)));
   }
-  auto copy = [&](int8_t* stage, int u) {
+  auto copy_x = [&](int8_t* to, int u) {
     const int q = (u < units ? u : units - 1) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LX; ++l) copy_1k(xr, stage + (l * kWaves + wave) * 1024, xo[l] + q);
+    for (int l = 0; l < LX; ++l) copy_1k(xr, to + (l * kWaves + wave) * 1024, xo[l] + q);
+  };
+  auto copy_w = [&](int8_t* to, int u) {
+    const int q = (u < units ? u : units - 1) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LW; ++l) copy_1k(wr, stage + BM * kUnit + (l * kWaves + wave) * 1024, wo[l] + q);
+    for (int l = 0; l < LW; ++l) copy_1k(wr, to + (l * kWaves + wave) * 1024, wo[l] + q);
   };
   // Fragments of the stage's first or second 64 codes. Token tile t reads rows
   // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,
   // which leaves a lane with runs of 16 neighbouring channels. Both keys are
   // i / 2.
   const int xa = (wm * TM * 16 + i) * kUnit;
-  const int wa = BM * kUnit + (wn * TN * 16 + 16 * (i >> 2) + (i & 3)) * kUnit;
+  const int wa = (wn * TN * 16 + 16 * (i >> 2) + (i & 3)) * kUnit;
   const int place[2] = {16 * (h ^ (i >> 1)), 16 * ((4 + h) ^ (i >> 1))};
   u32x4 fx[2][TM], fw[2][TN];
-  auto read = [&](const int8_t* stage, int half) {
+  auto read = [&](const int8_t* x, const int8_t* w, int half) {
 #pragma unroll
     for (int t = 0; t < TN; ++t)
-      fw[half][t] = ld16(stage + wa + place[half] + (t >> 2) * (64 * kUnit) + (t & 3) * (4 * kUnit));
+      fw[half][t] = ld16(w + wa + place[half] + (t >> 2) * (64 * kUnit) + (t & 3) * (4 * kUnit));
 #pragma unroll
-    for (int t = 0; t < TM; ++t) fx[half][t] = ld16(stage + xa + place[half] + t * (16 * kUnit));
+    for (int t = 0; t < TM; ++t) fx[half][t] = ld16(x + xa + place[half] + t * (16 * kUnit));
   };
   i32x4 acc[TM][TN];
 #pragma unroll
@@ -161,10 +174,10 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   };
   // Unit u, whose first half's fragments are in registers: its second half is
   // read while the first is multiplied; then the next unit has to be whole,
-  // its first half is read and this unit's stage filled again while the second
+  // its first half is read and this unit's parts filled again while the second
   // is multiplied. One barrier a unit.
-  auto unit = [&](int u, int8_t* mine, const int8_t* next) {
-    read(mine, 1);
+  auto unit = [&](int u, int8_t* x, int8_t* w, const int8_t* next_x, const int8_t* next_w) {
+    read(x, w, 1);
     multiply(0);
 #pragma unroll
     for (int j = 0; j < TM + TN; ++j) {
@@ -172,35 +185,45 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
       __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);  // MFMA
     }
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the fragments have left this unit's stage
-    wait_vmcnt<(S - 2) * kLoads>();
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the fragments have left this unit's parts
+    wait_vmcnt<(S - 2) * kLoads + (kOdd ? LX : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read(next, 0);
-    copy(mine, u + S);
+    if (kOdd) {
+      copy_w(x, u + S);
+      copy_x(w, u + S + 1);
+    } else {
+      copy_x(x, u + S);
+      copy_w(w, u + S);
+    }
+    read(next_x, next_w, 0);
     multiply(1);
 #pragma unroll
     for (int j = 0; j < TM + TN; ++j) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       if (j < kLoads) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // copy
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  int8_t* const ring[4] = {s0, s1, S > 2 ? s2 : s0, S > 3 ? s3 : s0};
 #pragma unroll
-  for (int u = 0; u < S; ++u) copy(ring[u], u);
-  wait_vmcnt<(S - 1) * kLoads>();
+  for (int p = 0; p < P; ++p) {
+    if (p % 2 == 0) copy_x(ring[p], p / 2);
+    else copy_w(ring[p], p / 2);
+  }
+  wait_vmcnt<(S - 1) * kLoads + (kOdd ? LX : 0)>();
   __builtin_amdgcn_s_barrier();
-  read(s0, 0);
+  read(p0, p1, 0);
   int u = 0;
-  for (; u + S <= whole; u += S) {
+  for (; u + kTurn <= whole; u += kTurn) {
 #pragma unroll
-    for (int j = 0; j < S; ++j) unit(u + j, ring[j], ring[(j + 1) % S]);
+    for (int j = 0; j < kTurn; ++j)
+      unit(u + j, ring[2 * j % P], ring[(2 * j + 1) % P], ring[(2 * j + 2) % P], ring[(2 * j + 3) % P]);
   }
 #pragma unroll
-  for (int j = 0; j < S - 1; ++j)
-    if (u + j < whole) unit(u + j, ring[j], ring[(j + 1) % S]);
+  for (int j = 0; j < kTurn - 1; ++j)
+    if (u + j < whole)
+      unit(u + j, ring[2 * j % P], ring[(2 * j + 1) % P], ring[(2 * j + 2) % P], ring[(2 * j + 3) % P]);
   if (whole < units) multiply(0);
   wait_vmcnt<0>();  // no copy may be in flight when the workgroup's LDS is given on
 
@@ -221,12 +244,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   }
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int P>
 hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
   const int tiles_m = static_cast<int>((g.m + BM - 1) / BM), tiles_n = static_cast<int>((g.n + BN - 1) / BN);
-  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, S, QLORA_F32>
-              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, S, QLORA_F16>
-                                       : tile_kernel<BM, BN, WM, WN, S, QLORA_BF16>;
+  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, P, QLORA_F32>
+              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, P, QLORA_F16>
+                                       : tile_kernel<BM, BN, WM, WN, P, QLORA_BF16>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(64 * WM * WN), 0, s, g, tiles_m, tiles_n);
   return hipGetLastError();
 }
@@ -386,7 +409,7 @@ hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, 
     if (k <= 4096) return launch_decode<8, 2, true>(g, out_dtype, s);
     return launch_decode<4, 2, false>(g, out_dtype, s);
   }
-  if (m > 32) return launch_tiles<256, 256, 2, 4, 2>(g, out_dtype, s);
+  if (m > 32) return launch_tiles<256, 256, 2, 4, 5>(g, out_dtype, s);
   const int64_t tiles = ((m + kTM - 1) / kTM) * ((n + kTN - 1) / kTN);
   auto kern = out_dtype == QLORA_F32   ? linear_kernel<QLORA_F32>
               : out_dtype == QLORA_F16 ? linear_kernel<QLORA_F16>
