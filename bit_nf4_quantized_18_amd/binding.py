@@ -32,7 +32,7 @@ EXPORTS = ("qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd", "ql
            "qlora_linear_fwd_grouped_f16", "qlora_linear_bwd_grouped_f16", "qlora_linear_fwd_dropout_f16",
            "qlora_linear_bwd_dropout_f16", "qlora_linear_fwd_noalloc", "qlora_int8_quantize",
            "qlora_int8_dequantize", "qlora_rmsnorm_int8", "qlora_int8_linear_fwd",
-           "qlora_int8_linear_workspace_bytes", "qlora_grad_norm", "qlora_grad_clip", "qlora_grad_workspace_bytes")
+           "qlora_grad_norm", "qlora_grad_clip", "qlora_grad_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 16 << 20  # QLORA_NOALLOC_SCRATCH_BYTES
 
 CODEBOOK_NF4 = 0   # normal-quantile levels
@@ -115,9 +115,7 @@ def load():
     lib.qlora_int8_dequantize.restype = i32
     lib.qlora_rmsnorm_int8.argtypes = [vp, vp, vp, i32, i32, i64, i64, f32, vp, vp, i64, vp, vp]
     lib.qlora_rmsnorm_int8.restype = i32
-    lib.qlora_int8_linear_workspace_bytes.argtypes = [i64, i64, i64]
-    lib.qlora_int8_linear_workspace_bytes.restype = sz
-    lib.qlora_int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, sz, vp]
+    lib.qlora_int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp]
     lib.qlora_int8_linear_fwd.restype = i32
     lib.qlora_grad_workspace_bytes.argtypes = [vp, i32]
     lib.qlora_grad_workspace_bytes.restype = sz
@@ -800,15 +798,10 @@ def _need_like(t, name, x, index):
         raise ValueError(f"{name} must be contiguous, of shape {tuple(x.shape)} on x's device")
 
 
-def int8_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Workspace bytes of int8_linear_fwd for m tokens and an (n, k) weight."""
-    return int(load().qlora_int8_linear_workspace_bytes(m, n, -(-k // 64) * 64))
-
-
-def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None, ws=None):
+def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
     """Y = X W^T of 8-bit rows: q the weight by channel (n, k), x the input by
     token (m, k). Returns (m, n) of ``dtype`` (bf16, fp16 or float32; bf16 by
-    default). ``out`` and ``ws`` (uint8 workspace) may be preallocated."""
+    default). ``out`` may be preallocated."""
     dtype, code = _out_dtype(dtype)
     codes = q.codes
     index = codes.get_device()
@@ -822,17 +815,8 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None, ws=None)
         out = codes.new_empty((m, n), dtype=dtype)
     else:
         _need(out, "out", (m, n), (dtype,), codes.device)
-    wp = None
-    if ws is not None:
-        _need_ws(ws, codes.device)
-        wp, nbytes = ws.data_ptr(), ws.numel()
-    else:
-        nbytes = _LIB.qlora_int8_linear_workspace_bytes(m, n, ld)
-        if nbytes:
-            ws = codes.new_empty((nbytes,), dtype=_torch.uint8)
-            wp = ws.data_ptr()
     _launch("qlora_int8_linear_fwd", index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
-            x.scale.data_ptr(), m, code, out.data_ptr(), wp, nbytes)
+            x.scale.data_ptr(), m, code, out.data_ptr())
     return out
 
 

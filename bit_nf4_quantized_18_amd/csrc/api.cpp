@@ -704,24 +704,15 @@ static bool int8_linear_ok(int64_t m, int64_t n, int64_t k) {
          k <= QLORA_INT8_MAX_K;
 }
 
-size_t qlora_int8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (!int8_linear_ok(m, n, k) || m == 0) return 0;
-  return qlora::int8_linear_ws_bytes(m, n, k);
-}
-
 qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
-                                   const float* x_scale, int64_t m, int out_dtype, void* y, void* ws, size_t ws_bytes,
-                                   hipStream_t stream) {
+                                   const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t stream) {
   if (!known_dtype(out_dtype)) return QLORA_ERR_UNSUPPORTED;
-  if (!int8_linear_ok(m, n, k)) return QLORA_ERR_SHAPE;
+  if (!int8_linear_ok(m, n, k) || !qlora::int8_linear_fits(m, n, k)) return QLORA_ERR_SHAPE;
   if (m == 0) return QLORA_OK;
   if (w == nullptr || w_scale == nullptr || x == nullptr || x_scale == nullptr || y == nullptr) return QLORA_ERR_NULL;
   if (!aligned16(w) || !aligned16(w_scale) || !aligned16(x) || !aligned16(x_scale) || !aligned16(y))
     return QLORA_ERR_ALIGN;
-  const size_t need = qlora::int8_linear_ws_bytes(m, n, k);
-  if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
-  if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
-  return hip_status(qlora::launch_int8_linear(w, w_scale, n, k, x, x_scale, m, out_dtype, y, ws, stream));
+  return hip_status(qlora::launch_int8_linear(w, w_scale, n, k, x, x_scale, m, out_dtype, y, stream));
 }
 
 // ---------------------------------------------------------------------------

@@ -33,6 +33,7 @@ struct LinearArgs {
 // ---------------------------------------------------------------------------
 constexpr int kUnit = 128;  // contraction codes of a stage: a whole cache line of a row
 constexpr int kXcds = 8;
+constexpr int kNowhere = 0x7FFFFFF0;  // an offset past every tile's range
 
 // 16 neighbouring outputs of one token: (acc sx) sw, each rounded once, the
 // first `left` of them stored.
@@ -70,8 +71,10 @@ __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t src, int8_t* dst,
 // P: parts of the LDS ring. A unit of 128 codes is two parts, the tokens' and
 // the channels'; the ring holds P / 2 units, and with an odd P the tokens' part
 // of one more, so that half of the codes have a unit's time more to arrive.
-template <int BM, int BN, int WM, int WN, int P, int kType>
-__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int tiles_m, int tiles_n) {
+// KS: groups of WM x WN waves that share the contraction of one tile, each with
+// a ring of its own; their sums are added through LDS at the end.
+template <int BM, int BN, int WM, int WN, int KS, int P, int kType>
+__global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave: tokens, channels
   constexpr int LX = BM / 8 / kWaves, LW = BN / 8 / kWaves;  // 1 KB copies of a wave a stage
@@ -81,22 +84,26 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   constexpr int kTurn = kOdd ? P : S;  // units after which parts lie in the same places again
   static_assert(TN % 4 == 0 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
   static_assert(P >= 4 && P <= 8 && (!kOdd || BM == BN), "ring");
+  // groups whose sums fit the channels' part of the ring
+  constexpr int kFit = KS * kUnit / (4 * BM);
+  static_assert(KS == 1 || (kFit >= 1 && (KS - 1 + kFit - 1) / kFit <= P / 2), "sums of the groups");
   typedef typename Elem<kType>::T T;
 
   // one array a part: the compiler can then tell a copy into one part from the
   // reads of another, and waits for none of them by itself
-  __shared__ __attribute__((aligned(1024))) int8_t p0[BM * kUnit];
-  __shared__ __attribute__((aligned(1024))) int8_t p1[BN * kUnit];
-  __shared__ __attribute__((aligned(1024))) int8_t p2[BM * kUnit];
-  __shared__ __attribute__((aligned(1024))) int8_t p3[BN * kUnit];
-  __shared__ __attribute__((aligned(1024))) int8_t p4[P > 4 ? BM * kUnit : 16];
-  __shared__ __attribute__((aligned(1024))) int8_t p5[P > 5 ? BN * kUnit : 16];
-  __shared__ __attribute__((aligned(1024))) int8_t p6[P > 6 ? BM * kUnit : 16];
-  __shared__ __attribute__((aligned(1024))) int8_t p7[P > 7 ? BN * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p0[KS * BM * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p1[KS * BN * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p2[KS * BM * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p3[KS * BN * kUnit];
+  __shared__ __attribute__((aligned(1024))) int8_t p4[P > 4 ? KS * BM * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p5[P > 5 ? KS * BN * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p6[P > 6 ? KS * BM * kUnit : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t p7[P > 7 ? KS * BN * kUnit : 16];
   int8_t* const ring[8] = {p0, p1, p2, p3, p4, p5, p6, p7};
 
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = wave_all / kWaves, wave = wave_all % kWaves;
   const int wm = wave / WN, wn = wave % WN;
 
   // Workgroups go to the XCDs in turn; each XCD takes a run of tiles, ordered
@@ -110,11 +117,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   const int64_t m0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(b0 + in % rows)) * BM;
   const int64_t n0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(in / rows)) * BN;
 
-  const int units = static_cast<int>((g.k + kUnit - 1) / kUnit), whole = static_cast<int>(g.k / kUnit);
+  // This group's units [u0, u0 + turns): the same number for all groups, the
+  // last ones' past the end of the contraction.
+  const int units = static_cast<int>((g.k + kUnit - 1) / kUnit);
+  const int turns = (units + KS - 1) / KS, u0 = group * turns;
   const int mrows = static_cast<int>(g.m - m0 < BM ? g.m - m0 : BM), nrows = static_cast<int>(g.n - n0 < BN ? g.n - n0 : BN);
-  // Ranges of the tile's own rows: the last unit of a contraction that is no
-  // multiple of 128 reads past its rows, into the next row or, past the last
-  // one, into zeros; neither is multiplied.
+  // Ranges of the tile's own rows: what is read at an offset past them is zero.
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.k, mrows * g.k);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + n0 * g.k, nrows * g.k);
 
@@ -124,11 +132,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   // then fall on 16 different 16-byte columns of the banks, both as 16
   // neighbouring lanes and as four quads of lanes out of two columns.
   const int lr = lane >> 3, lc = lane & 7;
-  int xo[LX], wo[LW];
+  int xo[LX], xc[LX], wo[LW];
 #pragma unroll
   for (int l = 0; l < LX; ++l) {
     const int row = 8 * (l * kWaves + wave) + lr;
-    xo[l] = static_cast<int>((row < mrows ? row : mrows - 1) * g.k) + 16 * (lc ^ ((row >> 1) & 7));
+    xc[l] = 16 * (lc ^ ((row >> 1) & 7));
+    xo[l] = static_cast<int>((row < mrows ? row : mrows - 1) * g.k) + xc[l];
   }
 #pragma unroll
   for (int l = 0; l < LW; ++l) {
@@ -136,22 +145,28 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
     wo[l] = static_cast<int>((row < nrows ? row : nrows - 1) * g.k) +
             16 * (lc ^ (2 * ((row >> 4) & 3) + ((row >> 1) & 1)));
   }
+  // Codes behind the contraction's end (in the second half of its last unit,
+  // and in units past it) become zeros on the tokens' side, so their products
+  // vanish whatever the channels' side holds.
   auto copy_x = [&](int8_t* to, int u) {
-    const int q = (u < units ? u : units - 1) * kUnit;
+    const int q = (u0 + u) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LX; ++l) copy_1k(xr, to + (l * kWaves + wave) * 1024, xo[l] + q);
+    for (int l = 0; l < LX; ++l) {
+      const int at = q + xc[l] < static_cast<int>(g.k) ? xo[l] + q : kNowhere;
+      copy_1k(xr, to + (group * BM / 8 + l * kWaves + wave) * 1024, at);
+    }
   };
   auto copy_w = [&](int8_t* to, int u) {
-    const int q = (u < units ? u : units - 1) * kUnit;
+    const int q = (u0 + u < units ? u0 + u : units - 1) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LW; ++l) copy_1k(wr, to + (l * kWaves + wave) * 1024, wo[l] + q);
+    for (int l = 0; l < LW; ++l) copy_1k(wr, to + (group * BN / 8 + l * kWaves + wave) * 1024, wo[l] + q);
   };
   // Fragments of the stage's first or second 64 codes. Token tile t reads rows
   // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,
   // which leaves a lane with runs of 16 neighbouring channels. Both keys are
   // i / 2.
-  const int xa = (wm * TM * 16 + i) * kUnit;
-  const int wa = (wn * TN * 16 + 16 * (i >> 2) + (i & 3)) * kUnit;
+  const int xa = (group * BM + wm * TM * 16 + i) * kUnit;
+  const int wa = (group * BN + wn * TN * 16 + 16 * (i >> 2) + (i & 3)) * kUnit;
   const int place[2] = {16 * (h ^ (i >> 1)), 16 * ((4 + h) ^ (i >> 1))};
   u32x4 fx[2][TM], fw[2][TN];
   auto read = [&](const int8_t* x, const int8_t* w, int half) {
@@ -215,17 +230,44 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   __builtin_amdgcn_s_barrier();
   read(p0, p1, 0);
   int u = 0;
-  for (; u + kTurn <= whole; u += kTurn) {
+  for (; u + kTurn <= turns; u += kTurn) {
 #pragma unroll
     for (int j = 0; j < kTurn; ++j)
       unit(u + j, ring[2 * j % P], ring[(2 * j + 1) % P], ring[(2 * j + 2) % P], ring[(2 * j + 3) % P]);
   }
 #pragma unroll
   for (int j = 0; j < kTurn - 1; ++j)
-    if (u + j < whole)
+    if (u + j < turns)
       unit(u + j, ring[2 * j % P], ring[(2 * j + 1) % P], ring[(2 * j + 2) % P], ring[(2 * j + 3) % P]);
-  if (whole < units) multiply(0);
-  wait_vmcnt<0>();  // no copy may be in flight when the workgroup's LDS is given on
+  wait_vmcnt<0>();  // no copy may be in flight when the ring is used again, here or by the next workgroup
+
+  if (KS > 1) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __syncthreads();  // every group's copies and reads have ended
+    auto sums = [&](int gr) {  // group gr's
+      int8_t* at = ring[1 + 2 * ((gr - 1) / (kFit > 0 ? kFit : 1))] + (gr - 1) % (kFit > 0 ? kFit : 1) * (BM * BN * 4);
+      return reinterpret_cast<i32x4*>(at) + wave * (TM * TN * 64) + lane;
+    };
+#pragma unroll
+    for (int gr = 1; gr < KS; ++gr) {
+      if (group != gr) continue;
+      i32x4* to = sums(gr);
+#pragma unroll
+      for (int a = 0; a < TM; ++a)
+#pragma unroll
+        for (int b = 0; b < TN; ++b) to[(a * TN + b) * 64] = acc[a][b];
+    }
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int gr = 1; gr < KS; ++gr) {
+      const i32x4* from = sums(gr);
+#pragma unroll
+      for (int a = 0; a < TM; ++a)
+#pragma unroll
+        for (int b = 0; b < TN; ++b) acc[a][b] += from[(a * TN + b) * 64];
+    }
+  }
 
   // Lane: tokens 16 a + i, channels 64 (b / 4) + 16 h + 4 (b % 4) + v: runs of
   // 16 neighbouring channels, 64 the four lanes of a token.
@@ -244,178 +286,149 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(LinearArgs g, int ti
   }
 }
 
-template <int BM, int BN, int WM, int WN, int P>
+template <int BM, int BN, int WM, int WN, int KS, int P>
 hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
   const int tiles_m = static_cast<int>((g.m + BM - 1) / BM), tiles_n = static_cast<int>((g.n + BN - 1) / BN);
-  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, P, QLORA_F32>
-              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, P, QLORA_F16>
-                                       : tile_kernel<BM, BN, WM, WN, P, QLORA_BF16>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(64 * WM * WN), 0, s, g, tiles_m, tiles_n);
+  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F32>
+              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F16>
+                                       : tile_kernel<BM, BN, WM, WN, KS, P, QLORA_BF16>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(64 * WM * WN * KS), 0, s, g, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: the weight is streamed once, bound by memory. A workgroup of 16
-// waves takes 16 channels; its waves split the contraction, each reading its
-// runs of the 16 rows straight into registers, all loads in flight at once,
-// and add their integer sums through LDS.
+// At most 16 tokens and few channels: the weight is streamed once, bound by
+// memory. A workgroup takes 16 channels (so 4096 channels fill the 256 CUs);
+// its waves split the contraction, read their runs of the 16 rows straight
+// into registers, and add their integer sums through LDS.
+// One token, 4096 x 4096: 5.8 us (graph replays; 4.3 TB/s behind a launch's
+// 2 us); 4 to 16 waves and 2 to 8 loads in flight measure alike. From 8192
+// channels on the 16 x 64 tiles above fill half the CUs and read the tokens
+// once for 64 channels, not for 16: 16 tokens, 11008 x 4096: 13.8 us here,
+// 11.0 us there; 8192 x 8192: 17.5 and 14.0 us; 4096 x 4096: 7.1 and 7.7 us.
 // ---------------------------------------------------------------------------
+constexpr int kDecodeTokens = 16;
+constexpr int kDecodeMaxN = 8191;
 constexpr int kDecodeWaves = 8;
-constexpr int kDecodeBlocks = 256;
+constexpr int kDecodeSteps = 4;  // 64-code steps of a wave a pass
 
-// J: 64-code steps of a wave a pass; TT: tiles of 16 tokens. kOne: one pass
-// covers the contraction, so the tokens stay in registers while the workgroup
-// goes through its channels, and the next weight rows are on their way while
-// the sums of the last ones are added.
-template <int J, int TT, bool kOne, int kType>
-__global__ __launch_bounds__(64 * kDecodeWaves) void decode_kernel(LinearArgs g, int groups) {
-  __shared__ int part[2][kDecodeWaves][TT * 256];
+template <int kType>
+__global__ __launch_bounds__(64 * kDecodeWaves) void decode_kernel(LinearArgs g) {
+  __shared__ int part[kDecodeWaves][256];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int steps = static_cast<int>(g.k / 64);
-  const int8_t* xp[TT];
+  const int8_t* wp = g.w + (n0 + i < g.n ? n0 + i : g.n - 1) * g.k + 16 * h;
+  const int8_t* xp = g.x + (i < g.m ? i : g.m - 1) * g.k + 16 * h;
+  i32x4 acc = {0, 0, 0, 0};
+  for (int base = 0; base < steps; base += kDecodeWaves * kDecodeSteps) {
+    // this wave's steps of the pass; past the end the last one is read again
+    // and multiplied by zeros
+    const int s0 = base + wave * kDecodeSteps;
+    u32x4 wf[kDecodeSteps], xf[kDecodeSteps];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) xp[t] = g.x + (16 * t + i < g.m ? 16 * t + i : g.m - 1) * g.k + 16 * h;
-  // Step j of this wave in the pass at `base`; past the end the last step is
-  // read again and multiplied by zeros.
-  auto at = [&](int base, int j) {
-    const int s = base + wave * J + j;
-    return 64 * (s < steps ? s : steps - 1);
-  };
-  u32x4 wf[J], xf[TT][J];
-  auto read_w = [&](int group, int base) {
-    const int64_t n = static_cast<int64_t>(group) * 16 + i;
-    const int8_t* wp = g.w + (n < g.n ? n : g.n - 1) * g.k + 16 * h;
-#pragma unroll
-    for (int j = 0; j < J; ++j) wf[j] = ld16(wp + at(base, j));
-  };
-  auto read_x = [&](int base) {
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        xf[t][j] = ld16(xp[t] + at(base, j));
-        if (base + wave * J + j >= steps) xf[t][j] = u32x4{0, 0, 0, 0};
-      }
-  };
-  read_w(blockIdx.x, 0);
-  read_x(0);
-  int turn = 0;
-  for (int group = blockIdx.x; group < groups; group += gridDim.x, turn ^= 1) {
-    i32x4 acc[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-    auto multiply = [&] {
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = mma8(wf[j], xf[t][j], acc[t]);
-    };
-    if (kOne) {
-      multiply();
-      const int next = group + gridDim.x;
-      if (next < groups) read_w(next, 0);
-    } else {
-      for (int base = 0; base < steps; base += kDecodeWaves * J) {
-        if (base > 0 || group != static_cast<int>(blockIdx.x)) {
-          read_w(group, base);
-          read_x(base);
-        }
-        multiply();
-      }
+    for (int j = 0; j < kDecodeSteps; ++j) {
+      const int q = 64 * (s0 + j < steps ? s0 + j : steps - 1);
+      wf[j] = ld16(wp + q);
+      xf[j] = ld16(xp + q);
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) *reinterpret_cast<i32x4*>(&part[turn][wave][t * 256 + 4 * lane]) = acc[t];
-    __syncthreads();  // the other turn's sums have been read by all in front of this
-    // output e: token e / 16, channel e % 16
-    const int64_t n = static_cast<int64_t>(group) * 16 + (tid & 15);
-#pragma unroll
-    for (int e = tid; e < TT * 256; e += 64 * kDecodeWaves) {
-      const int64_t m = e >> 4;
-      if (m >= g.m || n >= g.n) continue;
-      const int from = (e >> 8) * 256 + 4 * (((e >> 4) & 15) + 16 * ((e & 15) >> 2)) + (e & 3);
-      int sum = 0;
-#pragma unroll
-      for (int w = 0; w < kDecodeWaves; ++w) sum += part[turn][w][from];
-      static_cast<typename Elem<kType>::T*>(g.y)[m * g.n + n] =
-          Elem<kType>::put((static_cast<float>(sum) * g.sx[m]) * g.sw[n]);
+    for (int j = 0; j < kDecodeSteps; ++j) {
+      if (s0 + j >= steps) xf[j] = u32x4{0, 0, 0, 0};
+      acc = mma8(wf[j], xf[j], acc);
     }
   }
+  *reinterpret_cast<i32x4*>(&part[wave][4 * lane]) = acc;
+  __syncthreads();
+  // output tid: token tid / 16, channel tid % 16
+  const int tok = tid >> 4, ch = tid & 15;
+  if (tid >= 256 || tok >= g.m || n0 + ch >= g.n) return;
+  const int at = 4 * (tok + 16 * (ch >> 2)) + (ch & 3);
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kDecodeWaves; ++w) sum += part[w][at];
+  static_cast<typename Elem<kType>::T*>(g.y)[tok * g.n + n0 + ch] =
+      Elem<kType>::put((static_cast<float>(sum) * g.sx[tok]) * g.sw[n0 + ch]);
 }
 
-template <int J, int TT, bool kOne>
 hipError_t launch_decode(const LinearArgs& g, int out_dtype, hipStream_t s) {
-  const int groups = static_cast<int>((g.n + 15) / 16);
-  const int blocks = kOne && groups > kDecodeBlocks ? kDecodeBlocks : groups;
-  auto kern = out_dtype == QLORA_F32   ? decode_kernel<J, TT, kOne, QLORA_F32>
-              : out_dtype == QLORA_F16 ? decode_kernel<J, TT, kOne, QLORA_F16>
-                                       : decode_kernel<J, TT, kOne, QLORA_BF16>;
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(64 * kDecodeWaves), 0, s, g, groups);
+  auto kern = out_dtype == QLORA_F32   ? decode_kernel<QLORA_F32>
+              : out_dtype == QLORA_F16 ? decode_kernel<QLORA_F16>
+                                       : decode_kernel<QLORA_BF16>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((g.n + 15) / 16)), dim3(64 * kDecodeWaves), 0, s, g);
   return hipGetLastError();
 }
 
-constexpr int kTM = 64, kTN = 64, kTK = 64;
+bool decodes(int64_t m, int64_t n) { return m <= kDecodeTokens && n <= kDecodeMaxN; }
 
-// 64 tokens x 64 channels a workgroup, one wave 16 channels, straight from the
-// cache; rows past the edges are read from the last row and not stored.
-template <int kType>
-__global__ __launch_bounds__(256) void linear_kernel(LinearArgs g) {
-  typename Elem<kType>::T* y = static_cast<typename Elem<kType>::T*>(g.y);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, h = lane >> 4;
-  const int64_t tiles_n = (g.n + kTN - 1) / kTN;
-  const int64_t m0 = blockIdx.x / tiles_n * kTM, n0 = blockIdx.x % tiles_n * kTN + 16 * wave;
-  const int64_t wr = n0 + i < g.n ? n0 + i : g.n - 1;
-  const int8_t* wp = g.w + wr * g.k + 16 * h;
-  const int8_t* xp[4];
-  i32x4 acc[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int64_t xr = m0 + 16 * t + i < g.m ? m0 + 16 * t + i : g.m - 1;
-    xp[t] = g.x + xr * g.k + 16 * h;
-    acc[t] = i32x4{0, 0, 0, 0};
-  }
-  for (int64_t q = 0; q < g.k; q += kTK) {
-    const u32x4 a = ld16(wp + q);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[t] = mma8(a, ld16(xp[t] + q), acc[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int64_t m = m0 + 16 * t + i;
-    if (m >= g.m) continue;
-    const float s = g.sx[m];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t n = n0 + 4 * h + v;
-      if (n < g.n) y[m * g.n + n] = Elem<kType>::put((static_cast<float>(acc[t][v]) * s) * g.sw[n]);
+// ---------------------------------------------------------------------------
+// The tile for a call: the one with the least fixed + rounds * units * unit
+// microseconds, where rounds counts turns of the 256 CUs and units steps of 128
+// codes. Fitted to measured times (graph replays, bf16 out); it names the
+// fastest tile, or one within 10% of it, at (m x n x k, us):
+//   4096 x 22016 x 8192: 256 x 256 575, 128 x 256 634, 128 x 128 724
+//   4096 x 8192 x 8192:  256 x 256 206, 128 x 256 238
+//   2048 x 4096 x 11008: 128 x 256 76, 128 x 128 92, 256 x 256 102
+//   2048 x 11008 x 4096: 128 x 256 90, 256 x 256 104, 128 x 128 119
+//   512 x 4096 x 4096:   64 x 128 14.8, 64 x 64 17.6, 128 x 128 19.0
+//   200 x 11008 x 4096:  64 x 128 24.4, 64 x 64 25.4, 128 x 256 about 25
+//   333 x 5003 x 4160:   64 x 128 18.6, 64 x 64 21.3, 128 x 128 21.9
+//   128 x 4096 x 4096:   32 x 64 8.6, 64 x 64 10.8, 64 x 128 12.5
+//   64 x 11008 x 4096:   64 x 64 11.3, 64 x 128 13.5, 32 x 64 15.9
+//   32 x 4096 x 11008:   16 x 64 14.4, 32 x 64 17.1
+// ---------------------------------------------------------------------------
+struct Shape {
+  int bm, bn, threads;
+  double fixed, unit;
+};
+constexpr Shape kShapes[] = {{256, 256, 512, 8, 1.5},   {128, 256, 512, 5, 0.9},   {128, 128, 256, 4, 0.53},
+                             {64, 128, 256, 4, 0.34},   {64, 64, 256, 3.5, 0.22},  {32, 64, 256, 3.5, 0.16},
+                             {16, 64, 128, 3.5, 0.125}};
+constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
+
+// Index into kShapes, or -1: no tile's grid stays below 2^32 work items.
+int pick_shape(int64_t m, int64_t n, int64_t k) {
+  int best = -1;
+  double best_us = 0;
+  for (int i = 0; i < kNumShapes; ++i) {
+    const Shape& s = kShapes[i];
+    const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn);
+    if (tiles >= (INT64_C(1) << 32) / s.threads) continue;
+    const double us = s.fixed + static_cast<double>((tiles + 255) / 256) * static_cast<double>((k + 127) / 128) * s.unit;
+    if (best < 0 || us < best_us) {
+      best = i;
+      best_us = us;
     }
   }
+  return best;
 }
 
 }  // namespace
 
-size_t int8_linear_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+bool int8_linear_fits(int64_t m, int64_t n, int64_t k) { return decodes(m, n) || pick_shape(m, n, k) >= 0; }
 
 hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
-                              const float* x_scale, int64_t m, int out_dtype, void* y, void*, hipStream_t s) {
+                              const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s) {
   const LinearArgs g{w, w_scale, x, x_scale, y, m, n, k};
-  if (m <= 16) {
-    if (k <= 2048) return launch_decode<4, 1, true>(g, out_dtype, s);
-    if (k <= 4096) return launch_decode<8, 1, true>(g, out_dtype, s);
-    return launch_decode<4, 1, false>(g, out_dtype, s);
+  if (decodes(m, n)) return launch_decode(g, out_dtype, s);
+  switch (pick_shape(m, n, k)) {
+    case 0:
+      return launch_tiles<256, 256, 2, 4, 1, 5>(g, out_dtype, s);
+    case 1:
+      return launch_tiles<128, 256, 2, 4, 1, 6>(g, out_dtype, s);
+    case 2:
+      return launch_tiles<128, 128, 2, 2, 1, 8>(g, out_dtype, s);
+    case 3:
+      return launch_tiles<64, 128, 2, 2, 1, 8>(g, out_dtype, s);
+    case 4:
+      return launch_tiles<64, 64, 4, 1, 1, 8>(g, out_dtype, s);
+    case 5:
+      return launch_tiles<32, 64, 2, 1, 2, 8>(g, out_dtype, s);
+    case 6:
+      return launch_tiles<16, 64, 1, 1, 2, 8>(g, out_dtype, s);
   }
-  if (m <= 32) {
-    if (k <= 2048) return launch_decode<4, 2, true>(g, out_dtype, s);
-    if (k <= 4096) return launch_decode<8, 2, true>(g, out_dtype, s);
-    return launch_decode<4, 2, false>(g, out_dtype, s);
-  }
-  if (m > 32) return launch_tiles<256, 256, 2, 4, 5>(g, out_dtype, s);
-  const int64_t tiles = ((m + kTM - 1) / kTM) * ((n + kTN - 1) / kTN);
-  auto kern = out_dtype == QLORA_F32   ? linear_kernel<QLORA_F32>
-              : out_dtype == QLORA_F16 ? linear_kernel<QLORA_F16>
-                                       : linear_kernel<QLORA_BF16>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, g);
-  return hipGetLastError();
+  return hipErrorInvalidValue;  // int8_linear_fits refuses these sizes
 }
 
 }  // namespace qlora

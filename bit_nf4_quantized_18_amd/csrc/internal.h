@@ -203,10 +203,10 @@ hipError_t launch_rmsnorm_int8(const void* x, const void* residual, const void* 
                                int64_t rows, int64_t cols, float eps, void* residual_out, int8_t* codes, int64_t ld,
                                float* scale, hipStream_t s);
 
-// The 8-bit product; ws holds int8_linear_ws_bytes(m, n, k) bytes.
-size_t int8_linear_ws_bytes(int64_t m, int64_t n, int64_t k);
+// The 8-bit product, for sizes whose launch stays below 2^32 work items.
+bool int8_linear_fits(int64_t m, int64_t n, int64_t k);
 hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
-                              const float* x_scale, int64_t m, int out_dtype, void* y, void* ws, hipStream_t s);
+                              const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s);
 
 // Global norm of a list of tensors and (clip) their scaling: out null writes
 // in place. total is the sum of numel; ws holds grad_ws_bytes(numel, count).

@@ -464,18 +464,13 @@ qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void*
  *   w, w_scale : 8-bit rows of the weight (n x k, one scale a channel).
  *   x, x_scale : 8-bit rows of the input (m x k, one scale a token). k is the
  *                row length ld of both: k % 64 == 0, 64 .. QLORA_INT8_MAX_K.
- *   n          : 1 .. 2^22, n k <= 2^40; m 0 .. 2^31 - 1 (0: nothing is done).
+ *   n          : 1 .. 2^22; m 0 .. 2^31 - 1 (0: nothing is done);
+ *                ceil(m / 256) ceil(n / 256) < 2^23.
  *   out_dtype  : QLORA_BF16, QLORA_F16 or QLORA_F32; y is m x n.
- *   ws         : qlora_int8_linear_workspace_bytes(m, n, k) bytes (may be NULL
- *                when that is 0). Calls that may overlap need one each.
- * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (out_dtype) / WORKSPACE / HIP. */
+ * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (out_dtype) / HIP. */
 qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_t n, int64_t k,
                                    const int8_t* x, const float* x_scale, int64_t m, int out_dtype,
-                                   void* y, void* ws, size_t ws_bytes, hipStream_t stream);
-
-/* Workspace bytes for qlora_int8_linear_fwd; 0 for invalid sizes and where the
- * call needs none. Host only, no GPU use. */
-size_t qlora_int8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
+                                   void* y, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The global norm of a training step's adapter gradients (the dA and dB of

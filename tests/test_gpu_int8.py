@@ -6,8 +6,6 @@ formed in the same order), scales and values are single float32 roundings, and
 the product's sums are exact integers. The norm's scale takes a 64-bit sum
 whose order differs from the oracle's: relative difference at most about
 cols 2^-53, so the two float32 roundings differ by at most one step, 2^-23."""
-import ctypes
-
 import numpy as np
 import pytest
 
@@ -390,24 +388,3 @@ def test_other_stream(gpu_lib):
     s.synchronize()
     _same(y.cpu().numpy(), OI.linear(w, sw, x, sx))
 
-
-def test_abi_reports_short_workspace(gpu_lib):
-    """Sizes whose product is split along k refuse a missing or short workspace."""
-    import torch
-
-    lib = gpu_lib.load()
-    for m, n, k in ((40, 64, 4096), (300, 256, 11008), (17, 16, 131008)):
-        need = gpu_lib.int8_workspace_bytes(m, n, k)
-        if not need:
-            continue
-        w, sw, x, sx = _operands(m, n, k, 1)
-        qw, qx = _packed(gpu_lib, w, sw, k), _packed(gpu_lib, x, sx, k)
-        y = torch.zeros((m, n), device="cuda")
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-        args = (qw.codes.data_ptr(), qw.scale.data_ptr(), n, k, qx.codes.data_ptr(), qx.scale.data_ptr(), m, 1,
-                y.data_ptr())
-        stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        assert lib.qlora_int8_linear_fwd(*args, None, need, stream) == -5
-        assert lib.qlora_int8_linear_fwd(*args, ws.data_ptr(), need - 1, stream) == -5
-        torch.cuda.synchronize()
-        assert not y.any()

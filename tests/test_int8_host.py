@@ -47,8 +47,8 @@ def test_rmsnorm_argument_errors():
 def test_linear_argument_errors():
     lib = B.load()
 
-    def f(w=P, sw=P, n=64, k=128, x=P, sx=P, m=4, t=BF16, y=P, ws=None, nbytes=0):
-        return lib.qlora_int8_linear_fwd(w, sw, n, k, x, sx, m, t, y, ws, nbytes, None)
+    def f(w=P, sw=P, n=64, k=128, x=P, sx=P, m=4, t=BF16, y=P):
+        return lib.qlora_int8_linear_fwd(w, sw, n, k, x, sx, m, t, y, None)
 
     assert f(t=9) == -4
     for name in ("w", "sw", "x", "sx", "y"):
@@ -57,7 +57,7 @@ def test_linear_argument_errors():
     assert f(n=0) == -2 and f(k=0) == -2 and f(k=100) == -2 and f(m=-1) == -2 and f(m=1 << 31) == -2
     assert f(k=131072) == -2 and f(n=(1 << 22) + 1) == -2  # 131072 128^2 = 2^31: the sum could wrap
     assert f(m=0, x=None, sx=None, y=None) == 0
-    assert B.int8_workspace_bytes(0, 64, 128) == 0 and B.int8_workspace_bytes(4, 0, 128) == 0
+    assert f(n=1 << 22, m=(1 << 31) - 1) == -2  # more tiles than a launch takes
 
 
 def _grads(sizes, at=None):
@@ -142,8 +142,6 @@ def test_binding_rejects_packed_int8():
         B.int8_linear_fwd(_int8(), _int8(ld=192))
     with pytest.raises(ValueError, match="out has shape"):
         B.int8_linear_fwd(_int8(), _int8(3), out=torch.zeros(8, 3, dtype=torch.bfloat16))
-    with pytest.raises(ValueError, match="ws must be"):
-        B.int8_linear_fwd(_int8(), _int8(3), ws=torch.zeros(8))
     with pytest.raises(TypeError, match="dtype must be"):
         B.int8_linear_fwd(_int8(), _int8(3), torch.float64)
 
