@@ -33,7 +33,7 @@ struct LinearArgs {
 // ---------------------------------------------------------------------------
 constexpr int kUnit = 128;  // contraction codes of a stage: a whole cache line of a row
 constexpr int kXcds = 8;
-constexpr int kNowhere = 0x7FFFFFF0;  // an offset past every tile's range
+constexpr int kNowhere = 0x70000000;  // an offset past every tile's range, also with one of a tile added
 
 // 16 neighbouring outputs of one token: (acc sx) sw, each rounded once, the
 // first `left` of them stored.
@@ -131,20 +131,16 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   // stands at place c ^ key(row). The 16 lanes that read one chunk column
   // then fall on 16 different 16-byte columns of the banks, both as 16
   // neighbouring lanes and as four quads of lanes out of two columns.
+  // Rows past the tile's last lie past its range.
   const int lr = lane >> 3, lc = lane & 7;
-  int xo[LX], xc[LX], wo[LW];
+  const int k32 = static_cast<int>(g.k);
+  int xc[LX], wo[LW];  // byte in the row's unit; offset without rows of blocks
 #pragma unroll
-  for (int l = 0; l < LX; ++l) {
-    const int row = 8 * (l * kWaves + wave) + lr;
-    xc[l] = 16 * (lc ^ ((row >> 1) & 7));
-    xo[l] = static_cast<int>((row < mrows ? row : mrows - 1) * g.k) + xc[l];
-  }
+  for (int l = 0; l < LX; ++l) xc[l] = 16 * (lc ^ ((lr >> 1) + 4 * ((l * kWaves + wave) & 1)));
 #pragma unroll
-  for (int l = 0; l < LW; ++l) {
-    const int row = 8 * (l * kWaves + wave) + lr;
-    wo[l] = static_cast<int>((row < nrows ? row : nrows - 1) * g.k) +
-            16 * (lc ^ (2 * ((row >> 4) & 3) + ((row >> 1) & 1)));
-  }
+  for (int l = 0; l < LW; ++l)
+    wo[l] = (8 * wave + lr) * k32 + 16 * (lc ^ (2 * (((l * kWaves + wave) >> 1) & 3) + ((lr >> 1) & 1)));
+  const int xrow = (8 * wave + lr) * k32;
   // Codes behind the contraction's end (in the second half of its last unit,
   // and in units past it) become zeros on the tokens' side, so their products
   // vanish whatever the channels' side holds.
@@ -152,14 +148,15 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
     const int q = (u0 + u) * kUnit;
 #pragma unroll
     for (int l = 0; l < LX; ++l) {
-      const int at = q + xc[l] < static_cast<int>(g.k) ? xo[l] + q : kNowhere;
-      copy_1k(xr, to + (group * BM / 8 + l * kWaves + wave) * 1024, at);
+      const int at = xc[l] < k32 - q ? xrow + xc[l] : kNowhere;
+      copy_1k(xr, to + (group * BM / 8 + l * kWaves + wave) * 1024, at + (8 * l * kWaves * k32 + q));
     }
   };
   auto copy_w = [&](int8_t* to, int u) {
     const int q = (u0 + u < units ? u0 + u : units - 1) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LW; ++l) copy_1k(wr, to + (group * BN / 8 + l * kWaves + wave) * 1024, wo[l] + q);
+    for (int l = 0; l < LW; ++l)
+      copy_1k(wr, to + (group * BN / 8 + l * kWaves + wave) * 1024, wo[l] + (8 * l * kWaves * k32 + q));
   };
   // Fragments of the stage's first or second 64 codes. Token tile t reads rows
   // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,
