@@ -43,6 +43,26 @@ struct __attribute__((packed, aligned(2))) Any16 {
 __device__ __forceinline__ u32x4 ld16_any(const void* p) { return static_cast<const Any16*>(p)->v; }
 __device__ __forceinline__ void st16_any(void* p, u32x4 v) { static_cast<Any16*>(p)->v = v; }
 
+// Eight elements at any element's address, as float32 and back.
+template <int kType>
+__device__ __forceinline__ void get8(const typename Elem<kType>::T* p, float* f) {
+  if constexpr (kType == QLORA_F32) {
+    const u32x4 a = ld16_any(p), b = ld16_any(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = __uint_as_float(a[e]);
+      f[4 + e] = __uint_as_float(b[e]);
+    }
+  } else {
+    const u32x4 a = ld16_any(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = lo16<kType == QLORA_F16>(a[e]);
+      f[2 * e + 1] = hi16<kType == QLORA_F16>(a[e]);
+    }
+  }
+}
+
 // Four float32 as elements, in the words [0, sizeof(T)) of a store.
 template <int kType>
 __device__ __forceinline__ void put4(uint32_t* w, const float* f) {
@@ -54,6 +74,19 @@ __device__ __forceinline__ void put4(uint32_t* w, const float* f) {
     w[0] = E::put(f[0]) | static_cast<uint32_t>(E::put(f[1])) << 16;
     w[1] = E::put(f[2]) | static_cast<uint32_t>(E::put(f[3])) << 16;
   }
+}
+
+template <int kType>
+__device__ __forceinline__ void put8(typename Elem<kType>::T* p, const float* f) {
+  constexpr int kWords = 2 * sizeof(typename Elem<kType>::T);
+  union {
+    uint32_t w[kWords];
+    u32x4 v[kWords / 4];
+  } out;
+  put4<kType>(out.w, f);
+  put4<kType>(out.w + kWords / 2, f + 4);
+#pragma unroll
+  for (int j = 0; j < kWords / 4; ++j) st16_any(reinterpret_cast<u32x4*>(p) + j, out.v[j]);
 }
 
 }  // namespace qlora

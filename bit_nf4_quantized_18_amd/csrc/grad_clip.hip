@@ -19,7 +19,12 @@ namespace {
 
 constexpr int kTensors = 180;
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 1024;  // workgroups of a launch
+constexpr int kRun = 8;                         // elements of a thread at a time
+constexpr int kTurns = 4;                       // runs of a thread in a chunk, at most
+constexpr int kSmallChunk = kThreads * kRun;    // 2048
+constexpr int kChunk = kSmallChunk * kTurns;    // 8192
+constexpr int kSumBlocks = 512;                 // workgroups of a first launch, at most
+constexpr int kScaleBlocks = 1024;              // of the second
 
 struct Slice {
   const void* at[kTensors];
@@ -47,33 +52,64 @@ __device__ __forceinline__ double reduce_sum(double v) {
   return v;
 }
 
+// A thread's runs of a chunk: run i starts at element kRun (thread + i
+// kThreads); what lies behind the chunk's end is zero.
+template <int kType>
+__device__ __forceinline__ void load_chunk(const typename Elem<kType>::T* p, int64_t len, float (*v)[kRun]) {
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int64_t j = kRun * (threadIdx.x + i * kThreads);
+    if (j + kRun <= len) {
+      get8<kType>(p + j, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) v[i][e] = j + e < len ? Elem<kType>::get(p[j + e]) : 0.0f;
+    }
+  }
+}
+
 template <int kType>
 __global__ __launch_bounds__(kThreads) void square_sum_kernel(Slice l, int tensors, int chunk0, int chunk1,
-                                                              int64_t chunk, double* partial, Record* records) {
-  typedef Elem<kType> G;
+                                                              int chunk, double* partial, Record* records) {
+  typedef typename Elem<kType>::T T;
+  const int lane = threadIdx.x & 63;
   double sum = 0.0;
   for (int c = chunk0 + blockIdx.x; c < chunk1; c += gridDim.x) {
-    int t = 0;  // the last tensor that starts at or in front of chunk c
-    for (int i = 1; i < tensors; ++i) t = l.first[i] <= c ? i : t;
-    const int64_t begin = (c - l.first[t]) * chunk, size = l.off[t + 1] - l.off[t];
+    // the last tensor that starts at or in front of chunk c: the starts ascend
+    int t = -1;
+#pragma unroll
+    for (int j = 0; j < kTensors; j += 64)
+      t += __popcll(__ballot(j + lane < tensors && l.first[j + lane < kTensors ? j + lane : 0] <= c));
+    t = __builtin_amdgcn_readfirstlane(t);
+    const int64_t begin = static_cast<int64_t>(c - l.first[t]) * chunk, size = l.off[t + 1] - l.off[t];
     const int64_t len = size - begin < chunk ? size - begin : chunk;
-    const typename G::T* p = static_cast<const typename G::T*>(l.at[t]) + begin;
+    const T* p = static_cast<const T*>(l.at[t]) + begin;
     if (records != nullptr && threadIdx.x == 0) records[c] = Record{p, l.off[t] + begin, len};
-    for (int64_t j = threadIdx.x; j < len; j += kThreads) {
-      const double v = static_cast<double>(G::get(p[j]));
-      sum += v * v;
-    }
+    float v[kTurns][kRun];
+    load_chunk<kType>(p, len, v);
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) sum += static_cast<double>(v[i][e]) * static_cast<double>(v[i][e]);
   }
   sum = reduce_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// clip = false: only the norm (one workgroup). out null: in place.
+// clip = false: only the norm (one workgroup). out null: in place. The first
+// chunk is on its way while the partial sums are added.
 template <int kType>
 __global__ __launch_bounds__(kThreads) void scale_kernel(const double* partial, int partials, const Record* records,
                                                          int chunks, bool clip, float max_norm, void* out,
                                                          float* norm_out) {
-  typedef Elem<kType> G;
+  typedef typename Elem<kType>::T T;
+  int c = blockIdx.x;
+  Record r{};
+  float v[kTurns][kRun];
+  if (clip && c < chunks) {
+    r = records[c];
+    load_chunk<kType>(static_cast<const T*>(r.at), r.len, v);
+  }
   double sum = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
   const double norm = sqrt(reduce_sum(sum));
@@ -83,29 +119,42 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(const double* partial, 
   const double ratio = static_cast<double>(max_norm) / (norm + 1e-6);
   if (!(ratio >= 1.0) && !__builtin_isinf(max_norm)) f = static_cast<float>(ratio);  // a NaN norm: NaN
   if (out == nullptr && f == 1.0f) return;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Record r = records[c];
-    const typename G::T* p = static_cast<const typename G::T*>(r.at);
-    typename G::T* o = out == nullptr ? const_cast<typename G::T*>(p) : static_cast<typename G::T*>(out) + r.off;
-    for (int64_t j = threadIdx.x; j < r.len; j += kThreads) o[j] = G::put(G::get(p[j]) * f);
+  while (c < chunks) {
+    T* o = out == nullptr ? static_cast<T*>(const_cast<void*>(r.at)) : static_cast<T*>(out) + r.off;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int64_t j = kRun * (threadIdx.x + i * kThreads);
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) v[i][e] *= f;
+      if (j + kRun <= r.len) {
+        put8<kType>(o + j, v[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+          if (j + e < r.len) o[j + e] = Elem<kType>::put(v[i][e]);
+      }
+    }
+    c += gridDim.x;
+    if (c >= chunks) return;
+    r = records[c];
+    load_chunk<kType>(static_cast<const T*>(r.at), r.len, v);
   }
 }
 
 // Chunk length and what follows from it.
 struct Plan {
-  int64_t chunk;
+  int chunk;
   int chunks;    // of all tensors
   int partials;  // workgroups of all first launches
 };
 
-int64_t chunks_of(int64_t numel, int64_t chunk) { return (numel + chunk - 1) / chunk; }
+int64_t chunks_of(int64_t numel, int chunk) { return (numel + chunk - 1) / chunk; }
 
 Plan plan_for(const int64_t* numel, int count) {
   int64_t total = 0;
   for (int i = 0; i < count; ++i) total += numel[i];
   Plan p{};
-  p.chunk = 16384;
-  while (total / p.chunk > (1 << 20)) p.chunk *= 2;  // chunks are numbered in 32 bits
+  p.chunk = total < kChunk * 512 ? kSmallChunk : kChunk;  // short lists: chunks for every CU
   int64_t chunks = 0, in_slice = 0;
   int tensors = 0;
   for (int i = 0; i < count; ++i) {
@@ -114,12 +163,12 @@ Plan plan_for(const int64_t* numel, int count) {
     chunks += c;
     in_slice += c;
     if (++tensors == kTensors) {
-      p.partials += static_cast<int>(in_slice < kMaxBlocks ? in_slice : kMaxBlocks);
+      p.partials += static_cast<int>(in_slice < kSumBlocks ? in_slice : kSumBlocks);
       tensors = 0;
       in_slice = 0;
     }
   }
-  if (tensors > 0) p.partials += static_cast<int>(in_slice < kMaxBlocks ? in_slice : kMaxBlocks);
+  if (tensors > 0) p.partials += static_cast<int>(in_slice < kSumBlocks ? in_slice : kSumBlocks);
   p.chunks = static_cast<int>(chunks);
   return p;
 }
@@ -145,7 +194,7 @@ hipError_t launch_t(const void* const* grads, const int64_t* numel, int count, b
       l.off[++tensors] = off;
     }
     if (tensors == kTensors || (i == count && tensors > 0)) {
-      const int blocks = chunk1 - chunk0 < kMaxBlocks ? chunk1 - chunk0 : kMaxBlocks;
+      const int blocks = chunk1 - chunk0 < kSumBlocks ? chunk1 - chunk0 : kSumBlocks;
       hipLaunchKernelGGL((square_sum_kernel<kType>), dim3(blocks), dim3(kThreads), 0, s, l, tensors, chunk0, chunk1,
                          p.chunk, partial + partials, clip ? records : nullptr);
       const hipError_t e = hipGetLastError();
@@ -155,7 +204,7 @@ hipError_t launch_t(const void* const* grads, const int64_t* numel, int count, b
       tensors = 0;
     }
   }
-  int blocks = clip ? (p.chunks < 2 * kMaxBlocks ? p.chunks : 2 * kMaxBlocks) : 1;
+  int blocks = clip ? (p.chunks < kScaleBlocks ? p.chunks : kScaleBlocks) : 1;
   if (blocks < 1) blocks = 1;
   hipLaunchKernelGGL((scale_kernel<kType>), dim3(blocks), dim3(kThreads), 0, s, partial, partials, records, p.chunks,
                      clip, max_norm, out, norm);

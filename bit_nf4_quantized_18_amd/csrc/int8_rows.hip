@@ -18,32 +18,59 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // integer maximum carries a NaN through.
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// The code of v in a row of largest magnitude a > 0, inv = fl32(127 / a).
+// The code of v in a row of largest magnitude a > 0, inv = fl32(127 / a):
 // t = v inv is within 127 2^-23 < 2^-15 of 127 v / a, so it rounds as that does
-// unless it lies nearer than 2^-14 to a tie; the quotient in 64 bits decides
-// there (127 v is exact, and a quotient that is no tie differs from one by at
-// least 2^-26, far over the division's rounding). Rows so small that 127 / a
-// leaves the normal range take the quotient everywhere.
-__device__ __forceinline__ int encode(float v, float a, float inv) {
-  const float t = v * inv;
-  float c = rintf(t);
-  if (fabsf(fabsf(t - c) - 0.5f) < 0x1p-14f || !(inv < 0x1p100f))
-    c = static_cast<float>(rint(static_cast<double>(v) * 127.0 / static_cast<double>(a)));
-  return static_cast<int>(c);
+// unless it lies nearer than 2^-14 to a tie. Rows so small that 127 / a leaves
+// the normal range are near one everywhere.
+__device__ __forceinline__ float near_code(float v, float inv, bool& close) {
+  const float t = v * inv, c = rintf(t);
+  close |= !(fabsf(t - c) < 0.5f - 0x1p-14f);
+  return c;
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int mask) { return __shfl_xor(v, mask, 64); }
+// The same where t is close to a tie: the quotient in 64 bits. 127 v is exact,
+// and a quotient that is no tie differs from one by 2^-26 at least, far over
+// the division's rounding.
+__device__ __forceinline__ float exact_code(float v, float a) {
+  return static_cast<float>(rint(static_cast<double>(v) * 127.0 / static_cast<double>(a)));
+}
 
-// Maximum and sum over the workgroup, in every thread, in a fixed order.
-__device__ __forceinline__ void reduce_row(uint32_t& top, double& sum) {
-  __shared__ uint32_t tops[16];
-  __shared__ double sums[16];
+// Codes of eight values, packed.
+__device__ __forceinline__ u32x2 encode8(const float* v, float a, float inv) {
+  float c[8];
+  bool close = !(inv < 0x1p100f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c[e] = near_code(v[e], inv, close);
+  if (close) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = exact_code(v[e], a);
+  }
+  u32x2 out;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b |= (static_cast<uint32_t>(static_cast<int>(c[4 * w + e])) & 0xFFu) << (8 * e);
+    out[w] = b;
+  }
+  return out;
+}
+
+// Maximum and sum over a wave, in every lane.
+__device__ __forceinline__ void reduce_wave(uint32_t& top, double& sum) {
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) {
     const uint32_t o = __shfl_xor(top, s, 64);
     top = o > top ? o : top;
-    sum += shfl_xor_f64(sum, s);
+    sum += __shfl_xor(sum, s, 64);
   }
+}
+
+// Maximum and sum over the workgroup, in every thread, in a fixed order.
+__device__ __forceinline__ void reduce_block(uint32_t& top, double& sum) {
+  __shared__ uint32_t tops[16];
+  __shared__ double sums[16];
+  reduce_wave(top, sum);
   const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   __syncthreads();  // the last row's values have been read
   if ((threadIdx.x & 63) == 0) {
@@ -70,116 +97,224 @@ struct RowArgs {
   float* scale;
 };
 
-// One workgroup a row at a time; the row is read twice, the second time from
-// the cache. Every element is read and written by one thread in both passes,
-// so residual_out may be one of the inputs.
-template <int kType, bool kNorm, bool kGainF32>
-__global__ __launch_bounds__(256) void rows_kernel(RowArgs g) {
-  typedef Elem<kType> E;
-  typedef typename E::T T;
-  const T* gain16 = static_cast<const T*>(g.gain);
-  const float* gain32 = static_cast<const float*>(g.gain);
-  for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(g.x) + row * g.cols;
-    const T* res = g.residual != nullptr ? static_cast<const T*>(g.residual) + row * g.cols : nullptr;
-    T* out = g.residual != nullptr ? static_cast<T*>(g.residual_out) + row * g.cols : nullptr;
+// What a row's statistics decide.
+struct RowScale {
+  float a, inv, scale;
+  bool live;  // it has codes other than zero
+};
+template <bool kNorm>
+__device__ __forceinline__ RowScale row_scale(uint32_t top, double sum, const RowArgs& g) {
+  // a row with a NaN or an infinity: the sum is not finite where h is not
+  const bool bad = top >= kInfBits || !(sum < __longlong_as_double(0x7FF0000000000000LL));
+  RowScale r;
+  r.a = __uint_as_float(top);
+  r.inv = 127.0f / r.a;
+  double s = static_cast<double>(r.a) / 127.0;
+  if (kNorm) s = s / sqrt(sum / static_cast<double>(g.cols) + static_cast<double>(g.eps));
+  r.scale = bad ? __uint_as_float(0x7FC00000u) : (top == 0 ? 0.0f : static_cast<float>(s));
+  r.live = !bad && top != 0;
+  return r;
+}
+
+// Eight values of a row from column j on, zeros at and behind `cols`.
+template <int kType>
+__device__ __forceinline__ void load8(const typename Elem<kType>::T* row, int64_t j, int64_t cols, float* f) {
+  if (j + 8 <= cols) {
+    get8<kType>(row + j, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = j + e < cols ? Elem<kType>::get(row[j + e]) : 0.0f;
+  }
+}
+
+// v = x, or (norm) h gain with h = x + residual, for eight columns; h is stored
+// if `out` is given. Adds to the row's statistics.
+template <int kType, bool kNorm, bool kRes, bool kGainF32>
+__device__ __forceinline__ void row8(const RowArgs& g, int64_t row, int64_t j, bool store, float* v, uint32_t& top,
+                                     double& sum) {
+  typedef typename Elem<kType>::T T;
+  const int64_t at = row * g.cols;
+  load8<kType>(static_cast<const T*>(g.x) + at, j, g.cols, v);
+  if (kNorm) {
+    float w[8];
+    if (kRes) {
+      load8<kType>(static_cast<const T*>(g.residual) + at, j, g.cols, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += w[e];
+      if (store) {
+        T* out = static_cast<T*>(g.residual_out) + at;
+        if (j + 8 <= g.cols) {
+          put8<kType>(out + j, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (j + e < g.cols) out[j + e] = Elem<kType>::put(v[e]);
+        }
+      }
+    }
+    if (kGainF32) {
+      load8<QLORA_F32>(static_cast<const float*>(g.gain), j, g.cols, w);
+    } else {
+      load8<kType>(static_cast<const T*>(g.gain), j, g.cols, w);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sum += static_cast<double>(v[e]) * static_cast<double>(v[e]);
+      v[e] *= w[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = mag_bits(v[e]);
+    top = b > top ? b : top;
+  }
+}
+
+// A row in registers: thread t of the row's T threads holds columns 8 (t + i T)
+// .. + 7 for i < N, read once and written once. kWave: the row's threads are a
+// wave (4 rows a workgroup, no barrier), otherwise a workgroup.
+template <int kType, bool kNorm, bool kRes, bool kGainF32, int N, bool kWave>
+__global__ __launch_bounds__(kWave ? 256 : 1024) void rows_kernel(RowArgs g) {
+  const int threads = kWave ? 64 : blockDim.x, t = kWave ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t rows_at_once = kWave ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
+  const int64_t first = kWave ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  for (int64_t row = first; row < g.rows; row += rows_at_once) {
+    float v[N][8];
     uint32_t top = 0;
     double sum = 0.0;
-    for (int64_t j = threadIdx.x; j < g.cols; j += blockDim.x) {
-      float v = E::get(x[j]);
-      if (kNorm) {
-        if (res != nullptr) v += E::get(res[j]);
-        sum += static_cast<double>(v) * static_cast<double>(v);
-        v *= kGainF32 ? gain32[j] : E::get(gain16[j]);
-      }
-      const uint32_t b = mag_bits(v);
-      top = b > top ? b : top;
-    }
-    reduce_row(top, sum);
-    // a row with a NaN or an infinity: sum is not finite where h is not
-    const bool bad = top >= kInfBits || !(sum < __longlong_as_double(0x7FF0000000000000LL));
-    const float a = __uint_as_float(top);
-    const float inv = 127.0f / a;
-    if (threadIdx.x == 0) {
-      double s = static_cast<double>(a) / 127.0;
-      if (kNorm) s = s / sqrt(sum / static_cast<double>(g.cols) + static_cast<double>(g.eps));
-      g.scale[row] = bad ? __uint_as_float(0x7FC00000u) : (top == 0 ? 0.0f : static_cast<float>(s));
-    }
-    const bool live = !bad && top != 0;
-    int8_t* codes = g.codes + row * g.ld;
-    for (int64_t j = threadIdx.x; j < g.ld; j += blockDim.x) {
-      int code = 0;
-      if (j < g.cols) {
-        float v = E::get(x[j]);
-        if (kNorm) {
-          if (res != nullptr) {
-            v += E::get(res[j]);
-            out[j] = E::put(v);
-          }
-          v *= kGainF32 ? gain32[j] : E::get(gain16[j]);
-        }
-        if (live) code = encode(v, a, inv);
-      }
-      codes[j] = static_cast<int8_t>(code);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      row8<kType, kNorm, kRes, kGainF32>(g, row, 8 * (t + i * threads), true, v[i], top, sum);
+    if (kWave) reduce_wave(top, sum);
+    else reduce_block(top, sum);
+    const RowScale r = row_scale<kNorm>(top, sum, g);
+    if (t == 0) g.scale[row] = r.scale;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t j = 8 * (t + i * threads);
+      if (j < g.ld)
+        *reinterpret_cast<u32x2*>(g.codes + row * g.ld + j) = r.live ? encode8(v[i], r.a, r.inv) : u32x2{0, 0};
     }
   }
 }
 
+// Rows too long for the registers are read twice. Every element is read and
+// written by one thread in both passes and h is stored in the second, so
+// residual_out may be one of the inputs.
+template <int kType, bool kNorm, bool kRes, bool kGainF32>
+__global__ __launch_bounds__(1024) void long_rows_kernel(RowArgs g) {
+  for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+    uint32_t top = 0, unused_top = 0;
+    double sum = 0.0, unused_sum = 0.0;
+    float v[8];
+    for (int64_t j = 8 * threadIdx.x; j < g.cols; j += 8 * blockDim.x)
+      row8<kType, kNorm, kRes, kGainF32>(g, row, j, false, v, top, sum);
+    reduce_block(top, sum);
+    const RowScale r = row_scale<kNorm>(top, sum, g);
+    if (threadIdx.x == 0) g.scale[row] = r.scale;
+    for (int64_t j = 8 * threadIdx.x; j < g.ld; j += 8 * blockDim.x) {
+      row8<kType, kNorm, kRes, kGainF32>(g, row, j, true, v, unused_top, unused_sum);
+      *reinterpret_cast<u32x2*>(g.codes + row * g.ld + j) = r.live ? encode8(v, r.a, r.inv) : u32x2{0, 0};
+    }
+  }
+}
+
+// Eight codes a thread and turn; blockIdx.y takes a part of the columns.
 template <int kType>
 __global__ __launch_bounds__(256) void dequantize_rows_kernel(const int8_t* codes, int64_t ld, const float* scale,
-                                                              int64_t rows, int64_t cols, void* out) {
-  typedef Elem<kType> E;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+                                                              int64_t rows, int64_t cols, void* out, int tx) {
+  typedef typename Elem<kType>::T T;
+  const int64_t step = 256 / tx * static_cast<int64_t>(gridDim.x);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / tx) + threadIdx.x / tx; row < rows; row += step) {
     const float s = scale[row];
-    typename E::T* o = static_cast<typename E::T*>(out) + row * cols;
-    for (int64_t j = threadIdx.x; j < cols; j += blockDim.x)
-      o[j] = E::put(static_cast<float>(codes[row * ld + j]) * s);
+    T* o = static_cast<T*>(out) + row * cols;
+    for (int64_t j = 8 * (threadIdx.x % tx + static_cast<int64_t>(blockIdx.y) * tx); j < cols; j += 8 * tx * gridDim.y) {
+      const u32x2 c = *reinterpret_cast<const u32x2*>(codes + row * ld + j);
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(static_cast<int8_t>(c[e >> 2] >> (8 * (e & 3)))) * s;
+      if (j + 8 <= cols) {
+        put8<kType>(o + j, f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (j + e < cols) o[j + e] = Elem<kType>::put(f[e]);
+      }
+    }
   }
 }
 
-// Workgroups of a launch over rows: one a row, at most 2^20 (the grid's work
-// items are counted in 32 bits).
-unsigned row_blocks(int64_t rows) { return static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20)); }
+constexpr int kMaxBlocks = 1 << 20;  // a grid's work items are counted in 32 bits
 
-template <int kType>
-hipError_t launch_rows(const RowArgs& g, bool norm, bool gain_f32, hipStream_t s) {
-  const dim3 grid(row_blocks(g.rows)), block(256);
-  if (!norm) {
-    hipLaunchKernelGGL((rows_kernel<kType, false, true>), grid, block, 0, s, g);
-  } else if (gain_f32) {
-    hipLaunchKernelGGL((rows_kernel<kType, true, true>), grid, block, 0, s, g);
+unsigned blocks_for(int64_t rows, int per_block) {
+  const int64_t b = (rows + per_block - 1) / per_block;
+  return static_cast<unsigned>(b < kMaxBlocks ? b : kMaxBlocks);
+}
+
+template <int kType, bool kNorm, bool kRes, bool kGainF32>
+hipError_t launch_rows(const RowArgs& g, hipStream_t s) {
+  const int64_t chunks = g.ld / 8;
+  if (chunks <= 128) {
+    auto kern = chunks <= 64 ? rows_kernel<kType, kNorm, kRes, kGainF32, 1, true>
+                             : rows_kernel<kType, kNorm, kRes, kGainF32, 2, true>;
+    hipLaunchKernelGGL(kern, dim3(blocks_for(g.rows, 4)), dim3(256), 0, s, g);
+  } else if (chunks <= 4096) {
+    // Few rows: as many threads as there are chunks. Many: 256 threads of up to
+    // 4 chunks each where these hold the row.
+    const int most = g.rows <= 512 ? 1 : 4;
+    int threads = 256;
+    while (threads < 1024 && static_cast<int64_t>(threads) * most < chunks) threads *= 2;
+    const int n = static_cast<int>((chunks + threads - 1) / threads);
+    auto kern = n == 1   ? rows_kernel<kType, kNorm, kRes, kGainF32, 1, false>
+                : n == 2 ? rows_kernel<kType, kNorm, kRes, kGainF32, 2, false>
+                : n == 3 ? rows_kernel<kType, kNorm, kRes, kGainF32, 3, false>
+                         : rows_kernel<kType, kNorm, kRes, kGainF32, 4, false>;
+    hipLaunchKernelGGL(kern, dim3(blocks_for(g.rows, 1)), dim3(threads), 0, s, g);
   } else {
-    hipLaunchKernelGGL((rows_kernel<kType, true, false>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((long_rows_kernel<kType, kNorm, kRes, kGainF32>), dim3(blocks_for(g.rows, 1)), dim3(1024), 0, s,
+                       g);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_rows(const RowArgs& g, int dtype, bool norm, bool gain_f32, hipStream_t s) {
-  if (dtype == QLORA_F32) return launch_rows<QLORA_F32>(g, norm, true, s);
-  return dtype == QLORA_F16 ? launch_rows<QLORA_F16>(g, norm, gain_f32, s) : launch_rows<QLORA_BF16>(g, norm, gain_f32, s);
+template <int kType>
+hipError_t launch_norm(const RowArgs& g, bool gain_f32, hipStream_t s) {
+  const bool res = g.residual != nullptr;
+  if (kType == QLORA_F32 || gain_f32)
+    return res ? launch_rows<kType, true, true, true>(g, s) : launch_rows<kType, true, false, true>(g, s);
+  return res ? launch_rows<kType, true, true, false>(g, s) : launch_rows<kType, true, false, false>(g, s);
 }
 
 }  // namespace
 
 hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, int64_t ld,
                                 float* scale, hipStream_t s) {
-  return launch_rows(RowArgs{x, nullptr, nullptr, nullptr, rows, cols, ld, 0.0f, codes, scale}, dtype, false, true, s);
+  const RowArgs g{x, nullptr, nullptr, nullptr, rows, cols, ld, 0.0f, codes, scale};
+  return dtype == QLORA_F32   ? launch_rows<QLORA_F32, false, false, true>(g, s)
+         : dtype == QLORA_F16 ? launch_rows<QLORA_F16, false, false, true>(g, s)
+                              : launch_rows<QLORA_BF16, false, false, true>(g, s);
 }
 
 hipError_t launch_rmsnorm_int8(const void* x, const void* residual, const void* gain, int dtype, bool gain_f32,
                                int64_t rows, int64_t cols, float eps, void* residual_out, int8_t* codes, int64_t ld,
                                float* scale, hipStream_t s) {
-  return launch_rows(RowArgs{x, residual, gain, residual_out, rows, cols, ld, eps, codes, scale}, dtype, true, gain_f32,
-                     s);
+  const RowArgs g{x, residual, gain, residual_out, rows, cols, ld, eps, codes, scale};
+  return dtype == QLORA_F32   ? launch_norm<QLORA_F32>(g, gain_f32, s)
+         : dtype == QLORA_F16 ? launch_norm<QLORA_F16>(g, gain_f32, s)
+                              : launch_norm<QLORA_BF16>(g, gain_f32, s);
 }
 
 hipError_t launch_int8_dequantize(const int8_t* codes, int64_t ld, const float* scale, int64_t rows, int64_t cols,
                                   int dtype, void* out, hipStream_t s) {
-  const dim3 grid(row_blocks(rows)), block(256);
+  const int64_t chunks = (cols + 7) / 8;
+  int tx = 8;
+  while (tx < 256 && tx < chunks) tx *= 2;
+  const int64_t parts = (chunks + 4 * tx - 1) / (4 * tx);  // 4 turns a thread
+  const dim3 grid(blocks_for(rows, 256 / tx), static_cast<unsigned>(parts < 1024 ? parts : 1024)), block(256);
   auto kern = dtype == QLORA_F32   ? dequantize_rows_kernel<QLORA_F32>
               : dtype == QLORA_F16 ? dequantize_rows_kernel<QLORA_F16>
                                    : dequantize_rows_kernel<QLORA_BF16>;
-  hipLaunchKernelGGL(kern, grid, block, 0, s, codes, ld, scale, rows, cols, out);
+  hipLaunchKernelGGL(kern, grid, block, 0, s, codes, ld, scale, rows, cols, out, tx);
   return hipGetLastError();
 }
 
