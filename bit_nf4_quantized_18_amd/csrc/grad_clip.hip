@@ -17,19 +17,22 @@
 namespace qlora {
 namespace {
 
-constexpr int kTensors = 180;
+constexpr int kTensors = 240;
 constexpr int kThreads = 256;
 constexpr int kRun = 8;                         // elements of a thread at a time
 constexpr int kTurns = 4;                       // runs of a thread in a chunk, at most
 constexpr int kSmallChunk = kThreads * kRun;    // 2048
 constexpr int kChunk = kSmallChunk * kTurns;    // 8192
-constexpr int kSumBlocks = 512;                 // workgroups of a first launch, at most
+constexpr int kSumBlocks = 1024;                // workgroups of a first launch, at most
 constexpr int kScaleBlocks = 1024;              // of the second
 
+// A launch's tensors. Tensor i's chunks are first[i] .. first[i + 1] - 1,
+// counted from the launch's first; pad[i] elements are missing from the chunks
+// in front of it, so its elements in front in the list, and its length, follow.
 struct Slice {
   const void* at[kTensors];
-  int64_t off[kTensors + 1];  // elements in front of tensor i in the list
-  int32_t first[kTensors];    // its first chunk, counted over all launches
+  int32_t first[kTensors + 1];
+  int32_t pad[kTensors + 1];
 };
 static_assert(sizeof(Slice) <= 3900, "kernel arguments end at 4 KB");
 
@@ -53,14 +56,23 @@ __device__ __forceinline__ double reduce_sum(double v) {
 }
 
 // A thread's runs of a chunk: run i starts at element kRun (thread + i
-// kThreads); what lies behind the chunk's end is zero.
+// kThreads); what lies behind the chunk's end is zero. A whole chunk is loaded
+// without a branch, all runs in flight at once.
 template <int kType>
 __device__ __forceinline__ void load_chunk(const typename Elem<kType>::T* p, int64_t len, float (*v)[kRun]) {
+  if (len == kChunk) {
+    Words8<kType> w[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) w[i] = load8<kType>(p + kRun * (threadIdx.x + i * kThreads));
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) values8<kType>(w[i], v[i]);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
     const int64_t j = kRun * (threadIdx.x + i * kThreads);
     if (j + kRun <= len) {
-      get8<kType>(p + j, v[i]);
+      values8<kType>(load8<kType>(p + j), v[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < kRun; ++e) v[i][e] = j + e < len ? Elem<kType>::get(p[j + e]) : 0.0f;
@@ -69,22 +81,24 @@ __device__ __forceinline__ void load_chunk(const typename Elem<kType>::T* p, int
 }
 
 template <int kType>
-__global__ __launch_bounds__(kThreads) void square_sum_kernel(Slice l, int tensors, int chunk0, int chunk1,
-                                                              int chunk, double* partial, Record* records) {
+__global__ __launch_bounds__(kThreads) void square_sum_kernel(Slice l, int tensors, int chunk, int64_t off0,
+                                                              double* partial, Record* records) {
   typedef typename Elem<kType>::T T;
   const int lane = threadIdx.x & 63;
   double sum = 0.0;
-  for (int c = chunk0 + blockIdx.x; c < chunk1; c += gridDim.x) {
+  const int chunks = l.first[tensors];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     // the last tensor that starts at or in front of chunk c: the starts ascend
     int t = -1;
 #pragma unroll
     for (int j = 0; j < kTensors; j += 64)
       t += __popcll(__ballot(j + lane < tensors && l.first[j + lane < kTensors ? j + lane : 0] <= c));
     t = __builtin_amdgcn_readfirstlane(t);
-    const int64_t begin = static_cast<int64_t>(c - l.first[t]) * chunk, size = l.off[t + 1] - l.off[t];
-    const int64_t len = size - begin < chunk ? size - begin : chunk;
+    const int64_t begin = static_cast<int64_t>(c - l.first[t]) * chunk;
+    const int len = c + 1 < l.first[t + 1] ? chunk : chunk - (l.pad[t + 1] - l.pad[t]);
     const T* p = static_cast<const T*>(l.at[t]) + begin;
-    if (records != nullptr && threadIdx.x == 0) records[c] = Record{p, l.off[t] + begin, len};
+    if (records != nullptr && threadIdx.x == 0)
+      records[c] = Record{p, off0 + static_cast<int64_t>(c) * chunk - l.pad[t], len};
     float v[kTurns][kRun];
     load_chunk<kType>(p, len, v);
 #pragma unroll
@@ -182,25 +196,26 @@ hipError_t launch_t(const void* const* grads, const int64_t* numel, int count, b
   double* partial = static_cast<double*>(ws);
   Record* records = reinterpret_cast<Record*>(static_cast<char*>(ws) + up256(p.partials * 8));
   Slice l{};
-  int tensors = 0, chunk0 = 0, chunk1 = 0, partials = 0;
-  int64_t off = 0;
+  int tensors = 0, chunks = 0, partials = 0;
+  int64_t off = 0, off0 = 0;  // elements in front of the next tensor, of the launch
   for (int i = 0; i <= count; ++i) {
     if (i < count && numel[i] > 0) {
+      const int64_t n = chunks_of(numel[i], p.chunk);
       l.at[tensors] = grads[i];
-      l.off[tensors] = off;
-      l.first[tensors] = chunk1;
+      l.first[tensors + 1] = l.first[tensors] + static_cast<int32_t>(n);
+      l.pad[tensors + 1] = l.pad[tensors] + static_cast<int32_t>(n * p.chunk - numel[i]);
       off += numel[i];
-      chunk1 += static_cast<int>(chunks_of(numel[i], p.chunk));
-      l.off[++tensors] = off;
+      ++tensors;
     }
     if (tensors == kTensors || (i == count && tensors > 0)) {
-      const int blocks = chunk1 - chunk0 < kSumBlocks ? chunk1 - chunk0 : kSumBlocks;
-      hipLaunchKernelGGL((square_sum_kernel<kType>), dim3(blocks), dim3(kThreads), 0, s, l, tensors, chunk0, chunk1,
-                         p.chunk, partial + partials, clip ? records : nullptr);
+      const int mine = l.first[tensors], blocks = mine < kSumBlocks ? mine : kSumBlocks;
+      hipLaunchKernelGGL((square_sum_kernel<kType>), dim3(blocks), dim3(kThreads), 0, s, l, tensors, p.chunk, off0,
+                         partial + partials, clip ? records + chunks : nullptr);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       partials += blocks;
-      chunk0 = chunk1;
+      chunks += mine;
+      off0 = off;
       tensors = 0;
     }
   }

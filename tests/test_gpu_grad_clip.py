@@ -20,12 +20,14 @@ HALF_STEP = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8, "float16": 2.0 ** -11
 LISTS = {
     "one_element": [1],
     "small": [5, 0, 64, 1],
-    "chunk_edges": [16383, 16384, 16385, 32768, 2047, 2048, 2049, 4097],
+    "chunk_edges": [8191, 8192, 8193, 16383, 16384, 16385, 32768, 2047, 2048, 2049, 4097],
     "layer_rank8": [8 * 512, 512 * 8, 8 * 512, 1376 * 8, 8 * 1376],
     "many": [(37 * i) % 301 for i in range(500)],          # more than one launch's list, empties among them
-    "exactly_one_slice": [100] * 180,
-    "one_over_a_slice": [100] * 181,
+    "exactly_one_slice": [100] * 240,
+    "one_over_a_slice": [100] * 241,
+    "two_slices_of_chunks": [2049, 5000, 1] * 160,
     "long": [3_000_001],
+    "long_chunks": [4_194_305, 8191, 70_000, 8193],        # over 512 chunks of 8192: the longer chunks
 }
 
 
