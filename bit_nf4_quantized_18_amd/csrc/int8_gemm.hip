@@ -26,6 +26,7 @@ struct LinearArgs {
   const float* sx;
   void* y;
   int64_t m, n, k;
+  int64_t ldy;  // a row of y; n but for a part of the channels
 };
 
 // ---------------------------------------------------------------------------
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
       const int64_t m = m0 + wm * TM * 16 + 16 * a + i;
-      if (m < g.m) store_run<kType>(y + m * g.n + nc, acc[a] + 4 * c, g.sx[m], sw, g.n - nc);
+      if (m < g.m) store_run<kType>(y + m * g.ldy + nc, acc[a] + 4 * c, g.sx[m], sw, g.n - nc);
     }
   }
 }
@@ -345,7 +346,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void decode_kernel(LinearArgs g)
   int sum = 0;
 #pragma unroll
   for (int w = 0; w < kDecodeWaves; ++w) sum += part[w][at];
-  static_cast<typename Elem<kType>::T*>(g.y)[tok * g.n + n0 + ch] =
+  static_cast<typename Elem<kType>::T*>(g.y)[tok * g.ldy + n0 + ch] =
       Elem<kType>::put((static_cast<float>(sum) * g.sx[tok]) * g.sw[n0 + ch]);
 }
 
@@ -384,32 +385,40 @@ constexpr Shape kShapes[] = {{256, 256, 512, 8, 1.5},   {128, 256, 512, 5, 0.9},
                              {16, 64, 128, 3.5, 0.125}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 
-// Index into kShapes, or -1: no tile's grid stays below 2^32 work items.
-int pick_shape(int64_t m, int64_t n, int64_t k) {
-  int best = -1;
-  double best_us = 0;
+int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn); }
+
+struct Pick {
+  int shape;  // into kShapes; -1: no tile's grid stays below 2^32 work items
+  double us;
+};
+Pick pick_shape(int64_t m, int64_t n, int64_t k) {
+  Pick best{-1, 0};
   for (int i = 0; i < kNumShapes; ++i) {
     const Shape& s = kShapes[i];
-    const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn);
+    const int64_t tiles = tiles_of(s, m, n);
     if (tiles >= (INT64_C(1) << 32) / s.threads) continue;
     const double us = s.fixed + static_cast<double>((tiles + 255) / 256) * static_cast<double>((k + 127) / 128) * s.unit;
-    if (best < 0 || us < best_us) {
-      best = i;
-      best_us = us;
-    }
+    if (best.shape < 0 || us < best.us) best = Pick{i, us};
   }
   return best;
 }
 
-}  // namespace
+// Channels of a first launch in 256 x 256 tiles whose rounds are full, where
+// these and a second launch for the other channels cost less than one launch;
+// 0 where they do not. 4096 x 22016 x 8192 has 1376 tiles, 5.4 rounds: 574 us
+// in one launch, 551 us as five full rounds and 192 tiles of 128 x 256.
+constexpr double kSecondLaunch = 3;  // us
+int64_t full_rounds(int64_t m, int64_t n, int64_t k, const Pick& one) {
+  const int64_t tiles_m = (m + 255) / 256, tiles = tiles_of(kShapes[0], m, n);
+  if (one.shape != 0 || tiles_m > 256 || tiles % 256 == 0) return 0;
+  const int64_t rounds = tiles / 256, cols = rounds * 256 / tiles_m * 256;
+  if (cols < 256 || cols >= n) return 0;
+  const double first = kShapes[0].fixed + static_cast<double>(rounds) * static_cast<double>((k + 127) / 128) * kShapes[0].unit;
+  return first + kSecondLaunch + pick_shape(m, n - cols, k).us < one.us ? cols : 0;
+}
 
-bool int8_linear_fits(int64_t m, int64_t n, int64_t k) { return decodes(m, n) || pick_shape(m, n, k) >= 0; }
-
-hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
-                              const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s) {
-  const LinearArgs g{w, w_scale, x, x_scale, y, m, n, k};
-  if (decodes(m, n)) return launch_decode(g, out_dtype, s);
-  switch (pick_shape(m, n, k)) {
+hipError_t launch_shape(int shape, const LinearArgs& g, int out_dtype, hipStream_t s) {
+  switch (shape) {
     case 0:
       return launch_tiles<256, 256, 2, 4, 1, 5>(g, out_dtype, s);
     case 1:
@@ -426,6 +435,29 @@ hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, 
       return launch_tiles<16, 64, 1, 1, 2, 8>(g, out_dtype, s);
   }
   return hipErrorInvalidValue;  // int8_linear_fits refuses these sizes
+}
+
+}  // namespace
+
+bool int8_linear_fits(int64_t m, int64_t n, int64_t k) { return decodes(m, n) || pick_shape(m, n, k).shape >= 0; }
+
+hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
+                              const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s) {
+  LinearArgs g{w, w_scale, x, x_scale, y, m, n, k, n};
+  if (decodes(m, n)) return launch_decode(g, out_dtype, s);
+  const Pick one = pick_shape(m, n, k);
+  const int64_t cols = full_rounds(m, n, k, one);
+  if (cols > 0) {
+    g.n = cols;
+    const hipError_t e = launch_shape(0, g, out_dtype, s);
+    if (e != hipSuccess) return e;
+    g.w = w + cols * k;
+    g.sw = w_scale + cols;
+    g.y = static_cast<char*>(y) + cols * (out_dtype == QLORA_F32 ? 4 : 2);
+    g.n = n - cols;
+    return launch_shape(pick_shape(m, g.n, k).shape, g, out_dtype, s);
+  }
+  return launch_shape(one.shape, g, out_dtype, s);
 }
 
 }  // namespace qlora

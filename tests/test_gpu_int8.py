@@ -275,6 +275,29 @@ def test_linear_token_rows_do_not_depend_on_m(gpu_lib):
         assert torch.equal(part, whole[:m]), m
 
 
+def test_linear_in_two_launches(gpu_lib):
+    """A size whose 256 x 256 tiles fill three rounds of the CUs and part of a
+    fourth, whose channels go to two launches: every token's row is bit-equal to
+    the one computed in batches of 50, and sampled rows to the oracle's."""
+    import torch
+
+    m, n, k = 1000, 53248 + 77, 1856
+    say(f"[int8 linear] two launches, m={m} n={n} k={k}")
+    rng = np.random.default_rng(4)
+    w, sw, _, _ = _operands(1, n, k, 5)
+    x = np.clip(np.rint(rng.standard_normal((m, k)) * 32), -127, 127).astype(np.int8)
+    sx = (10.0 ** rng.uniform(-3, -1, m)).astype(np.float32)
+    qw = _packed(gpu_lib, w, sw, k)
+    for dtype in ("bfloat16", "float32"):
+        y = gpu_lib.int8_linear_fwd(qw, _packed(gpu_lib, x, sx, k), _t(dtype))
+        for a in range(0, m, 50):
+            part = gpu_lib.int8_linear_fwd(qw, _packed(gpu_lib, x[a:a + 50], sx[a:a + 50], k), _t(dtype))
+            torch.cuda.synchronize()
+            assert torch.equal(y[a:a + 50], part)
+        pick = [0, 255, 256, 511, 767, 768, 999]
+        _same(_f32(y[pick]), _round(OI.linear(w, sw, x[pick], sx[pick]), dtype))
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_writes_stay_inside(gpu_lib, m):
     """Memory behind the outputs keeps its values (odd sizes)."""
