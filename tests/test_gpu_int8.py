@@ -411,3 +411,62 @@ def test_other_stream(gpu_lib):
     s.synchronize()
     _same(y.cpu().numpy(), OI.linear(w, sw, x, sx))
 
+
+def test_no_rows_and_no_tokens(gpu_lib):
+    import torch
+
+    for dtype in TYPES:
+        x = torch.empty((0, 70), dtype=_t(dtype), device="cuda")
+        q = gpu_lib.quantize_int8(x)
+        assert q.codes.shape == (0, 128) and q.scale.shape == (0,)
+        assert gpu_lib.dequantize_int8(q, _t(dtype)).shape == (0, 70)
+        qn, h = gpu_lib.rmsnorm_int8(x, torch.ones(70, device="cuda"), residual=x)
+        assert qn.n == 0 and h.shape == (0, 70)
+        w, sw, _, _ = _operands(1, 9, 70, 1)
+        assert gpu_lib.int8_linear_fwd(_packed(gpu_lib, w, sw, 70), q, _t(dtype)).shape == (0, 9)
+
+
+def test_another_current_device(gpu_lib, monkeypatch):
+    """Where the tensors' GPU is not the current one the call makes it so: with
+    one GPU, the current index is read as another."""
+    w, sw, x, sx = _operands(20, 64, 128, 1)
+    qw, qx = _packed(gpu_lib, w, sw, 128), _packed(gpu_lib, x, sx, 128)
+    gpu_lib.int8_linear_fwd(qw, qx)
+    monkeypatch.setattr(gpu_lib, "_device_now", lambda: 1)
+    import torch
+
+    y = gpu_lib.int8_linear_fwd(qw, qx, torch.float32)
+    torch.cuda.synchronize()
+    _same(y.cpu().numpy(), OI.linear(w, sw, x, sx))
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Calls of the same shapes on two streams, each on its own buffers: no
+    state is shared between them."""
+    import torch
+
+    n, k = 777, 1024
+    rng = np.random.default_rng(8)
+    qw = gpu_lib.quantize_int8(torch.from_numpy(rng.standard_normal((n, k)).astype(np.float32)).cuda())
+    xs = [_rows(200, k, "bfloat16", i, spread=False).cuda() for i in range(2)]
+    gain = torch.ones(k, device="cuda")
+    grads = [[torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda() for s in (5000, 70001)] for _ in range(2)]
+
+    def work(i):
+        q, h = gpu_lib.rmsnorm_int8(xs[i], gain, residual=xs[1 - i])
+        out = torch.empty(75001, device="cuda")
+        norm = gpu_lib.grad_clip(grads[i], 1.0, out=out)
+        return gpu_lib.int8_linear_fwd(qw, q), h, out, norm
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))

@@ -80,7 +80,7 @@ def test_grad_argument_errors():
 
     for f in (norm, clip):
         assert f(t=3) == -4 and f(p=None) == -1 and f(s=None) == -1 and f(out=None) == -1
-        assert f(out=P + 4) == -3 and f(ws=P + 8) == -3
+        assert f(out=P + 2) == -3 and f(ws=P + 8) == -3
         assert f(nbytes=need - 1) == -5 and f(ws=None) == -5
         assert f(c=-1) == -2 and f(c=(1 << 20) + 1) == -2
         p2, s2, c2 = _grads([100, -1])
