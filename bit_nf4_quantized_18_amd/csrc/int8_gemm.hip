@@ -219,6 +219,26 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  // Lane: tokens 16 a + i, channels 64 (b / 4) + 16 h + 4 (b % 4) + v: runs of
+  // 16 neighbouring channels, 64 the four lanes of a token. Tiles that leave
+  // registers for their scales load these in front of the contraction.
+  constexpr bool kEarly = TM * TN <= 16;
+  float sx[TM], sw[kEarly ? TN / 4 : 1][16];
+  auto load_scales = [&](int c) {
+    const int64_t nc = n0 + wn * TN * 16 + 64 * c + 16 * h;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sw[kEarly ? c : 0][e] = g.sw[nc + e < g.n ? nc + e : g.n - 1];
+    if (c > 0) return;
+#pragma unroll
+    for (int a = 0; a < TM; ++a) {
+      const int64_t m = m0 + wm * TM * 16 + 16 * a + i;
+      sx[a] = g.sx[m < g.m ? m : g.m - 1];
+    }
+  };
+  if (kEarly) {
+#pragma unroll
+    for (int c = 0; c < TN / 4; ++c) load_scales(c);
+  }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     if (p % 2 == 0) copy_x(ring[p], p / 2);
@@ -267,19 +287,15 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
     }
   }
 
-  // Lane: tokens 16 a + i, channels 64 (b / 4) + 16 h + 4 (b % 4) + v: runs of
-  // 16 neighbouring channels, 64 the four lanes of a token.
   T* y = static_cast<T*>(g.y);
 #pragma unroll
   for (int c = 0; c < TN / 4; ++c) {
     const int64_t nc = n0 + wn * TN * 16 + 64 * c + 16 * h;
-    float sw[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sw[e] = g.sw[nc + e < g.n ? nc + e : g.n - 1];
+    if (!kEarly) load_scales(c);
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
       const int64_t m = m0 + wm * TM * 16 + 16 * a + i;
-      if (m < g.m) store_run<kType>(y + m * g.ldy + nc, acc[a] + 4 * c, g.sx[m], sw, g.n - nc);
+      if (m < g.m) store_run<kType>(y + m * g.ldy + nc, acc[a] + 4 * c, sx[a], sw[kEarly ? c : 0], g.n - nc);
     }
   }
 }
@@ -361,31 +377,36 @@ hipError_t launch_decode(const LinearArgs& g, int out_dtype, hipStream_t s) {
 bool decodes(int64_t m, int64_t n) { return m <= kDecodeTokens && n <= kDecodeMaxN; }
 
 // ---------------------------------------------------------------------------
-// The tile for a call: the one with the least fixed + rounds * units * unit
-// microseconds, where rounds counts turns of the 256 CUs and units steps of 128
-// codes. Fitted to measured times (graph replays, bf16 out); it names the
-// fastest tile, or one within 10% of it, at (m x n x k, us):
-//   4096 x 22016 x 8192: 256 x 256 575, 128 x 256 634, 128 x 128 724
-//   4096 x 8192 x 8192:  256 x 256 206, 128 x 256 238
+// The tile for a call: the one with the least kLaunch + rounds * (round + units *
+// unit) microseconds, where rounds counts turns of the 256 CUs, units steps of
+// 128 codes, `round` a tile's start and its outputs. Fitted to measured times
+// (graph replays, bf16 out). Over 48 sizes drawn from 1 .. 4096 tokens, 64 ..
+// 22016 channels and 64 .. 11008 codes its choice takes 1.4% longer on average
+// than the best tile for each. Some of the times behind it (m x n x k, us):
+//   4096 x 8192 x 8192:  256 x 256 206, 128 x 256 238, 128 x 128 317
 //   2048 x 4096 x 11008: 128 x 256 76, 128 x 128 92, 256 x 256 102
 //   2048 x 11008 x 4096: 128 x 256 90, 256 x 256 104, 128 x 128 119
 //   512 x 4096 x 4096:   64 x 128 14.8, 64 x 64 17.6, 128 x 128 19.0
-//   200 x 11008 x 4096:  64 x 128 24.4, 64 x 64 25.4, 128 x 256 about 25
-//   333 x 5003 x 4160:   64 x 128 18.6, 64 x 64 21.3, 128 x 128 21.9
 //   128 x 4096 x 4096:   32 x 64 8.6, 64 x 64 10.8, 64 x 128 12.5
 //   64 x 11008 x 4096:   64 x 64 11.3, 64 x 128 13.5, 32 x 64 15.9
 //   32 x 4096 x 11008:   16 x 64 14.4, 32 x 64 17.1
+//   745 x 21599 x 147:   256 x 256 22, 128 x 256 24, 64 x 64 34, 16 x 64 96
 // ---------------------------------------------------------------------------
 struct Shape {
   int bm, bn, threads;
-  double fixed, unit;
+  double round, unit;
 };
-constexpr Shape kShapes[] = {{256, 256, 512, 8, 1.5},   {128, 256, 512, 5, 0.9},   {128, 128, 256, 4, 0.53},
-                             {64, 128, 256, 4, 0.34},   {64, 64, 256, 3.5, 0.22},  {32, 64, 256, 3.5, 0.16},
-                             {16, 64, 128, 3.5, 0.125}};
+constexpr Shape kShapes[] = {{256, 256, 512, 12, 1.4},  {128, 256, 512, 8, 0.78},   {128, 128, 256, 4.5, 0.5},
+                             {64, 128, 256, 3, 0.34},   {64, 64, 256, 1.4, 0.22},   {32, 64, 256, 2.2, 0.14},
+                             {16, 64, 128, 1.2, 0.13}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
+constexpr double kLaunch = 2;
 
 int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn); }
+
+double cost(const Shape& s, int64_t tiles, int64_t k) {
+  return kLaunch + static_cast<double>((tiles + 255) / 256) * (s.round + static_cast<double>((k + 127) / 128) * s.unit);
+}
 
 struct Pick {
   int shape;  // into kShapes; -1: no tile's grid stays below 2^32 work items
@@ -394,10 +415,9 @@ struct Pick {
 Pick pick_shape(int64_t m, int64_t n, int64_t k) {
   Pick best{-1, 0};
   for (int i = 0; i < kNumShapes; ++i) {
-    const Shape& s = kShapes[i];
-    const int64_t tiles = tiles_of(s, m, n);
-    if (tiles >= (INT64_C(1) << 32) / s.threads) continue;
-    const double us = s.fixed + static_cast<double>((tiles + 255) / 256) * static_cast<double>((k + 127) / 128) * s.unit;
+    const int64_t tiles = tiles_of(kShapes[i], m, n);
+    if (tiles >= (INT64_C(1) << 32) / kShapes[i].threads) continue;
+    const double us = cost(kShapes[i], tiles, k);
     if (best.shape < 0 || us < best.us) best = Pick{i, us};
   }
   return best;
@@ -407,14 +427,12 @@ Pick pick_shape(int64_t m, int64_t n, int64_t k) {
 // these and a second launch for the other channels cost less than one launch;
 // 0 where they do not. 4096 x 22016 x 8192 has 1376 tiles, 5.4 rounds: 574 us
 // in one launch, 551 us as five full rounds and 192 tiles of 128 x 256.
-constexpr double kSecondLaunch = 3;  // us
 int64_t full_rounds(int64_t m, int64_t n, int64_t k, const Pick& one) {
   const int64_t tiles_m = (m + 255) / 256, tiles = tiles_of(kShapes[0], m, n);
   if (one.shape != 0 || tiles_m > 256 || tiles % 256 == 0) return 0;
-  const int64_t rounds = tiles / 256, cols = rounds * 256 / tiles_m * 256;
+  const int64_t cols = tiles / 256 * 256 / tiles_m * 256;
   if (cols < 256 || cols >= n) return 0;
-  const double first = kShapes[0].fixed + static_cast<double>(rounds) * static_cast<double>((k + 127) / 128) * kShapes[0].unit;
-  return first + kSecondLaunch + pick_shape(m, n - cols, k).us < one.us ? cols : 0;
+  return cost(kShapes[0], tiles_of(kShapes[0], m, cols), k) + pick_shape(m, n - cols, k).us < one.us ? cols : 0;
 }
 
 hipError_t launch_shape(int shape, const LinearArgs& g, int out_dtype, hipStream_t s) {
