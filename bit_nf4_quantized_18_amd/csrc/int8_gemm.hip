@@ -3,6 +3,19 @@
 // Codes are contracted with v_mfma_i32_16x16x64_i8 into exact 32-bit integer
 // sums (k 128^2 < 2^31), so the sums do not depend on the order or the split
 // of the work; the scales enter once, at the end.
+//
+// What bounds it, by size (MI355X; graph replays, bf16 out):
+//   - Few tokens: the weight's bytes. 1 x 4096 x 4096 (m x n x k) 5.8 us, 16 x
+//     11008 x 4096 10.7 us (45 MB; a large copy moves 4.7 TB/s here, read and
+//     written).
+//   - Hundreds of tokens: the copies into LDS. With the products left out a CU
+//     copies at most 85-90 bytes a nanosecond, and a tile of 64 x 128 needs 24
+//     KB for a unit of 128 codes: 333 x 5003 x 4160 takes 17.6 us, 0.36 us a
+//     unit and 6 us around them. Two groups of waves on that tile gain nothing.
+//   - Thousands: the matrix cores and their power. 4096 x 8192 x 8192 206 us
+//     (2670 TOP/s); the matrix cores are busy 68% of the cycles, at 1.8 GHz. With
+//     v_mfma_i32_32x32x32_i8 in 128 x 128 tiles a wave (a third fewer LDS reads)
+//     the cycles are as many, at 1.64 GHz: 236 us.
 #include "bufmem.h"
 #include "elem.h"
 
@@ -30,9 +43,12 @@ struct LinearArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Tiles through LDS.
+// Tiles through LDS: both operands are copied from memory into a ring of units
+// (128 codes of the tile's rows), read as fragments and multiplied. 128 codes
+// are a cache line of a row: copies of 64-code rows moved half as many codes a
+// cycle (4096 x 22016 x 8192: 632 us, 603 us with whole lines).
 // ---------------------------------------------------------------------------
-constexpr int kUnit = 128;  // contraction codes of a stage: a whole cache line of a row
+constexpr int kUnit = 128;
 constexpr int kXcds = 8;
 constexpr int kNowhere = 0x70000000;  // an offset past every tile's range, also with one of a tile added
 
@@ -71,14 +87,18 @@ __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t src, int8_t* dst,
 
 // P: parts of the LDS ring. A unit of 128 codes is two parts, the tokens' and
 // the channels'; the ring holds P / 2 units, and with an odd P the tokens' part
-// of one more, so that half of the codes have a unit's time more to arrive.
+// of one more, so that half of the codes have a unit's time more to arrive: the
+// 256 x 256 tile's five parts are all of LDS (4096 x 8192 x 8192: 212 us with
+// four, 206 with five).
 // KS: groups of WM x WN waves that share the contraction of one tile, each with
-// a ring of its own; their sums are added through LDS at the end.
+// a ring of its own; their sums are added through LDS at the end. For tiles so
+// small that one group keeps too few copies in flight (128 x 4096 x 4096 in 32
+// x 64 tiles: 8.6 us with two groups).
 template <int BM, int BN, int WM, int WN, int KS, int P, int kType>
 __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave: tokens, channels
-  constexpr int LX = BM / 8 / kWaves, LW = BN / 8 / kWaves;  // 1 KB copies of a wave a stage
+  constexpr int LX = BM / 8 / kWaves, LW = BN / 8 / kWaves;  // 1 KB copies of a wave a part
   constexpr int kLoads = LX + LW;
   constexpr int S = P / 2;        // units that the ring holds whole
   constexpr bool kOdd = P % 2 != 0;
@@ -127,7 +147,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.k, mrows * g.k);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + n0 * g.k, nrows * g.k);
 
-  // Copy l of a wave fills block l kWaves + wave of a stage: 8 rows of 128
+  // Copy l of a wave fills block l kWaves + wave of a part: 8 rows of 128
   // bytes, lane l the 16 bytes at row l / 8, place l % 8. A row's chunk c
   // stands at place c ^ key(row). The 16 lanes that read one chunk column
   // then fall on 16 different 16-byte columns of the banks, both as 16
@@ -159,7 +179,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
     for (int l = 0; l < LW; ++l)
       copy_1k(wr, to + (group * BN / 8 + l * kWaves + wave) * 1024, wo[l] + (8 * l * kWaves * k32 + q));
   };
-  // Fragments of the stage's first or second 64 codes. Token tile t reads rows
+  // Fragments of a unit's first or second 64 codes. Token tile t reads rows
   // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,
   // which leaves a lane with runs of 16 neighbouring channels. Both keys are
   // i / 2.

@@ -7,6 +7,13 @@
 // y = v rstd (v = h gain) keeps its factor rstd = 1 / sqrt(mean(h^2) + eps) out
 // of the codes: 127 y / max|y| = 127 v / max|v|. It enters the scale alone, so
 // both statistics of a row, sum h^2 and max|v|, come from one pass over it.
+//
+// Bound by memory: the norm of 4096 x 8192 bf16 with its residual moves 235 MB in
+// 49 us (4.8 TB/s; a large copy reaches 4.7), quantizing 11008 x 4096 float32 225
+// MB in 42 us, turning it back to bf16 135 MB in 28 us. One row of 4096 takes 4.8
+// us, most of it the launch and one memory latency. Rows stay in registers; what
+// decides is that all loads of a thread are in flight before the first is waited
+// for: with a branch around each load the norm above took 63 us.
 #include "elem.h"
 
 namespace qlora {
