@@ -786,7 +786,7 @@ def rmsnorm_int8(x, gain, eps: float = 1e-6, residual=None, residual_out=None, o
             _need_like(residual_out, "residual_out", x, index)
         rp, op = residual.data_ptr(), residual_out.data_ptr()
     q, ld = _int8_out(out, n, k, x, index)
-    _launch(_LIB.qlora_rmsnorm_int8, index, x.data_ptr(), rp, gain.data_ptr(), code, gain_code, n, k, eps, op,
+    _launch(_LIB.qlora_rmsnorm_int8, index, x.data_ptr(), rp, gain.data_ptr(), code, gain_code, n, k, float(eps), op,
             q.codes.data_ptr(), ld, q.scale.data_ptr())
     return q, residual_out
 
@@ -896,7 +896,7 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
         _need(out, "out", (g.total,), (g.dtype,), g.grads[0].device)
         op = out.data_ptr() if g.total else None
     norm, ws = _grad_buffers(g, index, norm, ws)
-    _launch(_LIB.qlora_grad_clip, index, g._pointers(), g._numel, len(g.grads), g.code, max_norm, op, norm.data_ptr(),
+    _launch(_LIB.qlora_grad_clip, index, g._pointers(), g._numel, len(g.grads), g.code, float(max_norm), op, norm.data_ptr(),
             ws.data_ptr(), ws.numel())
     return norm
 

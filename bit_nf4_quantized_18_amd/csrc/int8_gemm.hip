@@ -8,10 +8,11 @@
 //   - Few tokens: the weight's bytes. 1 x 4096 x 4096 (m x n x k) 5.8 us, 16 x
 //     11008 x 4096 10.7 us (45 MB; a large copy moves 4.7 TB/s here, read and
 //     written).
-//   - Hundreds of tokens: the copies into LDS. With the products left out a CU
-//     copies at most 85-90 bytes a nanosecond, and a tile of 64 x 128 needs 24
-//     KB for a unit of 128 codes: 333 x 5003 x 4160 takes 17.6 us, 0.36 us a
-//     unit and 6 us around them. Two groups of waves on that tile gain nothing.
+//   - Hundreds of tokens: the copies into LDS. 333 x 5003 x 4160 takes 17.6 us in
+//     64 x 128 tiles, 16.5 us with reads and products left out, 6.0 us with the
+//     copies left out too: 190 MB out of the L2 caches at 18 TB/s (20-21 is the
+//     most that any tile reached, 85-90 bytes/ns a CU). A deeper ring or two
+//     groups of waves on that tile gain nothing.
 //   - Thousands: the matrix cores and their power. 4096 x 8192 x 8192 206 us
 //     (2670 TOP/s); the matrix cores are busy 68% of the cycles, at 1.8 GHz. With
 //     v_mfma_i32_32x32x32_i8 in 128 x 128 tiles a wave (a third fewer LDS reads)

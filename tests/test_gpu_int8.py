@@ -398,6 +398,47 @@ def test_merged_adapter_served_in_8_bits(gpu_lib):
     assert err <= 0.016
 
 
+def test_life_of_an_adapter(gpu_lib):
+    """One training step with clipped gradients, the merge, and serving in 8
+    bits: the calls of both ends together. The step's update is checked against
+    float64, and the served output as in the test above (its 1.6%, and the
+    update's float32 roundings, far below it)."""
+    import torch
+
+    from gpu_cases import layer_inputs
+
+    n, k, m, r, alpha, lr = 256, 512, 40, 8, 16.0, 0.05
+    w, x, a, b, dy = layer_inputs(n, k, m, r, "life_of_an_adapter")
+    q = gpu_lib.quantize(torch.from_numpy(w).cuda())
+    x, a, b, dy = x.cuda(), a.cuda(), b.cuda(), dy.cuda()
+    say("[int8] life of an adapter")
+    _, h = gpu_lib.linear_fwd(q, x, a, b, alpha)
+    _, da, db = gpu_lib.linear_bwd(q, x, dy, a, b, alpha, h=h)
+    raw = [da.double(), db.double()]
+    norm = gpu_lib.grad_clip([da, db], 1.0)
+    torch.cuda.synchronize()
+    total = sum(float(g.square().sum()) for g in raw) ** 0.5
+    assert total > 1.0 and abs(float(norm) - total) <= 2.0 ** -22 * total
+    for g, c in zip(raw, (da, db)):
+        # the factor's and the product's roundings
+        assert ((c.double() - g / (total + 1e-6)).abs() <= 2.0 ** -22 * (g / total).abs()).all()
+    a2, b2 = (a.float() - lr * da).bfloat16(), (b.float() - lr * db).bfloat16()
+    merged = gpu_lib.merge(q, a2, b2, alpha, torch.float32)
+    served = gpu_lib.quantize_int8(merged)
+    res = x.clone()
+    qx, hid = gpu_lib.rmsnorm_int8(dy[:, :n].repeat(1, k // n), torch.ones(k, device="cuda"), 1e-6, residual=res,
+                                   residual_out=res)
+    y = gpu_lib.int8_linear_fwd(served, qx)
+    torch.cuda.synchronize()
+    assert hid is res
+    hn = (x.double() + dy.double().repeat(1, k // n)).cpu().numpy()
+    hn = hn / np.sqrt((hn ** 2).mean(axis=1, keepdims=True) + 1e-6)
+    want = hn @ merged.double().cpu().numpy().T
+    err = np.sqrt(np.mean((_f32(y) - want) ** 2) / np.mean(want ** 2))
+    say(f"   relative error {err:.4f}")
+    assert err <= 0.016
+
+
 def test_other_stream(gpu_lib):
     """Calls run on the caller's current stream."""
     import torch
