@@ -7,6 +7,7 @@ functions raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import dataclasses
 import os
@@ -847,16 +848,16 @@ class GradList:
         self.sizes = [g.numel() for g in grads]
         self.total = sum(self.sizes)
         self._numel = (ctypes.c_int64 * max(len(grads), 1))(*self.sizes)
-        self._at = ctypes.c_void_p * max(len(grads), 1)
         self.ws_bytes = int(_LIB.qlora_grad_workspace_bytes(self._numel, len(grads)))
         if self.total and not self.ws_bytes:
             raise ValueError("too many gradients or elements for one call")
 
     def _pointers(self):
+        """The addresses as they are now, in an array of 64-bit numbers."""
         tensor = _torch.Tensor
         if list(map(tensor.numel, self.grads)) != self.sizes:
             raise ValueError("a gradient changed its length since the list was made")
-        return self._at(*map(tensor.data_ptr, self.grads))
+        return array.array("Q", map(tensor.data_ptr, self.grads))
 
 
 def _grad_buffers(g, index, norm, ws):
@@ -879,8 +880,9 @@ def grad_norm(grads, norm=None, ws=None):
     g = grads if isinstance(grads, GradList) else GradList(grads)
     index = g.index if g.grads else _device_now()
     norm, ws = _grad_buffers(g, index, norm, ws)
-    _launch(_LIB.qlora_grad_norm, index, g._pointers(), g._numel, len(g.grads), g.code, norm.data_ptr(), ws.data_ptr(),
-            ws.numel())
+    at = g._pointers()
+    _launch(_LIB.qlora_grad_norm, index, at.buffer_info()[0], g._numel, len(at), g.code, norm.data_ptr(),
+            ws.data_ptr(), ws.numel())
     return norm
 
 
@@ -896,8 +898,9 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
         _need(out, "out", (g.total,), (g.dtype,), g.grads[0].device)
         op = out.data_ptr() if g.total else None
     norm, ws = _grad_buffers(g, index, norm, ws)
-    _launch(_LIB.qlora_grad_clip, index, g._pointers(), g._numel, len(g.grads), g.code, float(max_norm), op, norm.data_ptr(),
-            ws.data_ptr(), ws.numel())
+    at = g._pointers()
+    _launch(_LIB.qlora_grad_clip, index, at.buffer_info()[0], g._numel, len(at), g.code, float(max_norm), op,
+            norm.data_ptr(), ws.data_ptr(), ws.numel())
     return norm
 
 
