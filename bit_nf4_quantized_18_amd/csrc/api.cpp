@@ -166,7 +166,7 @@ const char* qlora_status_string(int status) {
     case QLORA_ERR_ALIGN:
       return "a pointer is not 16-byte aligned";
     case QLORA_ERR_UNSUPPORTED:
-      return "unsupported argument (rank above QLORA_MAX_RANK, dtype or flag)";
+      return "unsupported argument (rank above QLORA_MAX_RANK, dtype, flag, eps, max_norm or overlapping buffers)";
     case QLORA_ERR_WORKSPACE:
       return "workspace missing or too small";
     case QLORA_ERR_HIP:

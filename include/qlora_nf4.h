@@ -81,7 +81,8 @@ typedef enum {
                               /* or, for the linear entry points, k % 64 != 0   */
                               /* or n % 16 != 0                                 */
   QLORA_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned               */
-  QLORA_ERR_UNSUPPORTED = -4, /* r > QLORA_MAX_RANK, unknown dtype or flag      */
+  QLORA_ERR_UNSUPPORTED = -4, /* r > QLORA_MAX_RANK, unknown dtype or flag, or  */
+                              /* what a call says of its own arguments          */
   QLORA_ERR_WORKSPACE = -5,   /* workspace NULL or smaller than required        */
   QLORA_ERR_HIP = -6          /* a kernel launch failed                         */
 } qlora_status;
@@ -484,7 +485,9 @@ qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_
  *           summed in 64 bits in a fixed order, so they do not overflow and
  *           two calls on the same values and lengths agree bit for bit. 0
  *           without elements; NaN or infinity where an element is.
- *   ws    : qlora_grad_workspace_bytes(numel, count) bytes.
+ *   ws    : qlora_grad_workspace_bytes(numel, count) bytes. Calls that may
+ *           overlap need one each, captured ones too; a captured call keeps the
+ *           tensors' addresses.
  * ------------------------------------------------------------------------- */
 
 #define QLORA_MAX_GRADS (1 << 20) /* most tensors in one call */

@@ -227,6 +227,33 @@ def test_linear_bit_exact(gpu_lib, size):
         _same(_f32(y), _round(want, dtype))
 
 
+# Larger sizes, for which each of the tiles is the cheapest; contractions that end
+# in the middle of a unit of 128 codes and leave every remainder of the ring.
+TILES = [(m, n, k) for m, n, ks in (
+    (1604, 5012, (64, 128, 192)), (2317, 3460, (640, 832, 1088, 1216, 1472, 1536)),    # 256 x 256
+    (1282, 3848, (64, 128, 192)), (776, 5012, (832, 960, 1088, 1536)),                 # 128 x 256
+    (592, 4915, (64, 128)), (385, 4721, (192, 320, 832, 960, 1088, 1472, 1536)),       # 128 x 128
+    (201, 4139, (192, 320, 832, 960, 1088, 1536)),                                     # 64 x 128
+    (2064, 65, (64, 128, 832, 1088, 1472, 1536, 2112)), (1650, 259, (960, 1472, 1536)),  # 64 x 64, 32 x 64
+) for k in ks]
+
+
+@pytest.mark.parametrize("size", TILES, ids=lambda s: "x".join(map(str, s)))
+def test_linear_every_tile(gpu_lib, size):
+    import torch
+
+    m, n, k = size
+    say(f"[int8 linear] tiles m={m} n={n} k={k}")
+    w, sw, x, sx = _operands(m, n, k, m + 3 * n + 7 * k)
+    want = OI.linear(w, sw, x, sx)
+    qw, qx = _packed(gpu_lib, w, sw, k), _packed(gpu_lib, x, sx, k)
+    for dtype in ("bfloat16", "float32"):
+        y = torch.full((m, n), 7.0, dtype=_t(dtype), device="cuda")
+        gpu_lib.int8_linear_fwd(qw, qx, _t(dtype), out=y)
+        torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), torch.from_numpy(want).to(_t(dtype)))
+
+
 @pytest.mark.parametrize("m", [1, 16, 70, 300])
 def test_linear_largest_sums(gpu_lib, m):
     """Codes of -128 and 127 alone at the longest k: the sums come within 1.1%
