@@ -648,8 +648,8 @@ def _init():
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
     _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    _torch = torch
     load()
+    _torch = torch  # last: it tells other threads that all of this is there
 
 
 def _launch(fn, index, *args):
