@@ -10,6 +10,7 @@ from __future__ import annotations
 import array
 import ctypes
 import dataclasses
+import operator
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -636,6 +637,7 @@ _torch = None      # the torch module, after _init()
 _DTYPE = None      # torch dtype -> element code of the 16- and 32-bit types
 _raw_stream = None  # device index -> the current stream's handle
 _device_now = None  # the current device's index
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _init():
@@ -823,10 +825,10 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
 
 # ---------------------------------------------------------------- gradients
 class GradList:
-    """Gradients (contiguous tensors of one type on one GPU) checked once, for
-    grad_norm and grad_clip calls of every step on the same buffers. Addresses
-    and lengths are read again at every call; a tensor must keep its type,
-    device and contiguity."""
+    """Gradients (contiguous tensors of one type on one GPU) for grad_norm and
+    grad_clip calls of every step on the same buffers. Each call reads the
+    tensors' addresses again and refuses those whose type, device, length or
+    contiguity is no longer the list's."""
 
     def __init__(self, grads):
         if _torch is None:
@@ -837,27 +839,43 @@ class GradList:
         self.index = grads[0].get_device() if grads else None
         if self.code is None:
             raise TypeError(f"gradients must be bfloat16, float16 or float32, got {self.dtype}")
-        for i, g in enumerate(grads):
-            if g.dtype is not self.dtype:
-                raise TypeError(f"gradient {i} has dtype {g.dtype}, the first {self.dtype}")
-            if g.get_device() != self.index:
-                raise ValueError(f"gradient {i} is on {g.device}, the first on {grads[0].device}")
-            if not g.is_contiguous():
-                raise ValueError(f"gradient {i} must be contiguous")
         self.grads = grads
-        self.sizes = [g.numel() for g in grads]
+        self._check()
+        self.sizes = list(map(_torch.Tensor.numel, grads))
         self.total = sum(self.sizes)
         self._numel = (ctypes.c_int64 * max(len(grads), 1))(*self.sizes)
         self.ws_bytes = int(_LIB.qlora_grad_workspace_bytes(self._numel, len(grads)))
         if self.total and not self.ws_bytes:
             raise ValueError("too many gradients or elements for one call")
 
+    def _check(self):
+        """Raise unless every tensor is as the kernels will read it: a tensor's
+        ``data`` may have been replaced since the last call."""
+        tensor, grads = _torch.Tensor, self.grads
+        if (set(map(_dtype_of, grads)) <= {self.dtype} and set(map(tensor.get_device, grads)) <= {self.index}
+                and all(map(tensor.is_contiguous, grads))):
+            return
+        for i, g in enumerate(grads):
+            if g.dtype is not self.dtype:
+                raise TypeError(f"gradient {i} has dtype {g.dtype}, the list {self.dtype}")
+            if g.get_device() != self.index:
+                raise ValueError(f"gradient {i} is on {g.device}, the list on GPU {self.index}")
+            if not g.is_contiguous():
+                raise ValueError(f"gradient {i} must be contiguous")
+
     def _pointers(self):
         """The addresses as they are now, in an array of 64-bit numbers."""
-        tensor = _torch.Tensor
-        if list(map(tensor.numel, self.grads)) != self.sizes:
-            raise ValueError("a gradient changed its length since the list was made")
-        return array.array("Q", map(tensor.data_ptr, self.grads))
+        return array.array("Q", map(_torch.Tensor.data_ptr, self.grads))
+
+
+def _grad_list(grads):
+    """The GradList of a call, as its tensors are now."""
+    if not isinstance(grads, GradList):
+        return GradList(grads)
+    grads._check()
+    if list(map(_torch.Tensor.numel, grads.grads)) != grads.sizes:
+        raise ValueError("a gradient changed its length since the list was made")
+    return grads
 
 
 def _grad_buffers(g, index, norm, ws):
@@ -877,7 +895,7 @@ def grad_norm(grads, norm=None, ws=None):
     """The norm of all elements of ``grads`` (a list of tensors, or a GradList)
     as one float32 on the GPU (qlora_grad_norm). ``norm`` and ``ws`` (uint8,
     GradList.ws_bytes) may be preallocated."""
-    g = grads if isinstance(grads, GradList) else GradList(grads)
+    g = _grad_list(grads)
     index = g.index if g.grads else _device_now()
     norm, ws = _grad_buffers(g, index, norm, ws)
     at = g._pointers()
@@ -891,7 +909,7 @@ def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
     (norm + 1e-6)), in place, or packed one behind the other into ``out`` (1-D,
     their type and total length). Returns the norm before clipping as one
     float32 on the GPU (qlora_grad_clip)."""
-    g = grads if isinstance(grads, GradList) else GradList(grads)
+    g = _grad_list(grads)
     index = g.index if g.grads else _device_now()
     op = None
     if out is not None and g.grads:
