@@ -769,7 +769,8 @@ def rmsnorm_int8(x, gain, eps: float = 1e-6, residual=None, residual_out=None, o
     same, or None; gain: (cols,) of x's type or float32. Returns (PackedInt8,
     h in x's type, or None without a residual). ``residual_out`` may be
     preallocated, or be ``residual`` or ``x`` itself (in place); ``out`` may be
-    a PackedInt8 of x's sizes."""
+    a PackedInt8 of x's sizes. Outputs that overlap the inputs or each other in
+    any other way are refused."""
     code, n, k, index = _need_rows(x, "x")
     dtype = x.dtype
     gain_code = code if gain.dtype is dtype else QLORA_F32

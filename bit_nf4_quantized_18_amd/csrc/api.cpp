@@ -656,6 +656,18 @@ qlora_status qlora_linear_bwd_f16(const qlora_nf4_weight* w, const uint16_t* x, 
 // 8-bit rows and their product
 // ---------------------------------------------------------------------------
 static bool known_dtype(int t) { return t == QLORA_BF16 || t == QLORA_F32 || t == QLORA_F16; }
+static int dtype_bytes(int t) { return t == QLORA_F32 ? 4 : 2; }
+
+// A buffer's addresses. A workgroup may write its part of an output before
+// another has read the inputs, so calls refuse outputs that meet them.
+struct Span {
+  uintptr_t at, end;
+};
+static Span span(const void* p, int64_t bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return Span{at, p == nullptr ? at : at + static_cast<uintptr_t>(bytes)};
+}
+static bool meet(Span a, Span b) { return a.at < b.end && b.at < a.end; }
 
 static bool int8_rows_ok(int64_t rows, int64_t cols, int64_t ld) {
   return rows >= 0 && rows < (INT64_C(1) << 31) && cols >= 1 && ld >= cols && ld % 64 == 0 &&
@@ -669,6 +681,8 @@ qlora_status qlora_int8_quantize(const void* x, int dtype, int64_t rows, int64_t
   if (rows == 0) return QLORA_OK;
   if (x == nullptr || codes == nullptr || scale == nullptr) return QLORA_ERR_NULL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return QLORA_ERR_ALIGN;
+  const Span xs = span(x, rows * cols * dtype_bytes(dtype)), cs = span(codes, rows * ld), ss = span(scale, rows * 4);
+  if (meet(cs, xs) || meet(ss, xs) || meet(cs, ss)) return QLORA_ERR_UNSUPPORTED;
   return hip_status(qlora::launch_int8_quantize(x, dtype, rows, cols, codes, ld, scale, stream));
 }
 
@@ -679,6 +693,8 @@ qlora_status qlora_int8_dequantize(const int8_t* codes, int64_t ld, const float*
   if (rows == 0) return QLORA_OK;
   if (codes == nullptr || scale == nullptr || out == nullptr) return QLORA_ERR_NULL;
   if (!aligned16(codes) || !aligned16(scale) || !aligned16(out)) return QLORA_ERR_ALIGN;
+  const Span os = span(out, rows * cols * dtype_bytes(dtype));
+  if (meet(os, span(codes, rows * ld)) || meet(os, span(scale, rows * 4))) return QLORA_ERR_UNSUPPORTED;
   return hip_status(qlora::launch_int8_dequantize(codes, ld, scale, rows, cols, dtype, out, stream));
 }
 
@@ -695,6 +711,15 @@ qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void*
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(residual_out) || !aligned16(codes) ||
       !aligned16(scale))
     return QLORA_ERR_ALIGN;
+  const int64_t bytes = rows * cols * dtype_bytes(dtype);
+  const Span in[3] = {span(x, bytes), span(residual, bytes), span(gain, cols * dtype_bytes(gain_dtype))};
+  const Span hs = span(residual_out, bytes), cs = span(codes, rows * ld), ss = span(scale, rows * 4);
+  if (meet(cs, ss) || meet(cs, hs) || meet(ss, hs)) return QLORA_ERR_UNSUPPORTED;
+  for (const Span& i : in)
+    if (meet(cs, i) || meet(ss, i)) return QLORA_ERR_UNSUPPORTED;
+  // h may take the place of x or of the residual, element for element
+  if ((meet(hs, in[0]) && hs.at != in[0].at) || (meet(hs, in[1]) && hs.at != in[1].at) || meet(hs, in[2]))
+    return QLORA_ERR_UNSUPPORTED;
   return hip_status(qlora::launch_rmsnorm_int8(x, residual, gain, dtype, gain_dtype == QLORA_F32, rows, cols, eps,
                                                residual_out, codes, ld, scale, stream));
 }
@@ -718,8 +743,6 @@ qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_
 // ---------------------------------------------------------------------------
 // Gradient norm and clipping
 // ---------------------------------------------------------------------------
-static int dtype_bytes(int t) { return t == QLORA_F32 ? 4 : 2; }
-
 // The lengths are in range; *total is their sum.
 static bool grad_sizes_ok(const int64_t* numel, int count, int64_t* total) {
   if (count < 0 || count > QLORA_MAX_GRADS || (count > 0 && numel == nullptr)) return false;

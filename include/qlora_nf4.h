@@ -427,7 +427,8 @@ qlora_status qlora_requantize(const qlora_nf4_weight* w, const uint16_t* a, cons
  *   codes   : rows x ld int8, written whole (zeros behind the cols values).
  *   scale   : rows float32.
  *   rows 0 .. 2^31 - 1 (0: nothing is done); cols >= 1.
- * Bit-exact with the CPU oracle. Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtype) / HIP. */
+ * Bit-exact with the CPU oracle. Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtype, or buffers
+ * that overlap each other) / HIP. */
 qlora_status qlora_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes,
                                  int64_t ld, float* scale, hipStream_t stream);
 
@@ -450,9 +451,10 @@ qlora_status qlora_int8_dequantize(const int8_t* codes, int64_t ld, const float*
  *   eps         : finite, >= 0.
  *   residual_out: rows x cols of `dtype`, h rounded to nearest even; required
  *                 with a residual, ignored without. May be `residual` or `x`
- *                 itself (in place).
+ *                 itself (in place); no other overlap of an output with an
+ *                 input or another output is taken.
  *   codes, ld, scale: the 8-bit rows written.
- * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtypes, eps) / HIP. */
+ * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtypes, eps, overlapping buffers) / HIP. */
 qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void* gain, int dtype,
                                 int gain_dtype, int64_t rows, int64_t cols, float eps,
                                 void* residual_out, int8_t* codes, int64_t ld, float* scale,

@@ -1,0 +1,53 @@
+"""Buffers of the 8-bit row calls that touch without overlapping: results are
+those on buffers of their own, bit for bit."""
+import pytest
+
+from gpu_cases import say
+
+pytestmark = pytest.mark.gpu
+
+
+def test_rows_in_one_allocation(gpu_lib):
+    import torch
+
+    rows, cols, ld = 40, 96, 128
+    say("[int8] neighbouring buffers")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device="cuda").bfloat16()
+    r = torch.randn(rows, cols, generator=g, device="cuda").bfloat16()
+    gain = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    want, h = gpu_lib.rmsnorm_int8(x, gain, residual=r)
+    want_q = gpu_lib.quantize_int8(x)
+    want_v = gpu_lib.dequantize_int8(want_q)
+
+    pool = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    at = 0
+
+    def take(shape, dtype):
+        nonlocal at
+        n = torch.Size(shape).numel() * dtype.itemsize
+        t = pool[at:at + n].view(dtype).view(shape)
+        at += n
+        assert at % 16 == 0 and at <= pool.numel()
+        return t
+
+    # x | codes | h | scale | residual | gain | values, each behind the last
+    px, codes, ph = take((rows, cols), x.dtype), take((rows, ld), torch.int8), take((rows, cols), x.dtype)
+    scale, pr, pg = take((rows,), torch.float32), take((rows, cols), x.dtype), take((cols,), x.dtype)
+    pv = take((rows, cols), x.dtype)
+    px.copy_(x), pr.copy_(r), pg.copy_(gain)
+    out = gpu_lib.PackedInt8(rows, cols, codes, scale)
+    gpu_lib.rmsnorm_int8(px, pg, residual=pr, residual_out=ph, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(codes, want.codes) and torch.equal(scale, want.scale) and torch.equal(ph, h)
+    gpu_lib.quantize_int8(px, out=out)
+    gpu_lib.dequantize_int8(out, out=pv)
+    torch.cuda.synchronize()
+    assert torch.equal(codes, want_q.codes) and torch.equal(scale, want_q.scale) and torch.equal(pv, want_v)
+    # in place: h over the residual, and over x
+    for into in (pr, px):
+        keep = into.clone()
+        gpu_lib.rmsnorm_int8(px, pg, residual=pr, residual_out=into, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(into, h) and torch.equal(codes, want.codes) and torch.equal(scale, want.scale)
+        into.copy_(keep)
