@@ -667,7 +667,9 @@ static Span span(const void* p, int64_t bytes) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
   return Span{at, p == nullptr ? at : at + static_cast<uintptr_t>(bytes)};
 }
-static bool meet(Span a, Span b) { return a.at < b.end && b.at < a.end; }
+static bool meet(Span a, Span b) {  // an empty buffer meets nothing
+  return (a.at > b.at ? a.at : b.at) < (a.end < b.end ? a.end : b.end);
+}
 
 static bool int8_rows_ok(int64_t rows, int64_t cols, int64_t ld) {
   return rows >= 0 && rows < (INT64_C(1) << 31) && cols >= 1 && ld >= cols && ld % 64 == 0 &&
@@ -758,7 +760,7 @@ static bool grad_sizes_ok(const int64_t* numel, int count, int64_t* total) {
 }
 
 static qlora_status check_grads(const void* const* grads, const int64_t* numel, int count, int dtype, const float* norm,
-                                const void* ws, size_t ws_bytes, int64_t* total) {
+                                const void* ws, size_t ws_bytes, int64_t* total, size_t* need) {
   if (!known_dtype(dtype)) return QLORA_ERR_UNSUPPORTED;
   if (count > 0 && (grads == nullptr || numel == nullptr)) return QLORA_ERR_NULL;
   if (!grad_sizes_ok(numel, count, total)) return QLORA_ERR_SHAPE;
@@ -770,10 +772,25 @@ static qlora_status check_grads(const void* const* grads, const int64_t* numel, 
     if (grads[i] == nullptr) return QLORA_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(grads[i]) & mask) != 0) return QLORA_ERR_ALIGN;
   }
-  const size_t need = qlora::grad_ws_bytes(numel, count);
-  if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+  *need = qlora::grad_ws_bytes(numel, count);
+  if (*need > 0 && (ws == nullptr || ws_bytes < *need)) return QLORA_ERR_WORKSPACE;
   if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
   return QLORA_OK;
+}
+
+// The norm and the workspace (its `need` bytes that the kernels use) are apart
+// from each other and from the tensors: the first kernel writes the workspace
+// while it reads these, and one workgroup of the second writes the norm while
+// others still read both.
+static bool grad_outputs_apart(const void* const* grads, const int64_t* numel, int count, int dtype, const float* norm,
+                               const void* ws, size_t need) {
+  const Span ns = span(norm, 4), wss = span(ws, static_cast<int64_t>(need));
+  if (meet(ns, wss)) return false;
+  for (int i = 0; i < count; ++i) {
+    const Span g = span(grads[i], numel[i] * dtype_bytes(dtype));
+    if (meet(g, ns) || meet(g, wss)) return false;
+  }
+  return true;
 }
 
 size_t qlora_grad_workspace_bytes(const int64_t* numel, int count) {
@@ -784,8 +801,10 @@ size_t qlora_grad_workspace_bytes(const int64_t* numel, int count) {
 qlora_status qlora_grad_norm(const void* const* grads, const int64_t* numel, int count, int dtype, float* norm,
                              void* ws, size_t ws_bytes, hipStream_t stream) {
   int64_t total = 0;
-  const qlora_status st = check_grads(grads, numel, count, dtype, norm, ws, ws_bytes, &total);
+  size_t need = 0;
+  const qlora_status st = check_grads(grads, numel, count, dtype, norm, ws, ws_bytes, &total, &need);
   if (st != QLORA_OK) return st;
+  if (!grad_outputs_apart(grads, numel, count, dtype, norm, ws, need)) return QLORA_ERR_UNSUPPORTED;
   return hip_status(qlora::launch_grad_clip(grads, numel, count, dtype, false, 0.0f, nullptr, norm, ws, stream));
 }
 
@@ -793,34 +812,30 @@ qlora_status qlora_grad_clip(void* const* grads, const int64_t* numel, int count
                              float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!(max_norm >= 0.0f)) return QLORA_ERR_UNSUPPORTED;  // NaN fails the test
   int64_t total = 0;
-  const qlora_status st = check_grads(grads, numel, count, dtype, norm, ws, ws_bytes, &total);
+  size_t need = 0;
+  const qlora_status st = check_grads(grads, numel, count, dtype, norm, ws, ws_bytes, &total, &need);
   if (st != QLORA_OK) return st;
-  const uintptr_t size = static_cast<uintptr_t>(dtype_bytes(dtype));
+  const int64_t size = dtype_bytes(dtype);
   if (out != nullptr) {
-    const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), o1 = o0 + static_cast<uintptr_t>(total) * size;
-    if ((o0 & (size - 1)) != 0) return QLORA_ERR_ALIGN;
-    for (int i = 0; i < count; ++i) {
-      const uintptr_t g0 = reinterpret_cast<uintptr_t>(grads[i]), g1 = g0 + static_cast<uintptr_t>(numel[i]) * size;
-      if (numel[i] > 0 && g0 < o1 && o0 < g1) return QLORA_ERR_UNSUPPORTED;
-    }
+    if (reinterpret_cast<uintptr_t>(out) % static_cast<uintptr_t>(size) != 0) return QLORA_ERR_ALIGN;
+    const Span os = span(out, total * size);
+    if (meet(os, span(norm, 4)) || meet(os, span(ws, static_cast<int64_t>(need)))) return QLORA_ERR_UNSUPPORTED;
+    for (int i = 0; i < count; ++i)
+      if (meet(os, span(grads[i], numel[i] * size))) return QLORA_ERR_UNSUPPORTED;
   } else if (count > 1) {
     // in place: two tensors on the same memory would be scaled twice, in a race
-    struct Range {
-      uintptr_t at, end;
-    };
-    Range* r = new (std::nothrow) Range[static_cast<size_t>(count)];
+    Span* r = new (std::nothrow) Span[static_cast<size_t>(count)];
     if (r == nullptr) return QLORA_ERR_WORKSPACE;
     int used = 0;
-    for (int i = 0; i < count; ++i) {
-      const uintptr_t g0 = reinterpret_cast<uintptr_t>(grads[i]);
-      if (numel[i] > 0) r[used++] = Range{g0, g0 + static_cast<uintptr_t>(numel[i]) * size};
-    }
-    std::sort(r, r + used, [](const Range& a, const Range& b) { return a.at < b.at; });
+    for (int i = 0; i < count; ++i)
+      if (numel[i] > 0) r[used++] = span(grads[i], numel[i] * size);
+    std::sort(r, r + used, [](const Span& a, const Span& b) { return a.at < b.at; });
     bool apart = true;
     for (int i = 1; i < used; ++i) apart = apart && r[i - 1].end <= r[i].at;
     delete[] r;
     if (!apart) return QLORA_ERR_UNSUPPORTED;
   }
+  if (!grad_outputs_apart(grads, numel, count, dtype, norm, ws, need)) return QLORA_ERR_UNSUPPORTED;
   return hip_status(qlora::launch_grad_clip(const_cast<const void* const*>(grads), numel, count, dtype, true, max_norm,
                                             out, norm, ws, stream));
 }

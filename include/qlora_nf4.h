@@ -490,12 +490,14 @@ qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_
  *   ws    : qlora_grad_workspace_bytes(numel, count) bytes. Calls that may
  *           overlap need one each, captured ones too; a captured call keeps the
  *           tensors' addresses.
+ * norm and ws overlap neither each other nor a tensor or the output
+ * (QLORA_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 
 #define QLORA_MAX_GRADS (1 << 20) /* most tensors in one call */
 
 /* Errors: NULL / ALIGN / SHAPE (count or a length out of range) / UNSUPPORTED
- * (dtype) / WORKSPACE / HIP. */
+ * (dtype, overlapping buffers) / WORKSPACE / HIP. */
 qlora_status qlora_grad_norm(const void* const* grads, const int64_t* numel, int count, int dtype,
                              float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
 

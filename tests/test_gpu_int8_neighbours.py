@@ -51,3 +51,34 @@ def test_rows_in_one_allocation(gpu_lib):
         torch.cuda.synchronize()
         assert torch.equal(into, h) and torch.equal(codes, want.codes) and torch.equal(scale, want.scale)
         into.copy_(keep)
+
+
+def test_gradients_norm_and_workspace_in_one_allocation(gpu_lib):
+    """gradient | norm | workspace | gradient, an empty tensor's address among
+    them; then a workspace larger than needed whose end holds the norm."""
+    import torch
+
+    say("[grad clip] neighbouring buffers")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    host = [torch.randn(n, generator=gen, device="cuda") for n in (100, 5000)]
+    want = torch.empty(5100, device="cuda")
+    norm = gpu_lib.grad_clip(host, 0.5, out=want)
+    need = gpu_lib.GradList(host).ws_bytes
+    assert need % 16 == 0
+    pool = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    a = pool[:400].view(torch.float32)
+    pn = pool[400:404].view(torch.float32)
+    ws = pool[416:416 + need]
+    b = pool[416 + need:416 + need + 20000].view(torch.float32)
+    inside = ws[8:8].view(torch.float32)
+    a.copy_(host[0]), b.copy_(host[1])
+    assert gpu_lib.grad_norm([a, inside, b], norm=pn, ws=ws) is pn
+    torch.cuda.synchronize()
+    assert torch.equal(pn[0], norm)
+    pn.zero_()
+    gpu_lib.grad_clip([a, inside, b], 0.5, norm=pn, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(pn[0], norm) and torch.equal(torch.cat([a, b]), want)
+    long = torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
+    tail = long[need:need + 4].view(torch.float32)
+    assert torch.equal(gpu_lib.grad_norm(host, norm=tail, ws=long)[0], norm)
