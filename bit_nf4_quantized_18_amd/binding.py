@@ -802,10 +802,16 @@ def _need_like(t, name, x, index):
         raise ValueError(f"{name} must be contiguous, of shape {tuple(x.shape)} on x's device")
 
 
+def _overlap(s, t):
+    """Two contiguous tensors share memory."""
+    a, b = s.data_ptr(), t.data_ptr()
+    return max(a, b) < min(a + s.nbytes, b + t.nbytes)
+
+
 def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
     """Y = X W^T of 8-bit rows: q the weight by channel (n, k), x the input by
     token (m, k). Returns (m, n) of ``dtype`` (bf16, fp16 or float32; bf16 by
-    default). ``out`` may be preallocated."""
+    default). ``out`` may be preallocated; over the operands it is refused."""
     dtype, code = _out_dtype(dtype)
     codes = q.codes
     index = codes.get_device()
@@ -819,6 +825,10 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
         out = codes.new_empty(m, n, dtype=dtype)
     else:
         _need(out, "out", (m, n), (dtype,), codes.device)
+        for name, t in (("the weight's codes", codes), ("the weight's scale", q.scale), ("x's codes", x.codes),
+                        ("x's scale", x.scale)):
+            if _overlap(out, t):
+                raise ValueError(f"out overlaps {name}")
     _launch(_LIB.qlora_int8_linear_fwd, index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
             x.scale.data_ptr(), m, code, out.data_ptr())
     return out

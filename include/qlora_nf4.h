@@ -469,7 +469,8 @@ qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void*
  *                row length ld of both: k % 64 == 0, 64 .. QLORA_INT8_MAX_K.
  *   n          : 1 .. 2^22; m 0 .. 2^31 - 1 (0: nothing is done);
  *                ceil(m / 256) ceil(n / 256) < 2^23.
- *   out_dtype  : QLORA_BF16, QLORA_F16 or QLORA_F32; y is m x n.
+ *   out_dtype  : QLORA_BF16, QLORA_F16 or QLORA_F32; y is m x n and overlaps
+ *                none of the inputs (not checked here; the binding does).
  * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (out_dtype) / HIP. */
 qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_t n, int64_t k,
                                    const int8_t* x, const float* x_scale, int64_t m, int out_dtype,

@@ -1,6 +1,7 @@
 """The gradient calls refuse a norm or a workspace that overlaps the gradients,
-the output or each other (no GPU: fake addresses). The norm is written while other workgroups still read partial sums
-and gradients, the workspace while the gradients are read."""
+the output or each other (no GPU: fake addresses). The norm is written while
+other workgroups still read partial sums and gradients, the workspace while the
+gradients are read."""
 import ctypes
 
 import pytest

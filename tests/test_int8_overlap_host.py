@@ -58,3 +58,26 @@ def test_rmsnorm(t, gt):
     assert all(f(scale=a) == -4 for a in _around(CODES, ROWS * LD, ROWS * 4))
     # without a residual h is not written, its address does not count
     assert f(res=None, out=None, codes=X) == -4 and f(res=None, out=X, scale=GAIN) == -4
+
+
+@pytest.mark.parametrize("over", ["w_codes", "w_scale", "x_codes", "x_scale"])
+def test_product_output(over):
+    """The binding refuses an output over the operands (CPU tensors: an output
+    behind them is refused for these, later)."""
+    import torch
+
+    m, n, k = 8, 64, 64
+    pool = torch.zeros(1 << 16, dtype=torch.uint8)
+    at = {"w_codes": (0, n * k), "w_scale": (8192, n * 4), "x_codes": (16384, m * k), "x_scale": (24576, m * 4)}
+    part = {name: pool[a:a + b] for name, (a, b) in at.items()}
+    w = B.PackedInt8(n, k, part["w_codes"].view(torch.int8).view(n, k), part["w_scale"].view(torch.float32))
+    x = B.PackedInt8(m, k, part["x_codes"].view(torch.int8).view(m, k), part["x_scale"].view(torch.float32))
+    a, b = at[over]
+    size = m * n * 2
+    name = {"w": "the weight's ", "x": "x's "}[over[0]] + over[2:]
+    place = lambda i: pool[i:i + size].view(torch.bfloat16).view(m, n)  # noqa: E731
+    for i in [a, a + b - 16] + ([a - size + 16] if a >= size else []):
+        with pytest.raises(ValueError, match="out overlaps " + name):
+            B.int8_linear_fwd(w, x, out=place(i))
+    with pytest.raises(ValueError, match="on the GPU"):
+        B.int8_linear_fwd(w, x, out=place(a + b))
