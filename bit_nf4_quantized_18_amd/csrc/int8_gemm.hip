@@ -19,6 +19,7 @@
 //     the cycles are as many, at 1.64 GHz: 236 us.
 #include "bufmem.h"
 #include "elem.h"
+#include "int8_tiles.h"
 
 namespace qlora {
 namespace {
@@ -321,13 +322,15 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   }
 }
 
-template <int BM, int BN, int WM, int WN, int KS, int P>
+template <int I>
 hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
+  constexpr Shape t = kShapes[I];
+  constexpr int BM = t.bm, BN = t.bn, WM = t.wm, WN = t.wn, KS = t.groups, P = t.parts;
   const int tiles_m = static_cast<int>((g.m + BM - 1) / BM), tiles_n = static_cast<int>((g.n + BN - 1) / BN);
   auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F32>
               : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F16>
                                        : tile_kernel<BM, BN, WM, WN, KS, P, QLORA_BF16>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(64 * WM * WN * KS), 0, s, g, tiles_m, tiles_n);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(t.threads()), 0, s, g, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -342,8 +345,6 @@ hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
 // once for 64 channels, not for 16: 16 tokens, 11008 x 4096: 13.8 us here,
 // 11.0 us there; 8192 x 8192: 17.5 and 14.0 us; 4096 x 4096: 7.1 and 7.7 us.
 // ---------------------------------------------------------------------------
-constexpr int kDecodeTokens = 16;
-constexpr int kDecodeMaxN = 8191;
 constexpr int kDecodeWaves = 8;
 constexpr int kDecodeSteps = 4;  // 64-code steps of a wave a pass
 
@@ -395,83 +396,22 @@ hipError_t launch_decode(const LinearArgs& g, int out_dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool decodes(int64_t m, int64_t n) { return m <= kDecodeTokens && n <= kDecodeMaxN; }
-
-// ---------------------------------------------------------------------------
-// The tile for a call: the one with the least kLaunch + rounds * (round + units *
-// unit) microseconds, where rounds counts turns of the 256 CUs, units steps of
-// 128 codes, `round` a tile's start and its outputs. Fitted to measured times
-// (graph replays, bf16 out). Over 48 sizes drawn from 1 .. 4096 tokens, 64 ..
-// 22016 channels and 64 .. 11008 codes its choice takes 1.4% longer on average
-// than the best tile for each. Some of the times behind it (m x n x k, us):
-//   4096 x 8192 x 8192:  256 x 256 206, 128 x 256 238, 128 x 128 317
-//   2048 x 4096 x 11008: 128 x 256 76, 128 x 128 92, 256 x 256 102
-//   2048 x 11008 x 4096: 128 x 256 90, 256 x 256 104, 128 x 128 119
-//   512 x 4096 x 4096:   64 x 128 14.8, 64 x 64 17.6, 128 x 128 19.0
-//   128 x 4096 x 4096:   32 x 64 8.6, 64 x 64 10.8, 64 x 128 12.5
-//   64 x 11008 x 4096:   64 x 64 11.3, 64 x 128 13.5, 32 x 64 15.9
-//   32 x 4096 x 11008:   16 x 64 14.4, 32 x 64 17.1
-//   745 x 21599 x 147:   256 x 256 22, 128 x 256 24, 64 x 64 34, 16 x 64 96
-// ---------------------------------------------------------------------------
-struct Shape {
-  int bm, bn, threads;
-  double round, unit;
-};
-constexpr Shape kShapes[] = {{256, 256, 512, 12, 1.4},  {128, 256, 512, 8, 0.78},   {128, 128, 256, 4.5, 0.5},
-                             {64, 128, 256, 3, 0.34},   {64, 64, 256, 1.4, 0.22},   {32, 64, 256, 2.2, 0.14},
-                             {16, 64, 128, 1.2, 0.13}};
-constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
-constexpr double kLaunch = 2;
-
-int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn); }
-
-double cost(const Shape& s, int64_t tiles, int64_t k) {
-  return kLaunch + static_cast<double>((tiles + 255) / 256) * (s.round + static_cast<double>((k + 127) / 128) * s.unit);
-}
-
-struct Pick {
-  int shape;  // into kShapes; -1: no tile's grid stays below 2^32 work items
-  double us;
-};
-Pick pick_shape(int64_t m, int64_t n, int64_t k) {
-  Pick best{-1, 0};
-  for (int i = 0; i < kNumShapes; ++i) {
-    const int64_t tiles = tiles_of(kShapes[i], m, n);
-    if (tiles >= (INT64_C(1) << 32) / kShapes[i].threads) continue;
-    const double us = cost(kShapes[i], tiles, k);
-    if (best.shape < 0 || us < best.us) best = Pick{i, us};
-  }
-  return best;
-}
-
-// Channels of a first launch in 256 x 256 tiles whose rounds are full, where
-// these and a second launch for the other channels cost less than one launch;
-// 0 where they do not. 4096 x 22016 x 8192 has 1376 tiles, 5.4 rounds: 574 us
-// in one launch, 551 us as five full rounds and 192 tiles of 128 x 256.
-int64_t full_rounds(int64_t m, int64_t n, int64_t k, const Pick& one) {
-  const int64_t tiles_m = (m + 255) / 256, tiles = tiles_of(kShapes[0], m, n);
-  if (one.shape != 0 || tiles_m > 256 || tiles % 256 == 0) return 0;
-  const int64_t cols = tiles / 256 * 256 / tiles_m * 256;
-  if (cols < 256 || cols >= n) return 0;
-  return cost(kShapes[0], tiles_of(kShapes[0], m, cols), k) + pick_shape(m, n - cols, k).us < one.us ? cols : 0;
-}
-
 hipError_t launch_shape(int shape, const LinearArgs& g, int out_dtype, hipStream_t s) {
   switch (shape) {
     case 0:
-      return launch_tiles<256, 256, 2, 4, 1, 5>(g, out_dtype, s);
+      return launch_tiles<0>(g, out_dtype, s);
     case 1:
-      return launch_tiles<128, 256, 2, 4, 1, 6>(g, out_dtype, s);
+      return launch_tiles<1>(g, out_dtype, s);
     case 2:
-      return launch_tiles<128, 128, 2, 2, 1, 8>(g, out_dtype, s);
+      return launch_tiles<2>(g, out_dtype, s);
     case 3:
-      return launch_tiles<64, 128, 2, 2, 1, 8>(g, out_dtype, s);
+      return launch_tiles<3>(g, out_dtype, s);
     case 4:
-      return launch_tiles<64, 64, 4, 1, 1, 8>(g, out_dtype, s);
+      return launch_tiles<4>(g, out_dtype, s);
     case 5:
-      return launch_tiles<32, 64, 2, 1, 2, 8>(g, out_dtype, s);
+      return launch_tiles<5>(g, out_dtype, s);
     case 6:
-      return launch_tiles<16, 64, 1, 1, 2, 8>(g, out_dtype, s);
+      return launch_tiles<6>(g, out_dtype, s);
   }
   return hipErrorInvalidValue;  // int8_linear_fits refuses these sizes
 }
