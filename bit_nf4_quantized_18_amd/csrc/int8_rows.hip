@@ -42,8 +42,9 @@ struct Top {
 // fl32(127 / a). t = v inv is within 127 2^-23 < 2^-15 of 127 v / a, so it
 // rounds as that does unless it lies nearer than 2^-14 to a tie. There (and in
 // rows so small that 127 / a leaves the normal range) the quotient in 64 bits
-// decides: 127 v is exact, and a quotient that is no tie differs from one by
-// 2^-26 at least, far over the division's rounding. Adding 1.5 2^23 rounds to
+// decides: 127 v is exact, and with v / a = 2^e V / A (V, A whole, below 2^24) a
+// quotient q that is no tie differs from one by a whole number over 2 A 2^-e,
+// q / (254 V) > q 2^-32 at least, far over the division's rounding q 2^-53. Adding 1.5 2^23 rounds to
 // the nearest integer, ties to even, and leaves the code in the low byte.
 __device__ __forceinline__ u32x2 encode8(const float* v, float a, float inv) {
   constexpr float kRound = 12582912.0f;
