@@ -918,8 +918,9 @@ def grad_norm(grads, norm=None, ws=None):
 def grad_clip(grads, max_norm: float, out=None, norm=None, ws=None):
     """Scale ``grads`` (a list of tensors, or a GradList) by min(1, max_norm /
     (norm + 1e-6)), in place, or packed one behind the other into ``out`` (1-D,
-    their type and total length). Returns the norm before clipping as one
-    float32 on the GPU (qlora_grad_clip)."""
+    their type and total length). An infinite max_norm scales nothing, NaN and
+    infinite norms included. Returns the norm before clipping as one float32 on
+    the GPU (qlora_grad_clip)."""
     g = _grad_list(grads)
     index = g.index if g.grads else _device_now()
     op = None

@@ -504,10 +504,11 @@ qlora_status qlora_grad_norm(const void* const* grads, const int64_t* numel, int
 
 /* norm as qlora_grad_norm, then every element times min(1, max_norm / (norm +
  * 1e-6)), that factor computed in 64 bits and rounded once to float32, the
- * product rounded to nearest even into `dtype`. A NaN norm makes every element
- * NaN; an infinite norm gives the factor 0 (elements that are infinite become
- * NaN).
- *   max_norm : >= 0 (infinity: nothing is scaled).
+ * product rounded to nearest even into `dtype`. With a finite max_norm a NaN
+ * norm makes every element NaN, and an infinite norm gives the factor 0
+ * (elements that are infinite become NaN).
+ *   max_norm : >= 0. Infinity scales nothing, whatever the norm is: elements
+ *              keep their values also where the norm is NaN or infinite.
  *   out      : NULL writes in place; otherwise one buffer of the tensors'
  *              total length that takes them packed one behind the other in
  *              list order (`dtype`, aligned to the element size).

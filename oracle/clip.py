@@ -13,7 +13,7 @@ def norm(grads):
 
 
 def factor(total, max_norm):
-    """fl32(min(1, max_norm / (norm + 1e-6))); 1 for an infinite max_norm."""
+    """fl32(min(1, max_norm / (norm + 1e-6))); 1 for an infinite max_norm, whatever the norm."""
     if math.isinf(max_norm):
         return np.float32(1.0)
     if math.isnan(total):
