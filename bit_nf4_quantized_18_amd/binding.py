@@ -671,7 +671,10 @@ def _launch(fn, index, *args):
 @dataclasses.dataclass
 class PackedInt8:
     """8-bit rows on the device: n rows of k values, value = code * scale of
-    its row. Rows of codes are padded with zeros to a multiple of 64."""
+    its row. Rows of codes are padded with zeros to a multiple of 64. As every
+    buffer of the library both start at a multiple of 16 bytes: a view of some
+    rows is taken where its first row's number is a multiple of 4, and needs
+    ``scale[i:].clone()`` elsewhere (QLORA_ERR_ALIGN)."""
     n: int
     k: int
     codes: "object"  # int8 [n, ld], ld % 64 == 0, ld >= k, zeros behind the k codes

@@ -164,7 +164,7 @@ const char* qlora_status_string(int status) {
     case QLORA_ERR_SHAPE:
       return "invalid size (negative, zero, too large, k not a multiple of 64 or n not a multiple of 16)";
     case QLORA_ERR_ALIGN:
-      return "a pointer is not 16-byte aligned";
+      return "a pointer is not aligned as the call requires (16 bytes; gradients to their element size, norm to 4)";
     case QLORA_ERR_UNSUPPORTED:
       return "unsupported argument (rank above QLORA_MAX_RANK, dtype, flag, eps, max_norm or overlapping buffers)";
     case QLORA_ERR_WORKSPACE:

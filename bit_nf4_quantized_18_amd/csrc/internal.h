@@ -209,7 +209,7 @@ hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, 
                               const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s);
 
 // Global norm of a list of tensors and (clip) their scaling: out null writes
-// in place. total is the sum of numel; ws holds grad_ws_bytes(numel, count).
+// in place. ws holds grad_ws_bytes(numel, count).
 size_t grad_ws_bytes(const int64_t* numel, int count);
 hipError_t launch_grad_clip(const void* const* grads, const int64_t* numel, int count, int dtype, bool clip,
                             float max_norm, void* out, float* norm, void* ws, hipStream_t s);

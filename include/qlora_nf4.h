@@ -80,7 +80,8 @@ typedef enum {
   QLORA_ERR_SHAPE = -2,       /* a size is negative / zero where not allowed,   */
                               /* or, for the linear entry points, k % 64 != 0   */
                               /* or n % 16 != 0                                 */
-  QLORA_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned               */
+  QLORA_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned (gradients:   */
+                              /* to their element size, their norm: to 4 bytes) */
   QLORA_ERR_UNSUPPORTED = -4, /* r > QLORA_MAX_RANK, unknown dtype or flag, or  */
                               /* what a call says of its own arguments          */
   QLORA_ERR_WORKSPACE = -5,   /* workspace NULL or smaller than required        */

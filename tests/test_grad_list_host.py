@@ -47,3 +47,9 @@ def test_new_data_of_the_same_kind_is_taken():
     assert list(held._pointers()) == [g.data_ptr() for g in grads]
     with pytest.raises(ValueError, match="on the GPU"):
         B.grad_norm(held)
+
+
+def test_status_text_of_alignment():
+    """The gradient calls refuse by element size, not by 16 bytes."""
+    text = B.status_string(-3)
+    assert "16 bytes" in text and "element size" in text
