@@ -13,7 +13,9 @@
 // takes all records of all launches: every workgroup forms the norm from the
 // partial sums in the same order, then scales its chunks. 448 tensors of 40 M
 // float32 in all: 40 us for the norm (two launches, 4.0 TB/s), 67 us more for the
-// scaling into a second buffer (320 MB, 4.8 TB/s, a large copy's rate).
+// scaling into a second buffer (320 MB, 4.8 TB/s, a large copy's rate). Replayed
+// on one set of tensors, whose 160 MB partly stay in the 256 MB cache: 35 us the
+// norm, 86 us with the scaling, 84 us in place.
 #include "elem.h"
 
 namespace qlora {

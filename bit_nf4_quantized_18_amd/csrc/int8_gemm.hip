@@ -5,8 +5,8 @@
 // of the work; the scales enter once, at the end.
 //
 // What bounds it, by size (MI355X; graph replays, bf16 out):
-//   - Few tokens: the weight's bytes. 1 x 4096 x 4096 (m x n x k) 5.8 us, 16 x
-//     11008 x 4096 10.7 us (45 MB; a large copy moves 4.7 TB/s here, read and
+//   - Few tokens: the weight's bytes. 1 x 4096 x 4096 (m x n x k) 5.5 us, 16 x
+//     11008 x 4096 10.8 us (45 MB; a large copy moves 4.7 TB/s here, read and
 //     written).
 //   - Hundreds of tokens: the copies into LDS. 333 x 5003 x 4160 takes 17.6 us in
 //     64 x 128 tiles, 16.5 us with reads and products left out, 6.0 us with the
@@ -339,11 +339,18 @@ hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
 // memory. A workgroup takes 16 channels (so 4096 channels fill the 256 CUs);
 // its waves split the contraction, read their runs of the 16 rows straight
 // into registers, and add their integer sums through LDS.
-// One token, 4096 x 4096: 5.8 us (graph replays; 4.3 TB/s behind a launch's
-// 2 us); 4 to 16 waves and 2 to 8 loads in flight measure alike. From 8192
-// channels on the 16 x 64 tiles above fill half the CUs and read the tokens
-// once for 64 channels, not for 16: 16 tokens, 11008 x 4096: 13.8 us here,
-// 11.0 us there; 8192 x 8192: 17.5 and 14.0 us; 4096 x 4096: 7.1 and 7.7 us.
+// One token, 4096 x 4096: 5.5 us (graph replays; 4.8 TB/s behind a launch's
+// 2 us); 4 to 16 waves and 2 to 8 loads in flight measure alike. The 16 x 64 and
+// 32 x 64 tiles above read the tokens once for 64 channels, not for 16, and cost
+// more to start. Both, us, here / there:
+//   channels              1024      2048       4096       5120       6144       8128
+//   k 4096,  1 token     4.4/6.2   4.7/6.3    5.5/6.5    7.5/6.5    7.5/6.8    8.1/7.8
+//   k 4096,  16 tokens   5.7/6.3   6.0/6.6    6.2/6.7    9.6/6.8    9.6/7.0    9.7/8.1
+//   k 11008, 1 token     8.8/11.7  8.9/11.7  10.6/18.0  20.0/19.4  20.8/21.0  22.0/22.6
+//   k 11008, 16 tokens  12.7/12.4 12.8/12.7  14.1/19.9  26.3/21.8  27.5/23.6  29.3/25.1
+// Up to 4096 channels, one round of workgroups, this kernel is the faster one.
+// From there to the bound at 8191 the tiles mostly are, by up to 30% at 16
+// tokens: the bound stands above the crossing and is no part of the tiles' cost.
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8;
 constexpr int kDecodeSteps = 4;  // 64-code steps of a wave a pass

@@ -8,12 +8,18 @@
 // of the codes: 127 y / max|y| = 127 v / max|v|. It enters the scale alone, so
 // both statistics of a row, sum h^2 and max|v|, come from one pass over it.
 //
-// Bound by memory: the norm of 4096 x 8192 bf16 with its residual moves 235 MB in
-// 49 us (4.8 TB/s; a large copy reaches 4.7), quantizing 11008 x 4096 float32 225
-// MB in 42 us, turning it back to bf16 135 MB in 28 us. One row of 4096 takes 4.8
-// us, most of it the launch and one memory latency. Rows stay in registers; what
-// decides is that all loads of a thread are in flight before the first is waited
-// for: with a branch around each load the norm above took 63 us.
+// Rows of 32 bits and the norm are bound by memory: the norm of 4096 x 8192 bf16
+// with its residual moves 235 MB in 48 us (4.9 TB/s; a large copy reaches 4.7),
+// quantizing 11008 x 4096 float32 225 MB in 42 us, turning it back to bf16 135 MB
+// in 28 us. Quantizing 16-bit rows is not: 4096 x 8192 bf16 takes 28 us, 4096 x
+// 11008 39 us (3.6 and 3.5 TB/s), 1.2 elements a picosecond, as many as of
+// float32 rows, which points to the instructions an element. The norm of 777 x
+// 5001 fp16 takes 7.6 us for 12 MB (632 chunks in 768 places, two barriers a row;
+// 5000 columns, whose rows are aligned, 7.2). One row of 4096 takes 3.6 us, with
+// the norm and the residual 4.5, most of it the launch and one memory latency.
+// Rows stay in registers; what decides is that all loads of a thread are in
+// flight before the first is waited for: with a branch around each load the norm
+// above took 63 us.
 #include "elem.h"
 
 namespace qlora {
@@ -44,8 +50,9 @@ struct Top {
 // rows so small that 127 / a leaves the normal range) the quotient in 64 bits
 // decides: 127 v is exact, and with v / a = 2^e V / A (V, A whole, below 2^24) a
 // quotient q that is no tie differs from one by a whole number over 2 A 2^-e,
-// q / (254 V) > q 2^-32 at least, far over the division's rounding q 2^-53. Adding 1.5 2^23 rounds to
-// the nearest integer, ties to even, and leaves the code in the low byte.
+// q / (254 V) > q 2^-32 at least, far over the division's rounding q 2^-53.
+// Adding 1.5 2^23 rounds to the nearest integer, ties to even, and leaves the
+// code in the low byte.
 __device__ __forceinline__ u32x2 encode8(const float* v, float a, float inv) {
   constexpr float kRound = 12582912.0f;
   float c[8], off = 0.0f;

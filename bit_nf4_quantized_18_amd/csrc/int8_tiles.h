@@ -6,7 +6,8 @@
 
 namespace qlora {
 
-// At most these tokens and channels: the kernel that streams the weight.
+// At most these tokens and channels: the kernel that streams the weight (both
+// sides' times stand beside it, in int8_gemm.hip).
 constexpr int kDecodeTokens = 16;
 constexpr int kDecodeMaxN = 8191;
 inline bool decodes(int64_t m, int64_t n) { return m <= kDecodeTokens && n <= kDecodeMaxN; }

@@ -82,3 +82,23 @@ def test_gradients_norm_and_workspace_in_one_allocation(gpu_lib):
     long = torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
     tail = long[need:need + 4].view(torch.float32)
     assert torch.equal(gpu_lib.grad_norm(host, norm=tail, ws=long)[0], norm)
+
+
+def test_views_of_rows(gpu_lib):
+    """Some rows of a packed input as they lie, where their scales start at 16
+    bytes; elsewhere the call refuses them and takes a copy of the scales."""
+    import torch
+
+    m, n, k = 11, 70, 130
+    say("[int8] views of rows")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = gpu_lib.quantize_int8(torch.randn(n, k, generator=g, device="cuda"))
+    x = gpu_lib.quantize_int8(torch.randn(m, k, generator=g, device="cuda"))
+    whole = gpu_lib.int8_linear_fwd(w, x, torch.float32)
+    for i in range(m):
+        part = gpu_lib.PackedInt8(m - i, k, x.codes[i:], x.scale[i:])
+        if i % 4:
+            with pytest.raises(gpu_lib.QloraError, match="ALIGN"):
+                gpu_lib.int8_linear_fwd(w, part, torch.float32)
+            part.scale = part.scale.clone()
+        assert torch.equal(gpu_lib.int8_linear_fwd(w, part, torch.float32), whole[i:])
