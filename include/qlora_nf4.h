@@ -60,7 +60,8 @@
  *   - Weights must be finite; non-finite weights give undefined codes. X, dY,
  *     A and B must be finite as well: the matmul kernels may multiply
  *     elements past a ragged edge of X or dY by exact zeros, so a non-finite
- *     value there could reach a neighbouring output.
+ *     value there could reach a neighbouring output. The 8-bit row and gradient
+ *     calls take any value and say below what becomes of it.
  */
 #ifndef QLORA_NF4_H_
 #define QLORA_NF4_H_
