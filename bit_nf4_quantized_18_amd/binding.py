@@ -34,11 +34,18 @@ EXPORTS = ("qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd", "ql
            "qlora_linear_fwd_grouped_f16", "qlora_linear_bwd_grouped_f16", "qlora_linear_fwd_dropout_f16",
            "qlora_linear_bwd_dropout_f16", "qlora_linear_fwd_noalloc", "qlora_int8_quantize",
            "qlora_int8_dequantize", "qlora_rmsnorm_int8", "qlora_int8_linear_fwd",
-           "qlora_grad_norm", "qlora_grad_clip", "qlora_grad_workspace_bytes")
+           "qlora_grad_norm", "qlora_grad_clip", "qlora_grad_workspace_bytes", "qlora_linear_fwd_gated",
+           "qlora_linear_fwd_gated_f16", "qlora_linear_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_fwd_x8",
+           "qlora_gated_bwd", "qlora_gated_bwd_x8", "qlora_int8_linear_fwd_gated", "qlora_linear_bwd_x8",
+           "qlora_linear_bwd_x8_f16", "qlora_linear_bwd_grouped_x8", "qlora_linear_bwd_grouped_x8_f16",
+           "qlora_linear_x8_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 16 << 20  # QLORA_NOALLOC_SCRATCH_BYTES
 
 CODEBOOK_NF4 = 0   # normal-quantile levels
 CODEBOOK_INT4 = 1  # 16 evenly spaced levels on [-1, 1]
+
+ACT_SILU = 0  # g / (1 + e^-g)
+ACT_GELU = 1  # the tanh form: g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
 
 
 class QloraError(RuntimeError):
@@ -119,6 +126,24 @@ def load():
     lib.qlora_rmsnorm_int8.restype = i32
     lib.qlora_int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp]
     lib.qlora_int8_linear_fwd.restype = i32
+    lib.qlora_linear_fwd_gated.argtypes = [wp, vp, i64, vp, vp, i32, f32, i32, vp, vp, vp, vp, sz, vp]
+    lib.qlora_linear_gated_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.qlora_gated_fwd.argtypes = [vp, i32, i64, i64, i32, vp, vp]
+    lib.qlora_gated_fwd_x8.argtypes = [vp, i64, vp, i32, i64, i64, i32, vp, vp]
+    lib.qlora_gated_bwd.argtypes = [vp, vp, i32, i64, i64, i32, vp, vp]
+    lib.qlora_gated_bwd_x8.argtypes = [vp, i64, vp, vp, i32, i64, i64, i32, vp, vp]
+    lib.qlora_int8_linear_fwd_gated.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, i32, vp, vp]
+    lib.qlora_linear_bwd_x8.argtypes = [wp, vp, i64, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.qlora_linear_bwd_grouped_x8.argtypes = [wp, i32, p64, vp, i64, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp,
+                                                vp, sz, vp]
+    lib.qlora_linear_x8_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    lib.qlora_linear_gated_workspace_bytes.restype = lib.qlora_linear_x8_workspace_bytes.restype = sz
+    for name in ("linear_fwd_gated", "linear_bwd_x8", "linear_bwd_grouped_x8"):
+        fn, f16 = getattr(lib, f"qlora_{name}"), getattr(lib, f"qlora_{name}_f16")
+        f16.argtypes = fn.argtypes
+        fn.restype = f16.restype = i32
+    for name in ("gated_fwd", "gated_fwd_x8", "gated_bwd", "gated_bwd_x8", "int8_linear_fwd_gated"):
+        getattr(lib, f"qlora_{name}").restype = i32
     lib.qlora_grad_workspace_bytes.argtypes = [vp, i32]
     lib.qlora_grad_workspace_bytes.restype = sz
     lib.qlora_grad_norm.argtypes = [vp, vp, i32, i32, vp, vp, sz, vp]
@@ -437,9 +462,13 @@ def linear_bwd(q: PackedNF4, x, dy, a=None, b=None, alpha: float = 0.0, h=None, 
                dx=None, da=None, db=None, ws=None):
     """Returns (dx (m,k) of dy's 16-bit type or None, dA float32 (r,k), dB
     float32 (n,r)). fp16 inputs take the fp16 entry point. Outputs and the
-    workspace may be preallocated."""
+    workspace may be preallocated. ``x`` may be a PackedInt8 of m rows of k
+    values, an input kept in 8 bits (qlora_linear_bwd_x8); ``h`` is then
+    required with an adapter."""
     import torch
 
+    if isinstance(x, PackedInt8):
+        return _linear_bwd_x8(q, None, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws)
     dev = _need_packed(q)
     m = dy.shape[0]
     r = 0 if a is None else a.shape[0]
@@ -594,9 +623,11 @@ def linear_fwd_grouped(q: PackedNF4, parts, x, a, b, alpha: float, want_h: bool 
 def linear_bwd_grouped(q: PackedNF4, parts, x, dy, a, b, alpha: float, h=None, need_dx: bool = True, dx=None,
                        da=None, db=None, ws=None):
     """Grouped backward: (dx (m, k) = sum over parts, dA stacked (g r, k),
-    dB stacked (n, r))."""
+    dB stacked (n, r)). ``x`` may be a PackedInt8, as in linear_bwd."""
     import torch
 
+    if isinstance(x, PackedInt8):
+        return _linear_bwd_x8(q, parts, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws)
     dev = _need_packed(q)
     m, g, r = dy.shape[0], len(parts), b.shape[1]
     t16 = _half_types(dy, "dy")
@@ -834,6 +865,172 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
                 raise ValueError(f"out overlaps {name}")
     _launch(_LIB.qlora_int8_linear_fwd, index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
             x.scale.data_ptr(), m, code, out.data_ptr())
+    return out
+
+
+def x8_workspace_bytes(m: int, n: int, k: int, g: int, r: int) -> int:
+    return int(load().qlora_linear_x8_workspace_bytes(m, n, k, g, r))
+
+
+def _linear_bwd_x8(q, parts, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws):
+    """linear_bwd (``parts`` None) and linear_bwd_grouped with x as 8-bit rows."""
+    if _torch is None:
+        _init()
+    dev = _need_packed(q)
+    index = q.codes.get_device()
+    m = dy.shape[0]
+    g = 1 if parts is None else len(parts)
+    r = 0 if b is None else b.shape[-1]
+    t16 = _half_types(dy, "dy")
+    f32 = (_torch.float32,)
+    _need(dy, "dy", (m, q.n), t16, dev)
+    _need_adapter(a, b, g * r, q.k, q.n, t16, dev, rb=r)
+    ld = _need_int8(x, "x", index)
+    if x.n != m or x.k != q.k:
+        raise ValueError(f"x holds {x.n} rows of {x.k} values, expected {m} of {q.k}")
+    _need(h, "h", (m, g * r), f32, dev, optional=r == 0)
+    if dx is None and need_dx:
+        dx = dy.new_empty(m, q.k)
+    if r and da is None:
+        da = dy.new_empty(g * r, q.k, dtype=_torch.float32)
+    if r and db is None:
+        db = dy.new_empty(q.n, r, dtype=_torch.float32)
+    _need(dx, "dx", (m, q.k), t16, dev, optional=True)
+    _need(da, "da", (g * r, q.k), f32, dev, optional=r == 0)
+    _need(db, "db", (q.n, r), f32, dev, optional=r == 0)
+    _need_ws(ws, dev)
+    if ws is None:
+        nbytes = x8_workspace_bytes(m, q.n, q.k, g, r)
+        ws = dy.new_empty(nbytes, dtype=_torch.uint8) if nbytes else None
+    else:
+        nbytes = ws.numel()
+    wc = q.c_struct()
+    name = "qlora_linear_bwd" + ("" if parts is None else "_grouped") + "_x8" + ("_f16" if dy.dtype is _torch.float16 else "")
+    lead = () if parts is None else (g, _parts(parts))
+    _launch(getattr(_LIB, name), index, ctypes.byref(wc), *lead, x.codes.data_ptr(), ld, x.scale.data_ptr(),
+            dy.data_ptr(), m, _ptr(a), _ptr(b), r, float(alpha), _ptr(h), _ptr(dx), _ptr(da), _ptr(db), _ptr(ws), nbytes)
+    return dx, da, db
+
+
+# ---------------------------------------------------------------- gated block
+def gated_workspace_bytes(m: int, n: int, k: int, r: int) -> int:
+    """For linear_fwd_gated over a stacked weight of n rows (gate's and up's)."""
+    return int(load().qlora_linear_gated_workspace_bytes(m, n, k, r))
+
+
+def linear_fwd_gated(q: PackedNF4, x, a=None, b=None, alpha: float = 0.0, act: int = ACT_SILU, want_y: bool = True,
+                     want_h: bool = True, out=None, y_out=None, h_out=None, ws=None):
+    """The gated feed-forward block (qlora_linear_fwd_gated): P = act(G) U with
+    [G | U] = X W16^T + (alpha/r) (X A_l^T) B_l^T over a weight that holds gate's
+    rows above up's (q.n a multiple of 512). x: bf16 or fp16 (m, k); a: the stacked
+    (2 r, k) A, b: the stacked (q.n, r) B, or both None. Returns (p (m, q.n / 2),
+    y (m, q.n) = [G | U] in x's type or None, h (m, 2 r) float32 or None).
+    gated_bwd and linear_bwd_grouped are its backward."""
+    if _torch is None:
+        _init()
+    dev = _need_packed(q)
+    index = q.codes.get_device()
+    m = x.shape[0]
+    r = 0 if b is None else b.shape[-1]
+    t16 = _half_types(x, "x")
+    _need(x, "x", (m, q.k), t16, dev)
+    _need_adapter(a, b, 2 * r, q.k, q.n, t16, dev, rb=r)
+    p = out if out is not None else x.new_empty(m, q.n // 2)
+    y = y_out if y_out is not None else (x.new_empty(m, q.n) if want_y else None)
+    h = h_out if h_out is not None else (x.new_empty(m, 2 * r, dtype=_torch.float32) if want_h and r else None)
+    _need(p, "out", (m, q.n // 2), t16, dev)
+    _need(y, "y_out", (m, q.n), t16, dev, optional=True)
+    _need(h, "h_out", (m, 2 * r), (_torch.float32,), dev, optional=True)
+    _need_ws(ws, dev)
+    if ws is None:
+        nbytes = gated_workspace_bytes(m, q.n, q.k, r)
+        ws = x.new_empty(nbytes, dtype=_torch.uint8) if nbytes else None
+    else:
+        nbytes = ws.numel()
+    wc = q.c_struct()
+    fn = _LIB.qlora_linear_fwd_gated_f16 if x.dtype is _torch.float16 else _LIB.qlora_linear_fwd_gated
+    _launch(fn, index, ctypes.byref(wc), x.data_ptr(), m, _ptr(a), _ptr(b), r, float(alpha), int(act), _ptr(y),
+            p.data_ptr(), _ptr(h), _ptr(ws), nbytes)
+    return p, y, h
+
+
+def _gated_input(y):
+    """(type code or None, tokens, n, GPU index, leading arguments) of gate and up's
+    pre-activations: (m, 2 n), or a PackedInt8 of 2 m rows of n values."""
+    if isinstance(y, PackedInt8):
+        index = y.codes.get_device()
+        ld = _need_int8(y, "y", index)
+        if y.n % 2:
+            raise ValueError(f"y holds {y.n} rows, expected two a token: gate's and up's")
+        return None, y.n // 2, y.k, index, (y.codes.data_ptr(), ld, y.scale.data_ptr())
+    code, m, two_n, index = _need_rows(y, "y")
+    if two_n % 2:
+        raise ValueError(f"y has {two_n} columns, expected gate's and as many of up's")
+    return code, m, two_n // 2, index, (y.data_ptr(),)
+
+
+def gated_fwd(y, act: int = ACT_SILU, dtype=None, out=None):
+    """P = act(G) U (m, n) of the pre-activations [G | U] (qlora_gated_fwd). y: (m,
+    2 n) bf16, fp16 or float32, or a PackedInt8 of 2 m rows of n values, which
+    ``quantize_int8(y.view(2 * m, n))`` gives. ``dtype``: y's type, and for a
+    PackedInt8 the result's (bf16 by default). ``out`` may be preallocated."""
+    code, m, n, index, args = _gated_input(y)
+    rows = code is None
+    if rows:
+        dtype, code = _out_dtype(dtype)
+    elif dtype is not None and dtype is not y.dtype:
+        raise TypeError(f"dtype is {dtype}, y's {y.dtype}: they must agree")
+    like = y.codes if rows else y
+    dtype = dtype if rows else y.dtype
+    if out is None:
+        out = like.new_empty(m, n, dtype=dtype)
+    else:
+        _need(out, "out", (m, n), (dtype,), like.device)
+    _launch(_LIB.qlora_gated_fwd_x8 if rows else _LIB.qlora_gated_fwd, index, *args, code, m, n, int(act), out.data_ptr())
+    return out
+
+
+def gated_bwd(y, dp, act: int = ACT_SILU, out=None):
+    """d[G | U] (m, 2 n) of P = act(G) U for dP = dp (m, n) (qlora_gated_bwd). y: (m,
+    2 n) of dp's type or a PackedInt8 of 2 m rows of n values, as in gated_fwd.
+    ``out`` may be preallocated, or be y itself (in place)."""
+    code, m, n, index, args = _gated_input(y)
+    dcode = _need_rows(dp, "dp")[0]
+    if dp.shape != (m, n) or dp.get_device() != index:
+        raise ValueError(f"dp must have shape {(m, n)} on y's device, got {tuple(dp.shape)} on {dp.device}")
+    if code is not None and code != dcode:
+        raise TypeError(f"dp has dtype {dp.dtype}, expected {y.dtype}")
+    if out is None:
+        out = dp.new_empty(m, 2 * n)
+    else:
+        _need(out, "out", (m, 2 * n), (dp.dtype,), dp.device)
+    _launch(_LIB.qlora_gated_bwd_x8 if code is None else _LIB.qlora_gated_bwd, index, *args, dp.data_ptr(), dcode, m, n,
+            int(act), out.data_ptr())
+    return out
+
+
+def int8_linear_fwd_gated(q: PackedInt8, x: PackedInt8, act: int = ACT_SILU, dtype=None, out=None):
+    """The gated feed-forward block in 8 bits (qlora_int8_linear_fwd_gated): P =
+    act(G) U with [G | U] = X W^T, q holding gate's rows above up's (2 n, k), x the
+    input by token (m, k). Returns (m, n) of ``dtype`` (bf16, fp16 or float32; bf16
+    by default). ``out`` may be preallocated; over the operands it is refused."""
+    dtype, code = _out_dtype(dtype)
+    codes = q.codes
+    index = codes.get_device()
+    ld = _need_int8(q, "q", index)
+    if q.n % 2:
+        raise ValueError(f"q holds {q.n} rows, expected gate's and as many of up's")
+    if x.k != q.k:
+        raise ValueError(f"x holds rows of {x.k} values, the weight rows of {q.k}")
+    if _need_int8(x, "x", index) != ld:
+        raise ValueError("the rows of x and of the weight must be padded to the same length")
+    m, n = x.n, q.n // 2
+    if out is None:
+        out = codes.new_empty(m, n, dtype=dtype)
+    else:
+        _need(out, "out", (m, n), (dtype,), codes.device)
+    _launch(_LIB.qlora_int8_linear_fwd_gated, index, codes.data_ptr(), q.scale.data_ptr(), n, ld, x.codes.data_ptr(),
+            x.scale.data_ptr(), m, int(act), code, out.data_ptr())
     return out
 
 

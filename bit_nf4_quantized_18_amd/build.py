@@ -38,6 +38,8 @@ SOURCES = {
     "gemm_kernels.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "noalloc.hip": DEVICE,
     "int8_rows.hip": DEVICE + ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt"],
+    "gated_kernels.hip": DEVICE + ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt"],
+    "rank_grad8.hip": DEVICE,
     "int8_gemm.hip": DEVICE + ["-ffp-contract=off"],
     "grad_clip.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
 }

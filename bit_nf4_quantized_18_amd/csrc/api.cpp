@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 
 #include "internal.h"
@@ -81,6 +82,33 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
   return L;
 }
 
+// The gated forward: H's partial sums (decode, unless the kernel forms H
+// itself), or H, s H and the partial sums of H.
+bool gated_fuses_h(int slots) { return slots > 0 && slots <= 16; }
+FwdLayout gated_layout(int64_t m, int64_t k, int slots) {
+  Carve c;
+  FwdLayout L{};
+  if (m <= kGemvMaxM) {
+    L.h32 = c.take(slots == 0 || gated_fuses_h(slots) ? 0 : qlora::skinny_splits(m, k) * m * slots * 4);
+    L.total = c.off;
+    return L;
+  }
+  return fwd_layout(m, 0, k, slots, true);
+}
+
+// The backward from 8-bit rows: the plain one's buffers but for the partial sums
+// of dA and dB, which go last.
+BwdLayout x8_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
+  BwdLayout L = bwd_layout(m, n, k, r, rpart);
+  if (r == 0) return L;
+  Carve c;
+  c.off = L.part;
+  const int splits = qlora::rank_grad8_splits(m, n, k, r, rpart);
+  c.take(splits == 1 ? 0 : splits * (r * k + rpart * n) * 4);
+  L.total = c.off;
+  return L;
+}
+
 // Dropout calls: the masked copy of X first, then the forward's (GEMM path)
 // or the backward's buffers.
 int64_t drop_xm_bytes(int64_t m, int64_t k) { return round_up(m * k * 2, kAlign); }
@@ -96,6 +124,13 @@ int64_t drop_total(int64_t m, int64_t n, int64_t k, int r) {
 bool linear_sizes_ok(int64_t m, int64_t n, int64_t k) {
   return m > 0 && n > 0 && k > 0 && m <= (INT64_C(1) << 31) && n <= (INT64_C(1) << 22) && k <= (INT64_C(1) << 22);
 }
+
+// A linear's input kept as 8-bit rows.
+struct Rows8 {
+  const int8_t* codes;
+  int64_t ld;
+  const float* scale;
+};
 
 // Adapter dropout: keep mask (m x k bytes, non-zero = kept) and 1 / (1 - p).
 struct DropArg {
@@ -139,6 +174,34 @@ PackedW view(const qlora_nf4_weight* w) {
 }
 
 qlora_status hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
+
+bool known_dtype(int t) { return t == QLORA_BF16 || t == QLORA_F32 || t == QLORA_F16; }
+int dtype_bytes(int t) { return t == QLORA_F32 ? 4 : 2; }
+bool known_act(int a) { return a == QLORA_ACT_SILU || a == QLORA_ACT_GELU_TANH; }
+
+// A buffer's addresses. A workgroup may write its part of an output before
+// another has read the inputs, so calls refuse outputs that meet them.
+struct Span {
+  uintptr_t at, end;
+};
+Span span(const void* p, int64_t bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return Span{at, p == nullptr ? at : at + static_cast<uintptr_t>(bytes)};
+}
+bool meet(Span a, Span b) {  // an empty buffer meets nothing
+  return (a.at > b.at ? a.at : b.at) < (a.end < b.end ? a.end : b.end);
+}
+
+// The outputs meet neither an input nor each other.
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span& i : inputs)
+      if (meet(*o, i)) return false;
+    for (auto q = outputs.begin(); q != o; ++q)
+      if (meet(*o, *q)) return false;
+  }
+  return true;
+}
 
 // The fused GEMM numbers its 256 x 128 output tiles with 32-bit integers.
 bool gemm_tiles_fit(int64_t m, int64_t p) { return ((m + 255) / 256) * ((p + 127) / 128) < (INT64_C(1) << 31); }
@@ -310,7 +373,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
                              const uint16_t* dy, int64_t m, const uint16_t* a, const uint16_t* b, int r, int rpart,
                              float alpha, const float* h_saved, uint16_t* dx, float* da, float* db, void* ws,
                              size_t ws_bytes, hipStream_t stream, const DropArg* drop = nullptr,
-                             bool f16 = false) {
+                             bool f16 = false, const Rows8* x8 = nullptr) {
   qlora_status st = check_weight(w, true);
   if (st != QLORA_OK) return st;
   if (m < 0 || m > (INT64_C(1) << 31)) return QLORA_ERR_SHAPE;
@@ -331,16 +394,29 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     return QLORA_OK;
   }
   if (dy == nullptr) return QLORA_ERR_NULL;
-  if (r > 0 && x == nullptr) return QLORA_ERR_NULL;
+  if (r > 0 && x == nullptr && x8 == nullptr) return QLORA_ERR_NULL;
+  if (r > 0 && x8 != nullptr) {
+    if (x8->codes == nullptr || x8->scale == nullptr || h_saved == nullptr) return QLORA_ERR_NULL;
+    if (x8->ld < k || x8->ld % 64 != 0 || x8->ld > QLORA_INT8_MAX_COLS) return QLORA_ERR_SHAPE;
+    if (!aligned16(x8->codes) || !aligned16(x8->scale)) return QLORA_ERR_ALIGN;
+  }
   if (dx == nullptr && r == 0) return QLORA_OK;  // nothing requested
   if (!aligned16(dy) || (x != nullptr && !aligned16(x)) || (dx != nullptr && !aligned16(dx))) return QLORA_ERR_ALIGN;
   if (h_saved != nullptr && !aligned16(h_saved)) return QLORA_ERR_ALIGN;
   if (drop != nullptr && r == 0) drop = nullptr;  // no adapter, nothing to drop
   const size_t need = drop != nullptr ? static_cast<size_t>(drop_total(m, n, k, r))
+                      : x8 != nullptr ? static_cast<size_t>(x8_layout(m, n, k, r, rpart).total)
                       : grouped       ? qlora_linear_grouped_workspace_bytes(m, n, k, grp->g, rpart)
                                       : qlora_linear_workspace_bytes(m, n, k, r);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
   if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
+
+  if (x8 != nullptr &&
+      !apart({span(dx, 2 * m * k), span(da, 4 * r * k), span(db, 4 * n * rpart), span(ws, static_cast<int64_t>(need))},
+             {span(r > 0 ? x8->codes : nullptr, m * x8->ld), span(r > 0 ? x8->scale : nullptr, 4 * m),
+              span(dy, 2 * m * n), span(h_saved, 4 * m * r), span(a, 2 * r * k), span(b, 2 * n * rpart),
+              span(w->codes, n * k / 2)}))
+    return QLORA_ERR_UNSUPPORTED;
 
   const BwdLayout L = bwd_layout(m, n, k, r, rpart);
   char* base = static_cast<char*>(ws);
@@ -381,7 +457,10 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     if (drop != nullptr) dhs = nullptr;
     QLORA_TRY(qlora::launch_skinny_prefill(dy, bt, m, n, r, rp, drop != nullptr ? s * inv_keep : s, 1.0f, spart, dh32,
                                            dhs, stream, f16));
-    if (qlora::rank_grads_fused(r) && qlora::rank_grads_fused(rpart)) {
+    if (x8 != nullptr) {
+      QLORA_TRY(qlora::launch_rank_grads8(dh32, x8->codes, x8->ld, x8->scale, k, h, dy, n, m, r, grp, s, part, da, db,
+                                          stream, f16));
+    } else if (qlora::rank_grads_fused(r) && qlora::rank_grads_fused(rpart)) {
       // dA = dH^T X (r x k) and dB = s dY^T H (n x rpart) in one pass each
       QLORA_TRY(qlora::launch_rank_grads(dh32, xa, k, h, dy, n, m, r, grp, s,
                                          qlora::rank_grad_splits(m, n, k, r, rpart), part, da, db, stream, f16));
@@ -509,6 +588,131 @@ qlora_status qlora_linear_bwd_grouped_f16(const qlora_nf4_weight* w, int g, cons
                          true);
 }
 
+
+// ---------------------------------------------------------------------------
+// Backward from an input kept as 8-bit rows
+// ---------------------------------------------------------------------------
+size_t qlora_linear_x8_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r) {
+  if (!linear_sizes_ok(m, n, k) || g < 1 || g > QLORA_MAX_PARTS || r < 0 || g * r > QLORA_MAX_RANK) return 0;
+  return static_cast<size_t>(x8_layout(m, n, k, g * r, r).total);
+}
+
+static qlora_status bwd_x8(const qlora_nf4_weight* w, int g, const int64_t* parts, const int8_t* x, int64_t ldx,
+                           const float* x_scale, const uint16_t* dy, int64_t m, const uint16_t* a, const uint16_t* b,
+                           int r, float alpha, const float* h, uint16_t* dx, float* da, float* db, void* ws,
+                           size_t ws_bytes, hipStream_t stream, bool f16) {
+  qlora::LoraParts lp;
+  if (parts != nullptr) {
+    const qlora_status st = group_parts(w, g, parts, r, &lp);
+    if (st != QLORA_OK) return st;
+    if (r % 16 != 0) return QLORA_ERR_UNSUPPORTED;
+  }
+  const Rows8 rows{x, ldx, x_scale};
+  return linear_bwd_impl(w, parts != nullptr ? &lp : nullptr, nullptr, dy, m, a, b, g * r, r, alpha, h, dx, da, db, ws,
+                         ws_bytes, stream, nullptr, f16, &rows);
+}
+
+qlora_status qlora_linear_bwd_x8(const qlora_nf4_weight* w, const int8_t* x, int64_t ldx, const float* x_scale,
+                                 const uint16_t* dy, int64_t m, const uint16_t* a, const uint16_t* b, int r,
+                                 float alpha, const float* h, uint16_t* dx, float* da, float* db, void* ws,
+                                 size_t ws_bytes, hipStream_t stream) {
+  return bwd_x8(w, 1, nullptr, x, ldx, x_scale, dy, m, a, b, r, alpha, h, dx, da, db, ws, ws_bytes, stream, false);
+}
+
+qlora_status qlora_linear_bwd_x8_f16(const qlora_nf4_weight* w, const int8_t* x, int64_t ldx, const float* x_scale,
+                                     const uint16_t* dy, int64_t m, const uint16_t* a, const uint16_t* b, int r,
+                                     float alpha, const float* h, uint16_t* dx, float* da, float* db, void* ws,
+                                     size_t ws_bytes, hipStream_t stream) {
+  return bwd_x8(w, 1, nullptr, x, ldx, x_scale, dy, m, a, b, r, alpha, h, dx, da, db, ws, ws_bytes, stream, true);
+}
+
+qlora_status qlora_linear_bwd_grouped_x8(const qlora_nf4_weight* w, int g, const int64_t* parts, const int8_t* x,
+                                         int64_t ldx, const float* x_scale, const uint16_t* dy, int64_t m,
+                                         const uint16_t* a, const uint16_t* b, int r, float alpha, const float* h,
+                                         uint16_t* dx, float* da, float* db, void* ws, size_t ws_bytes,
+                                         hipStream_t stream) {
+  if (parts == nullptr) return QLORA_ERR_NULL;
+  return bwd_x8(w, g, parts, x, ldx, x_scale, dy, m, a, b, r, alpha, h, dx, da, db, ws, ws_bytes, stream, false);
+}
+
+qlora_status qlora_linear_bwd_grouped_x8_f16(const qlora_nf4_weight* w, int g, const int64_t* parts, const int8_t* x,
+                                             int64_t ldx, const float* x_scale, const uint16_t* dy, int64_t m,
+                                             const uint16_t* a, const uint16_t* b, int r, float alpha, const float* h,
+                                             uint16_t* dx, float* da, float* db, void* ws, size_t ws_bytes,
+                                             hipStream_t stream) {
+  if (parts == nullptr) return QLORA_ERR_NULL;
+  return bwd_x8(w, g, parts, x, ldx, x_scale, dy, m, a, b, r, alpha, h, dx, da, db, ws, ws_bytes, stream, true);
+}
+
+// ---------------------------------------------------------------------------
+// Gated feed-forward block
+// ---------------------------------------------------------------------------
+size_t qlora_linear_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int r) {
+  if (!linear_sizes_ok(m, n, k) || r < 0 || 2 * r > QLORA_MAX_RANK) return 0;
+  return static_cast<size_t>(gated_layout(m, k, 2 * r).total);
+}
+
+static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int64_t m, const uint16_t* a,
+                              const uint16_t* b, int r, float alpha, int act, uint16_t* y, uint16_t* p, float* h_out,
+                              void* ws, size_t ws_bytes, hipStream_t stream, bool f16) {
+  if (!known_act(act) || r > QLORA_MAX_RANK / 2) return QLORA_ERR_UNSUPPORTED;
+  if (r < 0) return QLORA_ERR_SHAPE;
+  const int slots = 2 * r;
+  const qlora_status st = check_fwd_args(w, x, m, a, b, slots, p, h_out);
+  if (st != QLORA_OK) return st;
+  if (w->n % 512 != 0) return QLORA_ERR_SHAPE;  // two parts of whole 256-row groups
+  if (m == 0) return QLORA_OK;
+  if (!aligned16(y)) return QLORA_ERR_ALIGN;
+  const int64_t n = w->n, k = w->k;
+  const FwdLayout L = gated_layout(m, k, slots);
+  const int64_t need = L.total;
+  if (need > 0 && (ws == nullptr || ws_bytes < static_cast<size_t>(need))) return QLORA_ERR_WORKSPACE;
+  if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (r == 0) h_out = nullptr;
+  if (!apart({span(p, m * n), span(y, 2 * m * n), span(h_out, 4 * m * slots), span(ws, need)},
+             {span(x, 2 * m * k), span(a, 2 * slots * k), span(b, 2 * n * r), span(w->codes, n * k / 2)}))
+    return QLORA_ERR_UNSUPPORTED;
+
+  qlora::LoraParts lp;
+  lp.g = 2;
+  lp.rpart = r;
+  lp.end[0] = static_cast<int>(n / 2);
+  lp.end[1] = static_cast<int>(n);
+  char* base = static_cast<char*>(ws);
+  const float s = r == 0 ? 0.0f : alpha / static_cast<float>(r);
+  const int rp = rank_pad(slots);
+  const PackedW pw = view(w);
+  if (m <= kGemvMaxM) {
+    float* hpart = nullptr;
+    const int splits = qlora::skinny_splits(m, k);
+    if (slots > 0 && !gated_fuses_h(slots)) {
+      hpart = reinterpret_cast<float*>(base + L.h32);
+      QLORA_TRY(qlora::launch_skinny_decode(x, a, m, k, slots, rp, hpart, splits, stream, f16));
+    }
+    return hip_status(qlora::launch_gemv_mfma(pw, x, m, a, hpart, splits, b, slots, s, y, h_out, stream, f16, &lp,
+                                              qlora::GateOut{p, act}));
+  }
+  uint16_t* hs = nullptr;
+  if (r > 0) {
+    float* h32 = h_out != nullptr ? h_out : reinterpret_cast<float*>(base + L.h32);
+    hs = reinterpret_cast<uint16_t*>(base + L.hs);
+    QLORA_TRY(qlora::launch_skinny_prefill(x, a, m, k, slots, rp, 1.0f, s, reinterpret_cast<float*>(base + L.part), h32,
+                                           hs, stream, f16));
+  }
+  return hip_status(qlora::launch_gemm_gated(pw, x, m, hs, b, r, rp, act, y, p, stream, f16));
+}
+
+qlora_status qlora_linear_fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int64_t m, const uint16_t* a,
+                                    const uint16_t* b, int r, float alpha, int act, uint16_t* y, uint16_t* p,
+                                    float* h_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return fwd_gated(w, x, m, a, b, r, alpha, act, y, p, h_out, ws, ws_bytes, stream, false);
+}
+
+qlora_status qlora_linear_fwd_gated_f16(const qlora_nf4_weight* w, const uint16_t* x, int64_t m, const uint16_t* a,
+                                        const uint16_t* b, int r, float alpha, int act, uint16_t* y, uint16_t* p,
+                                        float* h_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return fwd_gated(w, x, m, a, b, r, alpha, act, y, p, h_out, ws, ws_bytes, stream, true);
+}
 
 // Adapter arguments of the merge calls: r in 0..QLORA_MAX_RANK; for r > 0,
 // a (r x k) and b (n x r) are required and 16-byte aligned.
@@ -655,22 +859,6 @@ qlora_status qlora_linear_bwd_f16(const qlora_nf4_weight* w, const uint16_t* x, 
 // ---------------------------------------------------------------------------
 // 8-bit rows and their product
 // ---------------------------------------------------------------------------
-static bool known_dtype(int t) { return t == QLORA_BF16 || t == QLORA_F32 || t == QLORA_F16; }
-static int dtype_bytes(int t) { return t == QLORA_F32 ? 4 : 2; }
-
-// A buffer's addresses. A workgroup may write its part of an output before
-// another has read the inputs, so calls refuse outputs that meet them.
-struct Span {
-  uintptr_t at, end;
-};
-static Span span(const void* p, int64_t bytes) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  return Span{at, p == nullptr ? at : at + static_cast<uintptr_t>(bytes)};
-}
-static bool meet(Span a, Span b) {  // an empty buffer meets nothing
-  return (a.at > b.at ? a.at : b.at) < (a.end < b.end ? a.end : b.end);
-}
-
 static bool int8_rows_ok(int64_t rows, int64_t cols, int64_t ld) {
   return rows >= 0 && rows < (INT64_C(1) << 31) && cols >= 1 && ld >= cols && ld % 64 == 0 &&
          ld <= QLORA_INT8_MAX_COLS;
@@ -740,6 +928,60 @@ qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_
   if (!aligned16(w) || !aligned16(w_scale) || !aligned16(x) || !aligned16(x_scale) || !aligned16(y))
     return QLORA_ERR_ALIGN;
   return hip_status(qlora::launch_int8_linear(w, w_scale, n, k, x, x_scale, m, out_dtype, y, stream));
+}
+
+qlora_status qlora_int8_linear_fwd_gated(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
+                                         const float* x_scale, int64_t m, int act, int out_dtype, void* p,
+                                         hipStream_t stream) {
+  if (!known_dtype(out_dtype) || !known_act(act)) return QLORA_ERR_UNSUPPORTED;
+  if (n < 1 || n > (INT64_C(1) << 21) || !int8_linear_ok(m, 2 * n, k) || !qlora::int8_linear_fits(m, 2 * n, k))
+    return QLORA_ERR_SHAPE;
+  if (m == 0) return QLORA_OK;
+  if (w == nullptr || w_scale == nullptr || x == nullptr || x_scale == nullptr || p == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(w) || !aligned16(w_scale) || !aligned16(x) || !aligned16(x_scale) || !aligned16(p))
+    return QLORA_ERR_ALIGN;
+  if (!apart({span(p, m * n * dtype_bytes(out_dtype))},
+             {span(w, 2 * n * k), span(w_scale, 8 * n), span(x, m * k), span(x_scale, 4 * m)}))
+    return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_int8_gated(w, w_scale, n, k, x, x_scale, m, act, out_dtype, p, stream));
+}
+
+// The elementwise calls: `out` is m x n, or with dp m x 2 n, where it may be y.
+static qlora_status gated(const void* y, const int8_t* codes, int64_t ld, const float* scale, bool rows8,
+                          const void* dp, bool back, int dtype, int64_t m, int64_t n, int act, void* out,
+                          hipStream_t stream) {
+  if (!known_dtype(dtype) || !known_act(act)) return QLORA_ERR_UNSUPPORTED;
+  if (n < 1 || n > QLORA_INT8_MAX_COLS || m < 0 || m >= (INT64_C(1) << 30)) return QLORA_ERR_SHAPE;
+  if (rows8 && (ld < n || ld % 64 != 0 || ld > QLORA_INT8_MAX_COLS)) return QLORA_ERR_SHAPE;
+  if (m == 0) return QLORA_OK;
+  if ((rows8 ? codes == nullptr || scale == nullptr : y == nullptr) || (back && dp == nullptr) || out == nullptr)
+    return QLORA_ERR_NULL;
+  if (!aligned16(y) || !aligned16(codes) || !aligned16(scale) || !aligned16(dp) || !aligned16(out))
+    return QLORA_ERR_ALIGN;
+  const int64_t bytes = m * n * dtype_bytes(dtype);
+  const Span os = span(out, (back ? 2 : 1) * bytes), ys = span(y, 2 * bytes);
+  if (!apart({os}, {span(codes, 2 * m * ld), span(scale, 8 * m), span(dp, bytes)})) return QLORA_ERR_UNSUPPORTED;
+  if (meet(os, ys) && !(back && out == y)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_gated(y, codes, ld, scale, dp, dtype, m, n, act, out, stream));
+}
+
+qlora_status qlora_gated_fwd(const void* y, int dtype, int64_t m, int64_t n, int act, void* p, hipStream_t stream) {
+  return gated(y, nullptr, 0, nullptr, false, nullptr, false, dtype, m, n, act, p, stream);
+}
+
+qlora_status qlora_gated_fwd_x8(const int8_t* codes, int64_t ld, const float* scale, int dtype, int64_t m, int64_t n,
+                                int act, void* p, hipStream_t stream) {
+  return gated(nullptr, codes, ld, scale, true, nullptr, false, dtype, m, n, act, p, stream);
+}
+
+qlora_status qlora_gated_bwd(const void* y, const void* dp, int dtype, int64_t m, int64_t n, int act, void* dy,
+                             hipStream_t stream) {
+  return gated(y, nullptr, 0, nullptr, false, dp, true, dtype, m, n, act, dy, stream);
+}
+
+qlora_status qlora_gated_bwd_x8(const int8_t* codes, int64_t ld, const float* scale, const void* dp, int dtype,
+                                int64_t m, int64_t n, int act, void* dy, hipStream_t stream) {
+  return gated(nullptr, codes, ld, scale, true, dp, true, dtype, m, n, act, dy, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,49 @@
+// The activations of the gated feed-forward block, act(g) = g sigma(z(g)):
+//   QLORA_ACT_SILU       z = g
+//   QLORA_ACT_GELU_TANH  z = 2 c (g + 0.044715 g^3), c = sqrt(2 / pi), which is
+//                        0.5 g (1 + tanh(c (g + 0.044715 g^3)))
+// and act'(g) = sigma + g sigma (1 - sigma) z'(g), in float32. A NaN gate gives
+// NaN, an infinite one the limits: act(-inf) = -0, act' = 0; act(inf) = inf,
+// act' = 1.
+#pragma once
+
+#include "internal.h"
+
+namespace qlora {
+
+constexpr float kGeluC = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGeluC3 = 0.0713548162726009f;  // 0.044715 of it
+
+// 1 / (1 + e^-z). kFine: with the library's exponential and a correctly rounded
+// quotient, for results that stay in float32. Otherwise the hardware's exponent
+// and reciprocal, whose relative error, below 2^-21 (1 + |z|), vanishes in a
+// rounding to 16 bits wherever sigma is not itself below that type's range. Both
+// give 0 below z = -88.7, where e^-z leaves float32.
+template <bool kFine>
+__device__ __forceinline__ float sigma(float z) {
+  if constexpr (kFine) return 1.0f / (1.0f + expf(-z));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
+
+template <bool kFine>
+__device__ __forceinline__ float act_value(float g, int act) {
+  const float z = act == QLORA_ACT_SILU ? g : g * fmaf(kGeluC3 * g, g, kGeluC);
+  return fmaxf(g, -128.0f) * sigma<kFine>(z);  // sigma is 0 from there on: g = -inf gives no inf 0
+}
+
+// act(g) and act'(g). Beyond |g| = 128 the second term of act' is 0 in float32
+// for both activations, and a gate held there keeps g^2 from overflowing.
+template <bool kFine>
+__device__ __forceinline__ float act_both(float g, int act, float* slope) {
+  const float t = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
+  float z = g, zs = t;
+  if (act != QLORA_ACT_SILU) {
+    z = g * fmaf(kGeluC3 * g, g, kGeluC);
+    zs = t * fmaf(3.0f * kGeluC3 * t, t, kGeluC);
+  }
+  const float s = sigma<kFine>(z);
+  *slope = fmaf(zs * (1.0f - s), s, s);
+  return fmaxf(g, -128.0f) * s;
+}
+
+}  // namespace qlora

@@ -43,9 +43,17 @@
 // rows in that XCD's L2. The rank-r LoRA term is one more pass of MFMAs.
 // kF16 builds the same kernel for IEEE-half compute: half lookup tables, the
 // f16 MFMA and a half output; everything else is bit-pattern movement.
+//
+// kGated builds the forward for a gated feed-forward block: W holds gate's rows
+// above up's, and a workgroup's 128 weight rows are 64 gate rows and the 64 up
+// rows of the same outputs, 16 of each in turn, so that a lane's accumulators
+// hold both pre-activations of an output and the product act(gate) up is formed
+// from them unrounded: 256 x 64 outputs a tile, and the pre-activations are
+// written only where the backward pass wants them.
 #include <type_traits>
 
 #include "bufmem.h"
+#include "gate.h"
 #include "internal.h"
 #include "mfma.h"
 #include "nf4_lut.h"
@@ -102,11 +110,19 @@ __device__ __forceinline__ BlockLut make_block_lut_pair(const float (&lv)[8], fl
   return t;
 }
 
-template <bool kTransW, bool kDQ, bool kF16>
+// Weight row (output column of the stacked product) of row `row` of gated tile
+// p0 / kBP: 64 rows are four runs of 16, gate, gate, up, up.
+__device__ __forceinline__ int64_t gated_row(int64_t p0, int row, int64_t half) {
+  return p0 / 2 + 32 * (row >> 6) + (row & 31) + ((row & 32) != 0 ? half : 0);
+}
+
+template <bool kTransW, bool kDQ, bool kF16, bool kGated = false>
 __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t* __restrict__ A, int64_t M,
                                                        int64_t P, int64_t Qn, const uint16_t* __restrict__ ep_a,
                                                        const uint16_t* __restrict__ ep_b, int64_t ep_ld, int ep_lim,
-                                                       int rpad, LoraParts lp, uint16_t* __restrict__ out, Levels L) {
+                                                       int rpad, LoraParts lp, uint16_t* __restrict__ out, Levels L,
+                                                       GateOut gate) {
+  static_assert(!(kTransW && kGated), "the gated product is a forward");
   __shared__ __attribute__((aligned(16))) uint16_t As[kStages * kAStage];
   __shared__ __attribute__((aligned(16))) uint16_t Bs[kStages * kBStage];
 
@@ -196,7 +212,7 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t
     }
     // per-step byte offsets: A moves by 64 columns; the weight moves along k
     // (forward) or by 64 rows (backward)
-    const int64_t wrow0 = kTransW ? w_r : p0 + w_r;
+    const int64_t wrow0 = kTransW ? w_r : kGated ? gated_row(p0, w_r, P / 2) : p0 + w_r;
     const int64_t wk0 = kTransW ? p0 + w_c : w_c;
     const int c_voff = static_cast<int>((wrow0 * K + wk0) / 2);
     const int s_voff = static_cast<int>(wrow0 * nbk + wk0 / 64);
@@ -381,7 +397,7 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t
   // two) and part l only sees slots l rpart .. (l+1) rpart - 1, which carry its
   // own H; row p of ep_b holds that part's B row.
   int slot_shift = 0;
-  if (!kTransW) {
+  if (!kTransW && !kGated) {
     int part = 0;
 #pragma unroll
     for (int l = 0; l < 3; ++l) part += (l + 1 < lp.g && p0 >= lp.end[l]) ? 1 : 0;
@@ -396,8 +412,9 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t
     }
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const int64_t p = p0 + wp * 64 + 16 * nt + i;
-      xb[nt] = (p < P) ? ld8_bf16_window(ep_b + p * ep_ld, 32 * ks + 8 * g - slot_shift, ep_lim, (ep_ld % 8) == 0)
+      const int64_t p = kGated ? gated_row(p0, wp * 64 + 16 * nt + i, P / 2) : p0 + wp * 64 + 16 * nt + i;
+      const int shift = kGated ? (nt >> 1) * lp.rpart : slot_shift;  // up's slots follow gate's
+      xb[nt] = (p < P) ? ld8_bf16_window(ep_b + p * ep_ld, 32 * ks + 8 * g - shift, ep_lim, (ep_ld % 8) == 0)
                        : u32x4{0, 0, 0, 0};
     }
     mma(xa, xb);
@@ -410,6 +427,46 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t
   // 128-byte row runs, 16 bytes per lane. Lane holds out[m = .. + i][p = .. + 4g .. 4g+3].
   constexpr int kEpRow = 72;
   uint16_t* ep = As + wave * (128 * kEpRow);
+  if constexpr (kGated) {
+    // tiles are whole (the parts are multiples of 256 rows); 32 outputs of a
+    // wave and token: a run of 64 bytes
+    const int rr = lane >> 3, cc = lane & 7, r4 = lane >> 2, c4 = lane & 3;
+    if (out != nullptr) {
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          const f32x4 c = acc[nt][mt];
+          *reinterpret_cast<u32x2*>(ep + (16 * mt + i) * kEpRow + 16 * nt + 4 * g) =
+              u32x2{cvt_16x2<kF16>(c[0], c[1]), cvt_16x2<kF16>(c[2], c[3])};
+        }
+      const int64_t col = gated_row(p0, wp * 64 + 8 * cc, P / 2);
+#pragma unroll
+      for (int it = 0; it < 16; ++it) {
+        const u32x4 v = ld16(ep + (8 * it + rr) * kEpRow + 8 * cc);
+        const int64_t m = m0 + wm * 128 + 8 * it + rr;
+        if (m < M) *reinterpret_cast<u32x4*>(out + m * P + col) = v;
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_value<false>(acc[nt][mt][e], gate.act) * acc[nt + 2][mt][e];
+        *reinterpret_cast<u32x2*>(ep + (16 * mt + i) * kEpRow + 16 * nt + 4 * g) =
+            u32x2{cvt_16x2<kF16>(v[0], v[1]), cvt_16x2<kF16>(v[2], v[3])};
+      }
+    const int64_t pcol = p0 / 2 + wp * 32 + 8 * c4;
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const u32x4 v = ld16(ep + (16 * it + r4) * kEpRow + 8 * c4);
+      const int64_t m = m0 + wm * 128 + 16 * it + r4;
+      if (m < M) *reinterpret_cast<u32x4*>(gate.p + m * (P / 2) + pcol) = v;
+    }
+    return;
+  }
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -438,7 +495,19 @@ hipError_t launch_gemm_fwd(const PackedW& w, const uint16_t* x, int64_t m, const
   auto kern = f16 ? (w.dq ? nf4_gemm_kernel<false, true, true> : nf4_gemm_kernel<false, false, true>)
                   : (w.dq ? nf4_gemm_kernel<false, true, false> : nf4_gemm_kernel<false, false, false>);
   hipLaunchKernelGGL(kern, dim3(tiles(m, w.n)), dim3(512), 0, st, w, x, m, w.n, w.k, hs, b, static_cast<int64_t>(r), r,
-                     rpad, parts, y, codebook_table(w.codebook));
+                     rpad, parts, y, codebook_table(w.codebook), GateOut{});
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* hs, const uint16_t* b,
+                             int rpart, int rpad, int act, uint16_t* y, uint16_t* p, hipStream_t st, bool f16) {
+  auto kern = f16 ? (w.dq ? nf4_gemm_kernel<false, true, true, true> : nf4_gemm_kernel<false, false, true, true>)
+                  : (w.dq ? nf4_gemm_kernel<false, true, false, true> : nf4_gemm_kernel<false, false, false, true>);
+  LoraParts lp;
+  lp.g = 2;
+  lp.rpart = rpart;
+  hipLaunchKernelGGL(kern, dim3(tiles(m, w.n)), dim3(512), 0, st, w, x, m, w.n, w.k, hs, b,
+                     static_cast<int64_t>(rpart), rpart, rpad, lp, y, codebook_table(w.codebook), GateOut{p, act});
   return hipGetLastError();
 }
 
@@ -447,7 +516,7 @@ hipError_t launch_gemm_dx(const PackedW& w, const uint16_t* dy, int64_t m, const
   auto kern = f16 ? (w.dq ? nf4_gemm_kernel<true, true, true> : nf4_gemm_kernel<true, false, true>)
                   : (w.dq ? nf4_gemm_kernel<true, true, false> : nf4_gemm_kernel<true, false, false>);
   hipLaunchKernelGGL(kern, dim3(tiles(m, w.k)), dim3(512), 0, st, w, dy, m, w.k, w.n, dhs, at,
-                     static_cast<int64_t>(rpad), rpad, rpad, LoraParts{}, dx, codebook_table(w.codebook));
+                     static_cast<int64_t>(rpad), rpad, rpad, LoraParts{}, dx, codebook_table(w.codebook), GateOut{});
   return hipGetLastError();
 }
 

@@ -17,8 +17,15 @@
 //     (2670 TOP/s); the matrix cores are busy 68% of the cycles, at 1.8 GHz. With
 //     v_mfma_i32_32x32x32_i8 in 128 x 128 tiles a wave (a third fewer LDS reads)
 //     the cycles are as many, at 1.64 GHz: 236 us.
+//
+// The kernels built with kGated compute a gated feed-forward block, whose weight
+// holds gate's rows above up's: P = act(gate) up. Eight of the weight rows that a
+// lane ends with are gate's and eight the up rows of the same outputs, so the
+// product is formed where the sums are, and the pre-activations never leave the
+// registers.
 #include "bufmem.h"
 #include "elem.h"
+#include "gate.h"
 #include "int8_tiles.h"
 
 namespace qlora {
@@ -42,6 +49,9 @@ struct LinearArgs {
   void* y;
   int64_t m, n, k;
   int64_t ldy;  // a row of y; n but for a part of the channels
+  // gated: n counts outputs, and output j's weight rows are w's rows j and j + up
+  int64_t up;
+  int act;
 };
 
 // ---------------------------------------------------------------------------
@@ -82,6 +92,27 @@ __device__ __forceinline__ void store_run(typename Elem<kType>::T* y, const i32x
   }
 }
 
+// Eight outputs of a gated block of one token: gate's sums in acc[0], acc[1], up's
+// in acc[2], acc[3].
+template <int kType>
+__device__ __forceinline__ void store_gated(typename Elem<kType>::T* y, const i32x4* acc, float sx, const float* sw,
+                                            int act, int64_t left) {
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float gate = (static_cast<float>(acc[e >> 2][e & 3]) * sx) * sw[e];
+    const float up = (static_cast<float>(acc[2 + (e >> 2)][e & 3]) * sx) * sw[8 + e];
+    f[e] = act_value<kType == QLORA_F32>(gate, act) * up;
+  }
+  if (left >= 8) {
+    put8<kType>(y, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) y[e] = Elem<kType>::put(f[e]);
+  }
+}
+
 // 1 KB global -> LDS: lane l's 16 bytes at byte offset `off` to dst + 16 l.
 __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t src, int8_t* dst, int off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)dst, 16, off, 0, 0, 0);
@@ -96,7 +127,9 @@ __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t src, int8_t* dst,
 // a ring of its own; their sums are added through LDS at the end. For tiles so
 // small that one group keeps too few copies in flight (128 x 4096 x 4096 in 32
 // x 64 tiles: 8.6 us with two groups).
-template <int BM, int BN, int WM, int WN, int KS, int P, int kType>
+// kGated: BN weight rows are BN / 2 outputs; blocks of eight rows of the channels'
+// part are gate's and up's in turn.
+template <int BM, int BN, int WM, int WN, int KS, int P, int kType, bool kGated>
 __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave: tokens, channels
@@ -138,16 +171,21 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   const uint32_t b0 = lin / band * 8, in = lin % band;
   const uint32_t rows = static_cast<uint32_t>(tiles_m) - b0 < 8 ? static_cast<uint32_t>(tiles_m) - b0 : 8;
   const int64_t m0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(b0 + in % rows)) * BM;
-  const int64_t n0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(in / rows)) * BN;
+  constexpr int BO = kGated ? BN / 2 : BN;  // outputs of a tile
+  const int64_t n0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(in / rows)) * BO;
 
   // This group's units [u0, u0 + turns): the same number for all groups, the
   // last ones' past the end of the contraction.
   const int units = static_cast<int>((g.k + kUnit - 1) / kUnit);
   const int turns = (units + KS - 1) / KS, u0 = group * turns;
-  const int mrows = static_cast<int>(g.m - m0 < BM ? g.m - m0 : BM), nrows = static_cast<int>(g.n - n0 < BN ? g.n - n0 : BN);
+  const int mrows = static_cast<int>(g.m - m0 < BM ? g.m - m0 : BM), nrows = static_cast<int>(g.n - n0 < BO ? g.n - n0 : BO);
   // Ranges of the tile's own rows: what is read at an offset past them is zero.
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + m0 * g.k, mrows * g.k);
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + n0 * g.k, nrows * g.k);
+  // Gated: the odd blocks of eight rows are up's. Where the waves are even in
+  // number a wave copies blocks of one parity alone.
+  constexpr bool kEven = kWaves % 2 == 0;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (n0 + (kGated && kEven && (wave & 1) ? g.up : 0)) * g.k, nrows * g.k);
+  const __amdgpu_buffer_rsrc_t ur = make_rsrc(g.w + (n0 + (kGated && !kEven ? g.up : 0)) * g.k, nrows * g.k);
 
   // Copy l of a wave fills block l kWaves + wave of a part: 8 rows of 128
   // bytes, lane l the 16 bytes at row l / 8, place l % 8. A row's chunk c
@@ -162,7 +200,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   for (int l = 0; l < LX; ++l) xc[l] = 16 * (lc ^ ((lr >> 1) + 4 * ((l * kWaves + wave) & 1)));
 #pragma unroll
   for (int l = 0; l < LW; ++l)
-    wo[l] = (8 * wave + lr) * k32 + 16 * (lc ^ (2 * (((l * kWaves + wave) >> 1) & 3) + ((lr >> 1) & 1)));
+    wo[l] = ((kGated ? 8 * (wave >> 1) : 8 * wave) + lr) * k32 + 16 * (lc ^ (2 * (((l * kWaves + wave) >> 1) & 3) + ((lr >> 1) & 1)));
   const int xrow = (8 * wave + lr) * k32;
   // Codes behind the contraction's end (in the second half of its last unit,
   // and in units past it) become zeros on the tokens' side, so their products
@@ -179,7 +217,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
     const int q = (u0 + u < units ? u0 + u : units - 1) * kUnit;
 #pragma unroll
     for (int l = 0; l < LW; ++l)
-      copy_1k(wr, to + (group * BN / 8 + l * kWaves + wave) * 1024, wo[l] + (8 * l * kWaves * k32 + q));
+      copy_1k(kGated && !kEven && (l & 1) ? ur : wr, to + (group * BN / 8 + l * kWaves + wave) * 1024,
+              wo[l] + (8 * (kGated ? l * kWaves >> 1 : l * kWaves) * k32 + q));
   };
   // Fragments of a unit's first or second 64 codes. Token tile t reads rows
   // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,
@@ -247,9 +286,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   constexpr bool kEarly = TM * TN <= 16;
   float sx[TM], sw[kEarly ? TN / 4 : 1][16];
   auto load_scales = [&](int c) {
-    const int64_t nc = n0 + wn * TN * 16 + 64 * c + 16 * h;
+    const int64_t nc = kGated ? n0 + wn * TN * 8 + 32 * c + 8 * h : n0 + wn * TN * 16 + 64 * c + 16 * h;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sw[kEarly ? c : 0][e] = g.sw[nc + e < g.n ? nc + e : g.n - 1];
+    for (int e = 0; e < 16; ++e) {
+      const int64_t row = nc + (kGated ? e & 7 : e);
+      sw[kEarly ? c : 0][e] = g.sw[(row < g.n ? row : g.n - 1) + (kGated && e >= 8 ? g.up : 0)];
+    }
     if (c > 0) return;
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
@@ -312,24 +354,29 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void tile_kernel(LinearArgs g, i
   T* y = static_cast<T*>(g.y);
 #pragma unroll
   for (int c = 0; c < TN / 4; ++c) {
-    const int64_t nc = n0 + wn * TN * 16 + 64 * c + 16 * h;
+    const int64_t nc = kGated ? n0 + wn * TN * 8 + 32 * c + 8 * h : n0 + wn * TN * 16 + 64 * c + 16 * h;
     if (!kEarly) load_scales(c);
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
       const int64_t m = m0 + wm * TM * 16 + 16 * a + i;
-      if (m < g.m) store_run<kType>(y + m * g.ldy + nc, acc[a] + 4 * c, sx[a], sw[kEarly ? c : 0], g.n - nc);
+      if (m >= g.m) continue;
+      if constexpr (kGated)
+        store_gated<kType>(y + m * g.ldy + nc, acc[a] + 4 * c, sx[a], sw[kEarly ? c : 0], g.act, g.n - nc);
+      else
+        store_run<kType>(y + m * g.ldy + nc, acc[a] + 4 * c, sx[a], sw[kEarly ? c : 0], g.n - nc);
     }
   }
 }
 
-template <int I>
+template <int I, bool kGated>
 hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
   constexpr Shape t = kShapes[I];
   constexpr int BM = t.bm, BN = t.bn, WM = t.wm, WN = t.wn, KS = t.groups, P = t.parts;
-  const int tiles_m = static_cast<int>((g.m + BM - 1) / BM), tiles_n = static_cast<int>((g.n + BN - 1) / BN);
-  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F32>
-              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F16>
-                                       : tile_kernel<BM, BN, WM, WN, KS, P, QLORA_BF16>;
+  const int tiles_m = static_cast<int>((g.m + BM - 1) / BM), BO = kGated ? BN / 2 : BN;
+  const int tiles_n = static_cast<int>((g.n + BO - 1) / BO);
+  auto kern = out_dtype == QLORA_F32   ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F32, kGated>
+              : out_dtype == QLORA_F16 ? tile_kernel<BM, BN, WM, WN, KS, P, QLORA_F16, kGated>
+                                       : tile_kernel<BM, BN, WM, WN, KS, P, QLORA_BF16, kGated>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles_m) * tiles_n), dim3(t.threads()), 0, s, g, tiles_m, tiles_n);
   return hipGetLastError();
 }
@@ -355,14 +402,18 @@ hipError_t launch_tiles(const LinearArgs& g, int out_dtype, hipStream_t s) {
 constexpr int kDecodeWaves = 8;
 constexpr int kDecodeSteps = 4;  // 64-code steps of a wave a pass
 
-template <int kType>
+// kGated: 8 gate rows and the 8 up rows of the same outputs.
+template <int kType, bool kGated>
 __global__ __launch_bounds__(64 * kDecodeWaves) void decode_kernel(LinearArgs g) {
   __shared__ int part[kDecodeWaves][256];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (kGated ? 8 : 16);
   const int steps = static_cast<int>(g.k / 64);
-  const int8_t* wp = g.w + (n0 + i < g.n ? n0 + i : g.n - 1) * g.k + 16 * h;
+  // channel c's output and, gated, weight row
+  auto output = [&](int c) { return n0 + (kGated ? c & 7 : c); };
+  auto row = [&](int c) { return (output(c) < g.n ? output(c) : g.n - 1) + (kGated && c >= 8 ? g.up : 0); };
+  const int8_t* wp = g.w + row(i) * g.k + 16 * h;
   const int8_t* xp = g.x + (i < g.m ? i : g.m - 1) * g.k + 16 * h;
   i32x4 acc = {0, 0, 0, 0};
   for (int base = 0; base < steps; base += kDecodeWaves * kDecodeSteps) {
@@ -386,41 +437,70 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void decode_kernel(LinearArgs g)
   __syncthreads();
   // output tid: token tid / 16, channel tid % 16
   const int tok = tid >> 4, ch = tid & 15;
-  if (tid >= 256 || tok >= g.m || n0 + ch >= g.n) return;
+  if (tid >= 256 || tok >= g.m || output(ch) >= g.n) return;
   const int at = 4 * (tok + 16 * (ch >> 2)) + (ch & 3);
   int sum = 0;
 #pragma unroll
   for (int w = 0; w < kDecodeWaves; ++w) sum += part[w][at];
-  static_cast<typename Elem<kType>::T*>(g.y)[tok * g.ldy + n0 + ch] =
-      Elem<kType>::put((static_cast<float>(sum) * g.sx[tok]) * g.sw[n0 + ch]);
+  float v = (static_cast<float>(sum) * g.sx[tok]) * g.sw[row(ch)];
+  if (kGated) {
+    const float up = __shfl_xor(v, 8, 64);
+    if (ch >= 8) return;
+    v = act_value<kType == QLORA_F32>(v, g.act) * up;
+  }
+  static_cast<typename Elem<kType>::T*>(g.y)[tok * g.ldy + output(ch)] = Elem<kType>::put(v);
 }
 
+template <bool kGated>
 hipError_t launch_decode(const LinearArgs& g, int out_dtype, hipStream_t s) {
-  auto kern = out_dtype == QLORA_F32   ? decode_kernel<QLORA_F32>
-              : out_dtype == QLORA_F16 ? decode_kernel<QLORA_F16>
-                                       : decode_kernel<QLORA_BF16>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((g.n + 15) / 16)), dim3(64 * kDecodeWaves), 0, s, g);
+  constexpr int kOut = kGated ? 8 : 16;
+  auto kern = out_dtype == QLORA_F32   ? decode_kernel<QLORA_F32, kGated>
+              : out_dtype == QLORA_F16 ? decode_kernel<QLORA_F16, kGated>
+                                       : decode_kernel<QLORA_BF16, kGated>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((g.n + kOut - 1) / kOut)), dim3(64 * kDecodeWaves), 0, s, g);
   return hipGetLastError();
 }
 
+template <bool kGated>
 hipError_t launch_shape(int shape, const LinearArgs& g, int out_dtype, hipStream_t s) {
   switch (shape) {
     case 0:
-      return launch_tiles<0>(g, out_dtype, s);
+      return launch_tiles<0, kGated>(g, out_dtype, s);
     case 1:
-      return launch_tiles<1>(g, out_dtype, s);
+      return launch_tiles<1, kGated>(g, out_dtype, s);
     case 2:
-      return launch_tiles<2>(g, out_dtype, s);
+      return launch_tiles<2, kGated>(g, out_dtype, s);
     case 3:
-      return launch_tiles<3>(g, out_dtype, s);
+      return launch_tiles<3, kGated>(g, out_dtype, s);
     case 4:
-      return launch_tiles<4>(g, out_dtype, s);
+      return launch_tiles<4, kGated>(g, out_dtype, s);
     case 5:
-      return launch_tiles<5>(g, out_dtype, s);
+      return launch_tiles<5, kGated>(g, out_dtype, s);
     case 6:
-      return launch_tiles<6>(g, out_dtype, s);
+      return launch_tiles<6, kGated>(g, out_dtype, s);
   }
   return hipErrorInvalidValue;  // int8_linear_fits refuses these sizes
+}
+
+// The rules count weight rows, two of a gated output.
+template <bool kGated>
+hipError_t launch_product(LinearArgs g, int out_dtype, hipStream_t s) {
+  constexpr int kOf = kGated ? 2 : 1;
+  if (decodes(g.m, kOf * g.n)) return launch_decode<kGated>(g, out_dtype, s);
+  const Pick one = pick_shape(g.m, kOf * g.n, g.k);
+  const int64_t cols = full_rounds(g.m, kOf * g.n, g.k, one) / kOf;
+  if (cols > 0) {
+    const int64_t n = g.n;
+    g.n = cols;
+    const hipError_t e = launch_shape<kGated>(0, g, out_dtype, s);
+    if (e != hipSuccess) return e;
+    g.w += cols * g.k;
+    g.sw += cols;
+    g.y = static_cast<char*>(g.y) + cols * (out_dtype == QLORA_F32 ? 4 : 2);
+    g.n = n - cols;
+    return launch_shape<kGated>(pick_shape(g.m, kOf * g.n, g.k).shape, g, out_dtype, s);
+  }
+  return launch_shape<kGated>(one.shape, g, out_dtype, s);
 }
 
 }  // namespace
@@ -429,21 +509,12 @@ bool int8_linear_fits(int64_t m, int64_t n, int64_t k) { return decodes(m, n) ||
 
 hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
                               const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s) {
-  LinearArgs g{w, w_scale, x, x_scale, y, m, n, k, n};
-  if (decodes(m, n)) return launch_decode(g, out_dtype, s);
-  const Pick one = pick_shape(m, n, k);
-  const int64_t cols = full_rounds(m, n, k, one);
-  if (cols > 0) {
-    g.n = cols;
-    const hipError_t e = launch_shape(0, g, out_dtype, s);
-    if (e != hipSuccess) return e;
-    g.w = w + cols * k;
-    g.sw = w_scale + cols;
-    g.y = static_cast<char*>(y) + cols * (out_dtype == QLORA_F32 ? 4 : 2);
-    g.n = n - cols;
-    return launch_shape(pick_shape(m, g.n, k).shape, g, out_dtype, s);
-  }
-  return launch_shape(one.shape, g, out_dtype, s);
+  return launch_product<false>(LinearArgs{w, w_scale, x, x_scale, y, m, n, k, n, 0, 0}, out_dtype, s);
+}
+
+hipError_t launch_int8_gated(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
+                             const float* x_scale, int64_t m, int act, int out_dtype, void* p, hipStream_t s) {
+  return launch_product<true>(LinearArgs{w, w_scale, x, x_scale, p, m, n, k, n, n, act}, out_dtype, s);
 }
 
 }  // namespace qlora

@@ -98,6 +98,13 @@ struct LoraParts {
   int end[4] = {0, 0, 0, 0};
 };
 
+// The product of a gated feed-forward block, P = act(gate) up, m x (w.n / 2) of
+// the compute type; p null: an ordinary linear.
+struct GateOut {
+  uint16_t* p = nullptr;
+  int act = 0;  // QLORA_ACT_*
+};
+
 // Decode GEMV, m <= 16: y = x W16^T + s * h B^T in one launch when
 // gemv_fuses_h(n, k, r, parts) (H = x A^T computed in the kernel from a);
 // otherwise hpart holds hsplits partial sums of H (hsplits x m x r float32,
@@ -114,9 +121,11 @@ hipError_t launch_gemv(const PackedW& w, const uint16_t* x, int64_t m, const uin
                        int hsplits, const uint16_t* b, int r, float s, uint16_t* y, float* h_out, hipStream_t st,
                        bool f16 = false, const LoraParts* parts = nullptr);
 // The matrix-core form (3..16 tokens, or k > 4096); same arguments as launch_gemv.
+// H is fused where hpart is null (r <= 16). With gate.p, w's parts are gate's
+// rows above up's, and y may be null.
 hipError_t launch_gemv_mfma(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* a, const float* hpart,
                             int hsplits, const uint16_t* b, int r, float s, uint16_t* y, float* h_out, hipStream_t st,
-                            bool f16, const LoraParts* parts);
+                            bool f16, const LoraParts* parts, GateOut gate = {});
 
 // Fused dequant-GEMM, forward: y = x W16^T + the LoRA term where hs is bf16
 // m x rpad (already scaled by s) and b is n x r bf16 (r = slots per part);
@@ -124,6 +133,12 @@ hipError_t launch_gemv_mfma(const PackedW& w, const uint16_t* x, int64_t m, cons
 hipError_t launch_gemm_fwd(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* hs,
                            const uint16_t* b, int r, int rpad, const LoraParts& parts, uint16_t* y, hipStream_t st,
                            bool f16 = false);
+
+// The same for a gated block (w: gate's rows above up's, each a multiple of 64):
+// p = act(gate) up from the float32 sums, and y, the pre-activations, unless it
+// is null.
+hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* hs, const uint16_t* b,
+                             int rpart, int rpad, int act, uint16_t* y, uint16_t* p, hipStream_t st, bool f16);
 
 // Fused dequant-GEMM, backward data: dx = dy W16 + dhs At where dhs is bf16
 // m x rpad and at is bf16 k x rpad (A transposed, zero padded).
@@ -180,6 +195,15 @@ hipError_t launch_rank_grads(const float* dh, const uint16_t* x, int64_t k, cons
                              int64_t n, int64_t m, int r0, const LoraParts* parts, float scale, int splits, float* part,
                              float* da, float* db, hipStream_t st, bool f16 = false);
 
+// The same gradients of an input kept as 8-bit rows (m rows of ldx codes, scales
+// xscale): da (slots x k), slots = g r; db (n x r), times scale. Any r. part
+// holds splits x (slots k + r n) float32, none of which is used with one split.
+int rank_grad8_splits(int64_t m, int64_t n, int64_t k, int slots, int r);
+hipError_t launch_rank_grads8(const float* dh, const int8_t* x, int64_t ldx, const float* xscale, int64_t k,
+                              const float* h, const uint16_t* dy, int64_t n, int64_t m, int slots,
+                              const LoraParts* parts, float scale, float* part, float* da, float* db, hipStream_t st,
+                              bool f16);
+
 // The plain forward (qlora_linear_fwd) on a scratch area the caller
 // provides, checked against the forward's own workspace layout
 // (linear_fwd_scratch_bytes) rather than the two-direction size of the
@@ -203,10 +227,20 @@ hipError_t launch_rmsnorm_int8(const void* x, const void* residual, const void* 
                                int64_t rows, int64_t cols, float eps, void* residual_out, int8_t* codes, int64_t ld,
                                float* scale, hipStream_t s);
 
+// The product of a gated block alone (dp null) or its gradient, from rows x 2 n
+// pre-activations y, or (codes not null) 2 rows 8-bit rows of n.
+hipError_t launch_gated(const void* y, const int8_t* codes, int64_t ld, const float* scale, const void* dp, int dtype,
+                        int64_t rows, int64_t n, int act, void* out, hipStream_t s);
+
 // The 8-bit product, for sizes whose launch stays below 2^32 work items.
 bool int8_linear_fits(int64_t m, int64_t n, int64_t k);
 hipError_t launch_int8_linear(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
                               const float* x_scale, int64_t m, int out_dtype, void* y, hipStream_t s);
+
+// P = act(gate) up of a gated block: w holds n rows of gate above n of up, for
+// sizes that int8_linear_fits(m, 2 n, k) takes.
+hipError_t launch_int8_gated(const int8_t* w, const float* w_scale, int64_t n, int64_t k, const int8_t* x,
+                             const float* x_scale, int64_t m, int act, int out_dtype, void* p, hipStream_t s);
 
 // Global norm of a list of tensors and (clip) their scaling: out null writes
 // in place. ws holds grad_ws_bytes(numel, count).

@@ -1,0 +1,278 @@
+// Both adapter gradients of a linear whose input was kept as 8-bit rows:
+//   dA = dH^T X, X[m][c] = code[m][c] scale[m]  (slots x k)
+//   dB = s dY^T H                               (n x r)
+// as one launch over two problems out[j][c] = sum_m U[m][j] V[m][c], U float32
+// (dH times the row's scale; H) and V the codes (exact in bf16) or dY.
+//
+// Bound by reading V once: k + 2 n bytes a token, half the 16-bit input's.
+// 2048 tokens: k = 11008, n = 4096 holds 39 MB.
+//
+// Matrix cores in bf16 with float32 sums (v_mfma_f32_16x16x32_bf16), every
+// float32 U split into three bf16 terms that hold all of its 24 bits (the low 16
+// bits cut off twice, the rest rounded); an fp16 dY is split into two, its upper
+// eight bits and the other three, both exact. So no product is rounded, and the
+// gradients are float32 sums. The extra products are free next to the memory.
+//
+// No LDS on the way in: a contraction step is 32 rows; lane (i, g) loads 8 columns
+// of rows 8 g .. 8 g + 7 (whole 128- or 256-byte runs of a row for its 16 lanes)
+// and element t of the 8 rows is its operand for the tile of columns 8 i + t.
+// A workgroup takes 128 columns and 16 or 32 slots; its eight waves take the
+// steps of its rows in turn, and their sums meet in LDS in wave order. Few columns
+// are split over the rows as well, into partial sums that are added in order by a
+// second launch; results repeat bit for bit.
+#include <type_traits>
+
+#include "internal.h"
+#include "mfma.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kCols = 128, kRows = 32, kWaves = 8, kThreads = 64 * kWaves;
+
+enum VKind { kCodes, kBf16, kHalf };
+
+struct Problem {
+  const float* u;       // m x ldu
+  const float* uscale;  // m, or null
+  const void* v;        // m x ldv
+  float* out;           // splits x slots x cn partial sums (one split: dA itself)
+  float* db;            // one split: cn x slots, times scale
+  float scale;
+  int64_t cn, ldv;
+  int ldu;
+  int slots;  // of a column
+  int strips, tiles;  // workgroups along the columns and the slots
+  LoraParts lp;       // dB of grouped weights: a column's part owns slots from part rpart on
+};
+
+// Eight rows' 8 columns as loaded.
+template <int kKind>
+struct Block {
+  typedef typename std::conditional<kKind == kCodes, u32x2, u32x4>::type Word;
+  Word w[8];
+};
+
+// Element t of the eight rows as bf16 pairs; kHalf: its upper bits, and in `low`
+// the rest.
+template <int kKind>
+__device__ __forceinline__ u32x4 operand(const Block<kKind>& b, int t, u32x4* low) {
+  uint32_t hi[4], lo[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (kKind == kCodes) {
+      const float f0 = static_cast<float>(static_cast<int8_t>(b.w[2 * e][t >> 2] >> (8 * (t & 3))));
+      const float f1 = static_cast<float>(static_cast<int8_t>(b.w[2 * e + 1][t >> 2] >> (8 * (t & 3))));
+      hi[e] = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);  // exact: 8 bits
+    } else if constexpr (kKind == kBf16) {
+      hi[e] = __builtin_amdgcn_perm(b.w[2 * e + 1][t >> 1], b.w[2 * e][t >> 1], (t & 1) ? 0x07060302u : 0x05040100u);
+    } else {
+      const uint32_t w0 = b.w[2 * e][t >> 1], w1 = b.w[2 * e + 1][t >> 1];
+      const float f0 = (t & 1) ? hi16<true>(w0) : lo16<true>(w0), f1 = (t & 1) ? hi16<true>(w1) : lo16<true>(w1);
+      hi[e] = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
+      const float l0 = f0 - __uint_as_float(__float_as_uint(f0) & 0xFFFF0000u);
+      const float l1 = f1 - __uint_as_float(__float_as_uint(f1) & 0xFFFF0000u);
+      lo[e] = __builtin_amdgcn_perm(__float_as_uint(l1), __float_as_uint(l0), 0x07060302u);
+    }
+  }
+  if (kKind == kHalf) *low = u32x4{lo[0], lo[1], lo[2], lo[3]};
+  return u32x4{hi[0], hi[1], hi[2], hi[3]};
+}
+
+// The three bf16 terms of eight float32.
+struct Terms {
+  u32x4 t[3];
+};
+__device__ __forceinline__ Terms split3(const float* u) {
+  Terms r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t h[2], m[2], l[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float f = u[2 * e + q];
+      h[q] = __float_as_uint(f);
+      const float f1 = f - __uint_as_float(h[q] & 0xFFFF0000u);
+      m[q] = __float_as_uint(f1);
+      l[q] = f32_to_bf16_rne(f1 - __uint_as_float(m[q] & 0xFFFF0000u));
+    }
+    r.t[0][e] = __builtin_amdgcn_perm(h[1], h[0], 0x07060302u);
+    r.t[1][e] = __builtin_amdgcn_perm(m[1], m[0], 0x07060302u);
+    r.t[2][e] = l[0] | l[1] << 16;
+  }
+  return r;
+}
+
+template <int kKind, int RT>
+__device__ __forceinline__ void solve(const Problem& p, int64_t M, int id, int splits, int64_t per, f32x4* red) {
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = id % splits, tile = id / splits % p.tiles, strip = id / splits / p.tiles;
+  const int64_t c0 = static_cast<int64_t>(strip) * kCols;
+  const int j0 = tile * 16 * RT;
+  int part = 0;
+#pragma unroll
+  for (int l = 0; l < 3; ++l) part += (l + 1 < p.lp.g && c0 >= p.lp.end[l]) ? 1 : 0;
+  const float* u = p.u + part * p.lp.rpart;
+  const int64_t mb = split * per, me = mb + per < M ? mb + per : M;
+
+  const int64_t col = c0 + 8 * i < p.cn ? c0 + 8 * i : 0;  // cn % 16 == 0; columns past it are not stored
+  f32x4 acc[RT][8];
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // Rows past the last are read from it and multiplied by zeros.
+  typedef typename Block<kKind>::Word Word;
+  auto load = [&](int64_t m0, Block<kKind>& b, float (&uv)[RT][8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t m = m0 + 8 * g + e;
+      const int64_t mr = m < M ? m : M - 1;
+      const char* row = static_cast<const char*>(p.v) + (mr * p.ldv + col) * (kKind == kCodes ? 1 : 2);
+      b.w[e] = *reinterpret_cast<const Word*>(row);
+      const float sc = p.uscale != nullptr ? p.uscale[mr] : 1.0f;
+#pragma unroll
+      for (int a = 0; a < RT; ++a) {
+        const int j = j0 + 16 * a + i;
+        const float f = u[mr * p.ldu + (j < p.slots ? j : 0)];
+        uv[a][e] = m < me && j < p.slots ? f * sc : 0.0f;
+      }
+    }
+  };
+  Block<kKind> b, nb;
+  float uv[RT][8], nu[RT][8];
+  int64_t m0 = mb + wave * kRows;
+  if (m0 < me) load(m0, b, uv);
+  for (; m0 < me; m0 += kWaves * kRows) {
+    const bool more = m0 + kWaves * kRows < me;
+    if (more) load(m0 + kWaves * kRows, nb, nu);
+    Terms terms[RT];
+#pragma unroll
+    for (int a = 0; a < RT; ++a) terms[a] = split3(uv[a]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      u32x4 low;
+      const u32x4 v = operand<kKind>(b, t, &low);
+#pragma unroll
+      for (int a = 0; a < RT; ++a)
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          acc[a][t] = mma16<false>(terms[a].t[q], v, acc[a][t]);
+          if (kKind == kHalf) acc[a][t] = mma16<false>(terms[a].t[q], low, acc[a][t]);
+        }
+    }
+    if (more) {
+      b = nb;
+#pragma unroll
+      for (int a = 0; a < RT; ++a)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) uv[a][e] = nu[a][e];
+    }
+  }
+
+  // acc[a][t][v]: slot j0 + 16 a + 4 g + v, column c0 + 8 i + t. Thread q sums
+  // slot q / 32, columns 4 (q % 32) .. + 3 of each 16 slots over the waves.
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) red[((wave * RT + a) * 8 + t) * 64 + lane] = acc[a][t];
+  __syncthreads();
+  const float* rf = reinterpret_cast<const float*>(red);
+  const int slot = tid >> 5, c4 = 4 * (tid & 31);
+  const int64_t c = c0 + c4;
+  if (c >= p.cn) return;
+#pragma unroll
+  for (int a = 0; a < RT; ++a) {
+    const int j = j0 + 16 * a + slot;
+    if (j >= p.slots) continue;
+    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum[e] += rf[(((w * RT + a) * 8 + ((c4 + e) & 7)) * 64 + 16 * (slot >> 2) + (c4 >> 3)) * 4 + (slot & 3)];
+    if (p.db != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p.db[(c + e) * p.slots + j] = p.scale * sum[e];
+    } else {
+      *reinterpret_cast<f32x4*>(p.out + (static_cast<int64_t>(split) * p.slots + j) * p.cn + c) = sum;
+    }
+  }
+}
+
+template <bool kF16, int RT>
+__global__ __launch_bounds__(kThreads) void rank_grad8_kernel(Problem pa, Problem pb, int64_t M, int splits, int64_t per) {
+  __shared__ f32x4 red[kWaves * RT * 8 * 64];
+  const int id = blockIdx.x, first = pa.strips * pa.tiles * splits;
+  if (id < first) solve<kCodes, RT>(pa, M, id, splits, per, red);
+  else solve<kF16 ? kHalf : kBf16, RT>(pb, M, id - first, splits, per, red);
+}
+
+// da[j][c] = sum over splits of part0[s][j][c]; db[c][j] = scale times that of
+// part1, both in split order.
+__global__ __launch_bounds__(256) void rank_grad8_final_kernel(const float* part0, const float* part1, int64_t na,
+                                                               int64_t n, int r, int splits, float scale, float* da,
+                                                               float* db) {
+  const int64_t nb = n * r;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (idx >= na + nb) return;
+  const bool second = idx >= na;
+  const float* part = second ? part1 + (idx - na) : part0 + idx;
+  const int64_t step = second ? nb : na;
+  float sum = 0.0f;
+  for (int s = 0; s < splits; ++s) sum += part[s * step];
+  if (!second) {
+    da[idx] = sum;
+    return;
+  }
+  const int64_t j = (idx - na) / n, c = (idx - na) % n;
+  db[c * r + j] = scale * sum;
+}
+
+int slot_tiles(int slots) { return slots > 16 ? 2 : 1; }  // of a workgroup
+
+int64_t workgroups(int64_t n, int64_t k, int slots, int r, int rt) {
+  return (k + kCols - 1) / kCols * ((slots + 16 * rt - 1) / (16 * rt)) +
+         (n + kCols - 1) / kCols * ((r + 16 * rt - 1) / (16 * rt));
+}
+
+}  // namespace
+
+int rank_grad8_splits(int64_t m, int64_t n, int64_t k, int slots, int r) {
+  // about two workgroups a CU, a step at least for each of a workgroup's waves
+  int64_t s = 512 / workgroups(n, k, slots, r, slot_tiles(slots));
+  const int64_t by_rows = m / (kWaves * kRows);
+  if (s > by_rows) s = by_rows;
+  if (s > 16) s = 16;
+  return static_cast<int>(s < 1 ? 1 : s);
+}
+
+hipError_t launch_rank_grads8(const float* dh, const int8_t* x, int64_t ldx, const float* xscale, int64_t k,
+                              const float* h, const uint16_t* dy, int64_t n, int64_t m, int slots,
+                              const LoraParts* parts, float scale, float* part, float* da, float* db, hipStream_t st,
+                              bool f16) {
+  const int r = parts != nullptr ? parts->rpart : slots;
+  const int splits = rank_grad8_splits(m, n, k, slots, r);
+  const int rt = slot_tiles(slots);
+  const int64_t per = ((m + splits - 1) / splits + kRows - 1) / kRows * kRows;
+  float* part1 = part + static_cast<int64_t>(splits) * slots * k;
+  auto strips = [](int64_t c) { return static_cast<int>((c + kCols - 1) / kCols); };
+  const Problem pa{dh, xscale, x, splits == 1 ? da : part, nullptr, 1.0f, k, ldx, slots, slots, strips(k),
+                   (slots + 16 * rt - 1) / (16 * rt), LoraParts{}};
+  const Problem pb{h, nullptr, dy, part1, splits == 1 ? db : nullptr, scale, n, n, slots, r, strips(n),
+                   (r + 16 * rt - 1) / (16 * rt), parts != nullptr ? *parts : LoraParts{}};
+  const unsigned grid = static_cast<unsigned>(workgroups(n, k, slots, r, rt) * splits);
+  auto kern = rt == 1 ? (f16 ? rank_grad8_kernel<true, 1> : rank_grad8_kernel<false, 1>)
+                      : (f16 ? rank_grad8_kernel<true, 2> : rank_grad8_kernel<false, 2>);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), 0, st, pa, pb, m, splits, per);
+  if (splits > 1) {
+    const int64_t na = static_cast<int64_t>(slots) * k, total = na + n * r;
+    hipLaunchKernelGGL(rank_grad8_final_kernel, dim3(static_cast<unsigned>((total + 255) / 256)), dim3(256), 0, st,
+                       part, part1, na, n, r, splits, scale, da, db);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -102,6 +102,9 @@ typedef enum { QLORA_BF16 = 0, QLORA_F32 = 1, QLORA_F16 = 2 } qlora_dtype;
 #define QLORA_DQ_LINEAR8 1 /* 8-bit scale codes k / 255 (default)   */
 #define QLORA_DQ_FLOAT8 2  /* 8-bit float-like scale codes E_c      */
 
+#define QLORA_ACT_SILU 0      /* act(g) = g / (1 + e^-g)                             */
+#define QLORA_ACT_GELU_TANH 1 /* act(g) = g/2 (1 + tanh(sqrt(2/pi)(g + 0.044715 g^3))) */
+
 #define QLORA_CODEBOOK_NF4 0  /* normal-quantile levels (the default)  */
 #define QLORA_CODEBOOK_INT4 1 /* 16 evenly spaced levels on [-1, 1]    */
 
@@ -361,6 +364,108 @@ qlora_status qlora_linear_bwd_grouped_f16(const qlora_nf4_weight* w, int g, cons
  * sizes. Host only, no GPU use. */
 size_t qlora_linear_grouped_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r);
 
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block between a decoder layer's norm and its down
+ * projection, over the adapted gate and up projections ("LoRA y QLoRA en
+ * Profundidad", "Modulos Objetivo"): one call for both projections, the
+ * activation and the product,
+ *   [G | U] = X W^T + s [H_1 B_1^T | H_2 B_2^T],  H_l = X A_l^T,  P = act(G) U.
+ *   w     : gate's rows stacked above up's, as a grouped weight of two equal
+ *           parts (w->n = 2 np, np a multiple of 256).
+ *   a, b  : bf16 (2 r) x k and (2 np) x r, as in the grouped calls; may be NULL
+ *           when r = 0.
+ *   r     : rank of each part, 0 .. QLORA_MAX_RANK / 2; s = fl32(alpha / r).
+ *   act   : QLORA_ACT_SILU or QLORA_ACT_GELU_TANH.
+ *   y     : m x (2 np) output of [G | U] rounded to 16 bits, for the backward;
+ *           NULL where it is not wanted.
+ *   p     : m x np output, formed from the float32 sums of G and U and rounded
+ *           once.
+ *   h_out : float32 m x (2 r), [H_1 | H_2]; may be NULL.
+ *   ws    : qlora_linear_gated_workspace_bytes(m, w->n, k, r) bytes.
+ * Outputs and workspace overlap neither an input nor each other. The backward is
+ * qlora_gated_bwd for d[G | U], then qlora_linear_bwd_grouped. m = 0 is a no-op.
+ * Errors: NULL / ALIGN / SHAPE (as qlora_linear_fwd; w->n % 512 != 0) / UNSUPPORTED
+ * (act, r, overlapping buffers) / WORKSPACE / HIP. The _f16 call has IEEE half
+ * as its 16-bit type. */
+qlora_status qlora_linear_fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int64_t m,
+                                    const uint16_t* a, const uint16_t* b, int r, float alpha,
+                                    int act, uint16_t* y, uint16_t* p, float* h_out, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
+qlora_status qlora_linear_fwd_gated_f16(const qlora_nf4_weight* w, const uint16_t* x, int64_t m,
+                                        const uint16_t* a, const uint16_t* b, int r, float alpha,
+                                        int act, uint16_t* y, uint16_t* p, float* h_out, void* ws,
+                                        size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of the two calls above (n = w->n, both parts' rows); 0 if none
+ * is needed and for invalid sizes. Host only, no GPU use. */
+size_t qlora_linear_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int r);
+
+/* The block's product alone and its gradient, element by element in float32:
+ *   P = act(G) U;    dG = dP U act'(G),  dU = dP act(G).
+ * The pre-activations come as y (m x 2 n of `dtype`, [G | U]) or, in the _x8
+ * calls, as the 8-bit rows of qlora_int8_quantize over y taken as 2 m rows of n
+ * values: row 2 i holds token i's gate, row 2 i + 1 its up (2 m x ld codes, 2 m
+ * scales; ld as there).
+ *   dtype  : QLORA_BF16, QLORA_F16 or QLORA_F32, of y, dp and the outputs.
+ *   p      : m x n.    dp : m x n.    dy : m x 2 n, [dG | dU]; may be y itself.
+ *   m 0 .. 2^30 - 1 (0: nothing is done), n 1 .. QLORA_INT8_MAX_COLS.
+ * Any value is taken: a NaN gate gives NaN, a gate of -infinity its limit (act -0,
+ * act' 0), one of +infinity act infinity and act' 1.
+ * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (dtype, act, outputs that overlap an
+ * input in any other way) / HIP. */
+qlora_status qlora_gated_fwd(const void* y, int dtype, int64_t m, int64_t n, int act, void* p,
+                             hipStream_t stream);
+qlora_status qlora_gated_fwd_x8(const int8_t* codes, int64_t ld, const float* scale, int dtype,
+                                int64_t m, int64_t n, int act, void* p, hipStream_t stream);
+qlora_status qlora_gated_bwd(const void* y, const void* dp, int dtype, int64_t m, int64_t n, int act,
+                             void* dy, hipStream_t stream);
+qlora_status qlora_gated_bwd_x8(const int8_t* codes, int64_t ld, const float* scale, const void* dp,
+                                int dtype, int64_t m, int64_t n, int act, void* dy,
+                                hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The backward calls for an input that the forward pass kept as 8-bit rows
+ * (qlora_int8_quantize: half the memory of a 16-bit checkpoint). With
+ * X[i][q] = x[i][q] x_scale[i]:
+ *   dA = dH^T X, dB = s dY^T H, dX = dY W16 + dH A
+ * as in qlora_linear_bwd (qlora_linear_bwd_grouped), the products of dA and dB
+ * in float32 sums of unrounded products.
+ *   x, ldx, x_scale : m rows of k codes, ldx the row length (ldx % 64 == 0, k ..
+ *                     QLORA_INT8_MAX_COLS), and their scales. A row whose scale
+ *                     is NaN makes dA NaN.
+ *   h               : float32 m x r (m x (g r)), from the forward's h_out;
+ *                     required (H is not formed again from rounded rows).
+ *   ws              : qlora_linear_x8_workspace_bytes(m, n, k, g, r) bytes (g = 1
+ *                     for the plain calls).
+ * The other arguments, limits and errors are those of the calls with a 16-bit
+ * input; UNSUPPORTED also for outputs or a workspace that overlap an input or
+ * each other, SHAPE for a bad ldx. With r = 0 the rows are not read. */
+qlora_status qlora_linear_bwd_x8(const qlora_nf4_weight* w, const int8_t* x, int64_t ldx,
+                                 const float* x_scale, const uint16_t* dy, int64_t m,
+                                 const uint16_t* a, const uint16_t* b, int r, float alpha,
+                                 const float* h, uint16_t* dx, float* da, float* db, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+qlora_status qlora_linear_bwd_x8_f16(const qlora_nf4_weight* w, const int8_t* x, int64_t ldx,
+                                     const float* x_scale, const uint16_t* dy, int64_t m,
+                                     const uint16_t* a, const uint16_t* b, int r, float alpha,
+                                     const float* h, uint16_t* dx, float* da, float* db, void* ws,
+                                     size_t ws_bytes, hipStream_t stream);
+qlora_status qlora_linear_bwd_grouped_x8(const qlora_nf4_weight* w, int g, const int64_t* parts,
+                                         const int8_t* x, int64_t ldx, const float* x_scale,
+                                         const uint16_t* dy, int64_t m, const uint16_t* a,
+                                         const uint16_t* b, int r, float alpha, const float* h,
+                                         uint16_t* dx, float* da, float* db, void* ws,
+                                         size_t ws_bytes, hipStream_t stream);
+qlora_status qlora_linear_bwd_grouped_x8_f16(const qlora_nf4_weight* w, int g, const int64_t* parts,
+                                             const int8_t* x, int64_t ldx, const float* x_scale,
+                                             const uint16_t* dy, int64_t m, const uint16_t* a,
+                                             const uint16_t* b, int r, float alpha, const float* h,
+                                             uint16_t* dx, float* da, float* db, void* ws,
+                                             size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of the four calls above; 0 for invalid sizes. Host only. */
+size_t qlora_linear_x8_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r);
+
 /* Merge a trained adapter into the weight: out (n x k, row-major) =
  * fl32(W16 + t), where W16 is the bf16 dequantized weight (as
  * qlora_nf4_dequantize), t = fl32(s d), s = fl32(alpha / r), and d is the
@@ -477,6 +582,20 @@ qlora_status qlora_rmsnorm_int8(const void* x, const void* residual, const void*
 qlora_status qlora_int8_linear_fwd(const int8_t* w, const float* w_scale, int64_t n, int64_t k,
                                    const int8_t* x, const float* x_scale, int64_t m, int out_dtype,
                                    void* y, hipStream_t stream);
+
+/* The gated feed-forward block in 8 bits: P = act(G) U, where [G | U] is
+ * qlora_int8_linear_fwd's product in float32 over a weight that holds gate's n
+ * rows above up's n (w: 2 n x k, w_scale: 2 n). G and U are those exact sums
+ * times their scales; act and the product are float32, rounded once to nearest
+ * even into `out_dtype`.
+ *   n   : outputs, 1 .. 2^21; p: m x n. The other arguments and limits are
+ *         those of qlora_int8_linear_fwd with 2 n channels.
+ *   act : QLORA_ACT_SILU or QLORA_ACT_GELU_TANH.
+ * Errors: NULL / ALIGN / SHAPE / UNSUPPORTED (out_dtype, act, p over an input) /
+ * HIP. */
+qlora_status qlora_int8_linear_fwd_gated(const int8_t* w, const float* w_scale, int64_t n, int64_t k,
+                                         const int8_t* x, const float* x_scale, int64_t m, int act,
+                                         int out_dtype, void* p, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The global norm of a training step's adapter gradients (the dA and dB of
