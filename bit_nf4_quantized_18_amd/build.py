@@ -35,11 +35,13 @@ SOURCES = {
     "dropout_kernels.hip": DEVICE,
     "gemv_kernels.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "gemv_mfma.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
+    "gated_gemv.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "gemm_kernels.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "noalloc.hip": DEVICE,
     "int8_rows.hip": DEVICE + ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt"],
     "gated_kernels.hip": DEVICE + ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt"],
     "rank_grad8.hip": DEVICE,
+    "dense_gemm.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
     "int8_gemm.hip": DEVICE + ["-ffp-contract=off"],
     "grad_clip.hip": DEVICE + ["-fhip-fp32-correctly-rounded-divide-sqrt"],
 }

@@ -7,6 +7,7 @@
 #include <initializer_list>
 #include <new>
 
+#include "dense_rule.h"
 #include "internal.h"
 
 namespace {
@@ -32,7 +33,7 @@ struct Carve {
 };
 
 struct FwdLayout {
-  int64_t h32, hs, part, total;
+  int64_t h32, hs, part, w16, total;
 };
 // gemm: the fused GEMM for every m (dropout calls)
 FwdLayout fwd_layout(int64_t m, int64_t n, int64_t k, int r, bool gemm = false) {
@@ -54,7 +55,7 @@ FwdLayout fwd_layout(int64_t m, int64_t n, int64_t k, int r, bool gemm = false) 
 }
 
 struct BwdLayout {
-  int64_t h32, dh32, dhs, at, bt, part, spart, total;
+  int64_t h32, dh32, dhs, at, bt, part, spart, w16, total;
 };
 // r: adapter slots in total (g rpart for grouped weights)
 BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
@@ -82,29 +83,34 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
   return L;
 }
 
-// The gated forward: H's partial sums (decode, unless the kernel forms H
-// itself), or H, s H and the partial sums of H.
-bool gated_fuses_h(int slots) { return slots > 0 && slots <= 16; }
-FwdLayout gated_layout(int64_t m, int64_t k, int slots) {
+// The gated forward: H (decode), or H, s H and the partial sums of H; last, from
+// w16 on, the restored weight where restoring it once pays (dense_rule.h). A
+// workspace that ends in front of it is taken as well.
+FwdLayout gated_layout(int64_t m, int64_t n, int64_t k, int slots) {
   Carve c;
   FwdLayout L{};
   if (m <= kGemvMaxM) {
-    L.h32 = c.take(slots == 0 || gated_fuses_h(slots) ? 0 : qlora::skinny_splits(m, k) * m * slots * 4);
+    L.h32 = c.take(m * slots * 4);
+    L.w16 = c.off;
     L.total = c.off;
     return L;
   }
-  return fwd_layout(m, 0, k, slots, true);
+  L = fwd_layout(m, n, k, slots, true);
+  c.off = L.total;
+  L.w16 = c.take(qlora::dense_pays(m, n, k) ? n * k * 2 : 0);
+  L.total = c.off;
+  return L;
 }
 
 // The backward from 8-bit rows: the plain one's buffers but for the partial sums
-// of dA and dB, which go last.
+// of dA and dB, which go last, in front of the restored weight (w16, as above).
 BwdLayout x8_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
   BwdLayout L = bwd_layout(m, n, k, r, rpart);
-  if (r == 0) return L;
   Carve c;
   c.off = L.part;
-  const int splits = qlora::rank_grad8_splits(m, n, k, r, rpart);
+  const int splits = r == 0 ? 1 : qlora::rank_grad8_splits(m, n, k, r, rpart);
   c.take(splits == 1 ? 0 : splits * (r * k + rpart * n) * 4);
+  L.w16 = c.take(qlora::dense_pays(m, k, n) ? n * k * 2 : 0);
   L.total = c.off;
   return L;
 }
@@ -405,20 +411,24 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
   if (h_saved != nullptr && !aligned16(h_saved)) return QLORA_ERR_ALIGN;
   if (drop != nullptr && r == 0) drop = nullptr;  // no adapter, nothing to drop
   const size_t need = drop != nullptr ? static_cast<size_t>(drop_total(m, n, k, r))
-                      : x8 != nullptr ? static_cast<size_t>(x8_layout(m, n, k, r, rpart).total)
+                      : x8 != nullptr ? static_cast<size_t>(x8_layout(m, n, k, r, rpart).w16)
                       : grouped       ? qlora_linear_grouped_workspace_bytes(m, n, k, grp->g, rpart)
                                       : qlora_linear_workspace_bytes(m, n, k, r);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
   if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
 
+  const BwdLayout L = x8 != nullptr ? x8_layout(m, n, k, r, rpart) : bwd_layout(m, n, k, r, rpart);
+  // from 8-bit rows: the weight is restored once where that pays and the workspace holds it
+  const bool restores = x8 != nullptr && dx != nullptr && L.total > L.w16 && ws != nullptr &&
+                        ws_bytes >= static_cast<size_t>(L.total);
   if (x8 != nullptr &&
-      !apart({span(dx, 2 * m * k), span(da, 4 * r * k), span(db, 4 * n * rpart), span(ws, static_cast<int64_t>(need))},
+      !apart({span(dx, 2 * m * k), span(da, 4 * r * k), span(db, 4 * n * rpart),
+              span(ws, restores ? L.total : static_cast<int64_t>(need))},
              {span(r > 0 ? x8->codes : nullptr, m * x8->ld), span(r > 0 ? x8->scale : nullptr, 4 * m),
               span(dy, 2 * m * n), span(h_saved, 4 * m * r), span(a, 2 * r * k), span(b, 2 * n * rpart),
               span(w->codes, n * k / 2)}))
     return QLORA_ERR_UNSUPPORTED;
 
-  const BwdLayout L = bwd_layout(m, n, k, r, rpart);
   char* base = static_cast<char*>(ws);
   const uint16_t* xa = x;  // the adapter's input
   if (drop != nullptr) {
@@ -479,6 +489,10 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
       QLORA_TRY(qlora::launch_gemm_dx(pw, dy, m, nullptr, nullptr, 0, dx, stream, f16));
       QLORA_TRY(qlora::launch_masked_lora_add(dx, drop->keep, reinterpret_cast<const float*>(base + L.dh32), a, m, k,
                                               r, stream, f16));
+    } else if (x8 != nullptr && restores) {
+      uint16_t* wt16 = reinterpret_cast<uint16_t*>(base + L.w16);
+      QLORA_TRY(qlora::launch_restore_t(pw, wt16, stream, f16));
+      QLORA_TRY(qlora::launch_dense_dx(wt16, n, k, dy, m, dhs, at, rp, dx, stream, f16));
     } else {
       QLORA_TRY(qlora::launch_gemm_dx(pw, dy, m, dhs, at, rp, dx, stream, f16));
     }
@@ -649,7 +663,7 @@ qlora_status qlora_linear_bwd_grouped_x8_f16(const qlora_nf4_weight* w, int g, c
 // ---------------------------------------------------------------------------
 size_t qlora_linear_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int r) {
   if (!linear_sizes_ok(m, n, k) || r < 0 || 2 * r > QLORA_MAX_RANK) return 0;
-  return static_cast<size_t>(gated_layout(m, k, 2 * r).total);
+  return static_cast<size_t>(gated_layout(m, n, k, 2 * r).total);
 }
 
 static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int64_t m, const uint16_t* a,
@@ -664,33 +678,24 @@ static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int6
   if (m == 0) return QLORA_OK;
   if (!aligned16(y)) return QLORA_ERR_ALIGN;
   const int64_t n = w->n, k = w->k;
-  const FwdLayout L = gated_layout(m, k, slots);
-  const int64_t need = L.total;
+  const FwdLayout L = gated_layout(m, n, k, slots);
+  const int64_t need = L.w16;
   if (need > 0 && (ws == nullptr || ws_bytes < static_cast<size_t>(need))) return QLORA_ERR_WORKSPACE;
   if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
   if (r == 0) h_out = nullptr;
-  if (!apart({span(p, m * n), span(y, 2 * m * n), span(h_out, 4 * m * slots), span(ws, need)},
+  const bool restores = L.total > L.w16 && ws != nullptr && ws_bytes >= static_cast<size_t>(L.total);
+  if (!apart({span(p, m * n), span(y, 2 * m * n), span(h_out, 4 * m * slots), span(ws, restores ? L.total : need)},
              {span(x, 2 * m * k), span(a, 2 * slots * k), span(b, 2 * n * r), span(w->codes, n * k / 2)}))
     return QLORA_ERR_UNSUPPORTED;
 
-  qlora::LoraParts lp;
-  lp.g = 2;
-  lp.rpart = r;
-  lp.end[0] = static_cast<int>(n / 2);
-  lp.end[1] = static_cast<int>(n);
   char* base = static_cast<char*>(ws);
   const float s = r == 0 ? 0.0f : alpha / static_cast<float>(r);
   const int rp = rank_pad(slots);
   const PackedW pw = view(w);
   if (m <= kGemvMaxM) {
-    float* hpart = nullptr;
-    const int splits = qlora::skinny_splits(m, k);
-    if (slots > 0 && !gated_fuses_h(slots)) {
-      hpart = reinterpret_cast<float*>(base + L.h32);
-      QLORA_TRY(qlora::launch_skinny_decode(x, a, m, k, slots, rp, hpart, splits, stream, f16));
-    }
-    return hip_status(qlora::launch_gemv_mfma(pw, x, m, a, hpart, splits, b, slots, s, y, h_out, stream, f16, &lp,
-                                              qlora::GateOut{p, act}));
+    float* h = h_out != nullptr ? h_out : reinterpret_cast<float*>(base + L.h32);
+    if (r > 0) QLORA_TRY(qlora::launch_gated_h(x, m, a, k, slots, h, stream, f16));
+    return hip_status(qlora::launch_gated_gemv(pw, x, m, r > 0 ? h : nullptr, b, r, s, act, y, p, stream, f16));
   }
   uint16_t* hs = nullptr;
   if (r > 0) {
@@ -698,6 +703,11 @@ static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int6
     hs = reinterpret_cast<uint16_t*>(base + L.hs);
     QLORA_TRY(qlora::launch_skinny_prefill(x, a, m, k, slots, rp, 1.0f, s, reinterpret_cast<float*>(base + L.part), h32,
                                            hs, stream, f16));
+  }
+  if (restores) {
+    uint16_t* w16 = reinterpret_cast<uint16_t*>(base + L.w16);
+    QLORA_TRY(qlora::launch_dequantize(pw, f16 ? 2 : 0, w16, stream));
+    return hip_status(qlora::launch_dense_gated(w16, n, k, x, m, hs, b, r, rp, act, y, p, stream, f16));
   }
   return hip_status(qlora::launch_gemm_gated(pw, x, m, hs, b, r, rp, act, y, p, stream, f16));
 }

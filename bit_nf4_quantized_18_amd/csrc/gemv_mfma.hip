@@ -26,13 +26,7 @@
 //     skinny kernel;
 //   * partial sums of the waves are reduced in a fixed order in LDS, so
 //     results do not depend on scheduling.
-//
-// kGated builds both forms for a gated feed-forward block, whose weight holds
-// gate's rows above up's: a group's 16 rows are 8 gate rows and the 8 up rows of
-// the same outputs, whose float32 sums meet in one row of 16 lanes for the
-// product act(gate) up.
 #include "bufmem.h"
-#include "gate.h"
 #include "internal.h"
 #include "mfma.h"
 #include "nf4_lut.h"
@@ -61,43 +55,18 @@ __device__ __forceinline__ int part_slot0(const LoraParts& P, int p, int rb) {
   return off;
 }
 
-// Weight row i of row group rg.
-template <bool kGated>
-__device__ __forceinline__ int group_row(int rg, int i, int N) {
-  return kGated ? rg * 8 + (i & 7) + (i >> 3) * (N >> 1) : rg * 16 + i;
-}
-
-// Element e of the rows of B (N x rb) of row group rg, laid out row by row.
-template <bool kGated>
-__device__ __forceinline__ int group_b(int rg, int e, int N, int rb) {
-  return kGated ? (rg * 8 + (e >= 8 * rb ? (N >> 1) - 8 : 0)) * rb + e : rg * 16 * rb + e;
-}
-
-// The sum of one output row and token; in a gated block lanes 8 .. 15 of a row
-// of 16 hold up's sums of the outputs whose gate's lanes 0 .. 7 hold.
-template <bool kGated, bool kF16>
-__device__ __forceinline__ void put_sum(float sum, int token, int no, int rg, int col, int N, uint16_t* y, GateOut gate) {
-  if (!kGated) {
-    y[token * N + no] = to16<kF16>(sum);
-    return;
-  }
-  const float up = __shfl_xor(sum, 8, 64);
-  if (y != nullptr) y[token * N + no] = to16<kF16>(sum);
-  if (col < 8) gate.p[token * (N >> 1) + rg * 8 + col] = to16<kF16>(act_value<false>(sum, gate.act) * up);
-}
-
 // Multi-pass form for k > 4096: one workgroup per group of 16 weight rows,
 // passes of 64 blocks (one per lane group). In each pass a wave stages the
 // 256-k slice of X, then of A, that its lane groups multiply through its own
 // LDS region (see the persistent form below for the layout), so neither the
 // fragment loads nor the H product need anything from another wave.
-template <int WAVES, bool kDQ, bool kFuseH, bool kF16, bool kGated>
+template <int WAVES, bool kDQ, bool kFuseH, bool kF16>
 __global__ __launch_bounds__(WAVES * 64) void gemv_kernel(PackedW w, const uint16_t* __restrict__ x, int M,
                                                           const uint16_t* __restrict__ a,
                                                           const float* __restrict__ hpart, int hsplits,
                                                           const uint16_t* __restrict__ b, int rh, int rb,
                                                           LoraParts P, float s, uint16_t* __restrict__ y,
-                                                          float* __restrict__ h_out, Levels L, GateOut gate) {
+                                                          float* __restrict__ h_out, Levels L) {
   static_assert(WAVES == 16, "one pass covers 64 blocks, four per wave");
   constexpr int kLaneGroups = WAVES * 4;
   constexpr int kSlice = 16 * 512;  // one wave's region: 16 rows x 256 k of bf16
@@ -119,8 +88,8 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_kernel(PackedW w, const uint1
   // 32-bit offsets: the host guarantees n * k <= 2^31
   const int K = static_cast<int>(w.k), N = static_cast<int>(w.n);
   const int nbk = K / 64;
-  const int rg = blockIdx.x;
-  const int n = group_row<kGated>(rg, i, N);
+  const int n0 = blockIdx.x * 16;
+  const int n = n0 + i;
   const int n_c = n < N ? n : N - 1;  // clamped: every load is unconditional
   // X through a buffer resource sized to its M rows, A to its rh rows: rows
   // past them read zeros without touching memory
@@ -160,7 +129,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_kernel(PackedW w, const uint1
     // element of B; rows past N are never stored)
 #pragma unroll
     for (int u = 0; u < kBPer; ++u) {
-      const int e = group_b<kGated>(rg, tid + u * WAVES * 64, N, rb);
+      const int e = n0 * rb + tid + u * WAVES * 64;
       bv[u] = b[e < blast ? e : blast];
     }
   }
@@ -278,7 +247,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_kernel(PackedW w, const uint1
     __syncthreads();
   }
   if (tid >= 256) return;
-  const int no = group_row<kGated>(rg, l2 & 15, N);
+  const int no = n0 + (l2 & 15);
   if (mo >= M || no >= N) return;
   float sum = 0.0f;
 #pragma unroll
@@ -290,7 +259,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_kernel(PackedW w, const uint1
     for (int j = 0; j < rb; ++j) lo = fmaf(hrow[j], to_f32<kF16>(brow[j]), lo);
     sum = fmaf(s, lo, sum);
   }
-  put_sum<kGated, kF16>(sum, mo, no, rg, l2 & 15, N, y, gate);
+  y[mo * N + no] = to16<kF16>(sum);
 }
 
 // Persistent form for k <= 4096 (one pass covers a row): a workgroup takes
@@ -310,13 +279,13 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_kernel(PackedW w, const uint1
 // the row, so the 16 rows of one piece fall in 16 different bank groups. The
 // region holds X first; once X is in registers it receives the wave's slice
 // of A, which only that wave reads: H needs no barrier of its own.
-template <bool kDQ, bool kFuseH, bool kF16, bool kGated>
+template <bool kDQ, bool kFuseH, bool kF16>
 __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const uint16_t* __restrict__ x, int M,
                                                                const uint16_t* __restrict__ a,
                                                                const float* __restrict__ hpart, int hsplits,
                                                                const uint16_t* __restrict__ b, int rh, int rb,
                                                                LoraParts P, float s, uint16_t* __restrict__ y,
-                                                               float* __restrict__ h_out, Levels L, GateOut gate) {
+                                                               float* __restrict__ h_out, Levels L) {
   constexpr int WAVES = 16;
   constexpr int kSlice = 16 * 512;  // one wave's region: 16 rows x 256 k of bf16
   constexpr int kRedBytes = (kFuseH ? 2 : 1) * WAVES * 64 * 16;
@@ -355,7 +324,7 @@ __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const 
   // loads of row group rg < nrg; with real = false the same instructions on
   // the first element of every array (one cache line each, results unused)
   auto issue = [&](int rgc, Loads& T, bool real) {
-    const int n = group_row<kGated>(rgc, i, N);
+    const int n = rgc * 16 + i;
     const int n_c = real ? (n < N ? n : N - 1) : 0;
     const int kb_r = real ? kb_c : 0;
     const u32x4* cp = reinterpret_cast<const u32x4*>(w.codes + (n_c * (K / 2) + kb_r * 32));
@@ -373,7 +342,7 @@ __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const 
     // B), so that every path issues the same number of loads per row group
 #pragma unroll
     for (int u = 0; u < kBPer; ++u) {
-      const int e = group_b<kGated>(rgc, tid + u * WAVES * 64, N, rb);
+      const int e = rgc * 16 * rb + tid + u * WAVES * 64;
       const uint16_t* bp = (rb > 0 && real) ? b + (e < blast ? e : blast) : x;
       T.bv[u] = *bp;
     }
@@ -451,7 +420,7 @@ __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const 
     issue(rg + static_cast<int>(gridDim.x), Tn, has_next);
     // wave-uniform guard; lane groups past the row's blocks get a zero scale
     if (wave * 4 < nbk) {
-      const int n = group_row<kGated>(rg, i, N);
+      const int n = rg * 16 + i;
       const bool ok = (n < N) && kval;
       const float sc = kDQ ? dq_unit(Tc.scode, w.dq) * Tc.gsc : Tc.gsc;
       const BlockLut lut = make_block_lut<kF16>(L.v, ok ? sc : 0.0f);
@@ -507,7 +476,7 @@ __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const 
       }
       __syncthreads();
     }
-    const int no = group_row<kGated>(rg, l2 & 15, N);
+    const int no = rg * 16 + (l2 & 15);
     if (tid < 256 && mo < M && no < N) {
       float sum = 0.0f;
 #pragma unroll
@@ -519,7 +488,7 @@ __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const 
         for (int j = 0; j < rb; ++j) lo = fmaf(hrow[j], to_f32<kF16>(brow[j]), lo);
         sum = fmaf(s, lo, sum);
       }
-      put_sum<kGated, kF16>(sum, mo, no, rg, l2 & 15, N, y, gate);
+      y[mo * N + no] = to16<kF16>(sum);
     }
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
   };
@@ -533,26 +502,26 @@ __global__ __launch_bounds__(1024) void gemv_persistent_kernel(PackedW w, const 
 
 namespace {
 
-template <bool kF16, bool kGated>
+template <bool kF16>
 hipError_t launch_gemv_t(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* a, const float* hpart,
                          int hsplits, const uint16_t* b, int r, float s, uint16_t* y, float* h_out, hipStream_t st,
-                         const LoraParts& P, GateOut gate) {
+                         const LoraParts& P) {
   constexpr int kWaves = 16;
   const int64_t nrg = (w.n + 15) / 16;
-  const bool fuse = r > 0 && hpart == nullptr;
+  const bool fuse = gemv_fuses_h(m, w.k, r, P.g > 1 ? &P : nullptr);
   const int rb = P.g > 1 ? P.rpart : r;
   if (w.k <= 4096) {
     const unsigned grid = static_cast<unsigned>(nrg < device_cus() ? nrg : device_cus());
-    auto kern = w.dq ? (fuse ? gemv_persistent_kernel<true, true, kF16, kGated> : gemv_persistent_kernel<true, false, kF16, kGated>)
-                     : (fuse ? gemv_persistent_kernel<false, true, kF16, kGated> : gemv_persistent_kernel<false, false, kF16, kGated>);
+    auto kern = w.dq ? (fuse ? gemv_persistent_kernel<true, true, kF16> : gemv_persistent_kernel<true, false, kF16>)
+                     : (fuse ? gemv_persistent_kernel<false, true, kF16> : gemv_persistent_kernel<false, false, kF16>);
     hipLaunchKernelGGL(kern, dim3(grid), dim3(kWaves * 64), 0, st, w, x, static_cast<int>(m), a, hpart, hsplits, b,
-                       r, rb, P, s, y, h_out, codebook_table(w.codebook), gate);
+                       r, rb, P, s, y, h_out, codebook_table(w.codebook));
     return hipGetLastError();
   }
-  auto kern = w.dq ? (fuse ? gemv_kernel<kWaves, true, true, kF16, kGated> : gemv_kernel<kWaves, true, false, kF16, kGated>)
-                   : (fuse ? gemv_kernel<kWaves, false, true, kF16, kGated> : gemv_kernel<kWaves, false, false, kF16, kGated>);
+  auto kern = w.dq ? (fuse ? gemv_kernel<kWaves, true, true, kF16> : gemv_kernel<kWaves, true, false, kF16>)
+                   : (fuse ? gemv_kernel<kWaves, false, true, kF16> : gemv_kernel<kWaves, false, false, kF16>);
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(nrg)), dim3(kWaves * 64), 0, st, w, x, static_cast<int>(m), a,
-                     hpart, hsplits, b, r, rb, P, s, y, h_out, codebook_table(w.codebook), gate);
+                     hpart, hsplits, b, r, rb, P, s, y, h_out, codebook_table(w.codebook));
   return hipGetLastError();
 }
 
@@ -560,18 +529,14 @@ hipError_t launch_gemv_t(const PackedW& w, const uint16_t* x, int64_t m, const u
 
 hipError_t launch_gemv_mfma(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* a, const float* hpart,
                             int hsplits, const uint16_t* b, int r, float s, uint16_t* y, float* h_out, hipStream_t st,
-                            bool f16, const LoraParts* parts, GateOut gate) {
-  if (hpart == nullptr && r > 16) return hipErrorInvalidValue;
+                            bool f16, const LoraParts* parts) {
   LoraParts one;
   one.g = 1;
   one.rpart = r;
   one.end[0] = static_cast<int>(w.n);
   const LoraParts& P = parts != nullptr ? *parts : one;
-  if (gate.p != nullptr)
-    return f16 ? launch_gemv_t<true, true>(w, x, m, a, hpart, hsplits, b, r, s, y, h_out, st, P, gate)
-               : launch_gemv_t<false, true>(w, x, m, a, hpart, hsplits, b, r, s, y, h_out, st, P, gate);
-  return f16 ? launch_gemv_t<true, false>(w, x, m, a, hpart, hsplits, b, r, s, y, h_out, st, P, gate)
-             : launch_gemv_t<false, false>(w, x, m, a, hpart, hsplits, b, r, s, y, h_out, st, P, gate);
+  return f16 ? launch_gemv_t<true>(w, x, m, a, hpart, hsplits, b, r, s, y, h_out, st, P)
+             : launch_gemv_t<false>(w, x, m, a, hpart, hsplits, b, r, s, y, h_out, st, P);
 }
 
 }  // namespace qlora

@@ -121,11 +121,17 @@ hipError_t launch_gemv(const PackedW& w, const uint16_t* x, int64_t m, const uin
                        int hsplits, const uint16_t* b, int r, float s, uint16_t* y, float* h_out, hipStream_t st,
                        bool f16 = false, const LoraParts* parts = nullptr);
 // The matrix-core form (3..16 tokens, or k > 4096); same arguments as launch_gemv.
-// H is fused where hpart is null (r <= 16). With gate.p, w's parts are gate's
-// rows above up's, and y may be null.
 hipError_t launch_gemv_mfma(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* a, const float* hpart,
                             int hsplits, const uint16_t* b, int r, float s, uint16_t* y, float* h_out, hipStream_t st,
-                            bool f16, const LoraParts* parts, GateOut gate = {});
+                            bool f16, const LoraParts* parts);
+
+// Decode of a gated block, m <= 16 (w: gate's rows above up's, each a multiple of
+// 8): h (m x 2 rpart float32) from launch_gated_h with slots = 2 rpart; y, the
+// pre-activations, may be null; rpart = 0: no adapter.
+hipError_t launch_gated_h(const uint16_t* x, int64_t m, const uint16_t* a, int64_t k, int slots, float* h,
+                          hipStream_t st, bool f16);
+hipError_t launch_gated_gemv(const PackedW& w, const uint16_t* x, int64_t m, const float* h, const uint16_t* b,
+                             int rpart, float s, int act, uint16_t* y, uint16_t* p, hipStream_t st, bool f16);
 
 // Fused dequant-GEMM, forward: y = x W16^T + the LoRA term where hs is bf16
 // m x rpad (already scaled by s) and b is n x r bf16 (r = slots per part);
@@ -144,6 +150,17 @@ hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, con
 // m x rpad and at is bf16 k x rpad (A transposed, zero padded).
 hipError_t launch_gemm_dx(const PackedW& w, const uint16_t* dy, int64_t m, const uint16_t* dhs,
                           const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16 = false);
+
+// The product over a weight restored to 16 bits in the workspace (dense_gemm.hip):
+// w16 as launch_dequantize writes it (n2 rows of k), wt16 as launch_restore_t
+// does (k rows of n). Other arguments as launch_gemm_gated and launch_gemm_dx.
+// For sizes that dense_fits (dense_rule.h).
+hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const uint16_t* x, int64_t m,
+                              const uint16_t* hs, const uint16_t* b, int rpart, int rpad, int act, uint16_t* y,
+                              uint16_t* p, hipStream_t st, bool f16);
+hipError_t launch_restore_t(const PackedW& w, uint16_t* out, hipStream_t st, bool f16);
+hipError_t launch_dense_dx(const uint16_t* wt16, int64_t n, int64_t k, const uint16_t* dy, int64_t m,
+                           const uint16_t* dhs, const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16);
 
 // Transposes with zero padding: bt (rpad x n) from b (n x r); at (k x rpad) from a (r x k).
 // Grouped weights (parts != null, r = g rpart): b is n x rpart (the parts' B

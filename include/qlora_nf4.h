@@ -381,7 +381,11 @@ size_t qlora_linear_grouped_workspace_bytes(int64_t m, int64_t n, int64_t k, int
  *   p     : m x np output, formed from the float32 sums of G and U and rounded
  *           once.
  *   h_out : float32 m x (2 r), [H_1 | H_2]; may be NULL.
- *   ws    : qlora_linear_gated_workspace_bytes(m, w->n, k, r) bytes.
+ *   ws    : qlora_linear_gated_workspace_bytes(m, w->n, k, r) bytes. Their last
+ *           2 w->n k are, where the size counts them, for the weight restored to
+ *           16 bits; a workspace without them is taken too, and the weight then
+ *           restored as it is multiplied (the same bounds, more time; sums in
+ *           another order).
  * Outputs and workspace overlap neither an input nor each other. The backward is
  * qlora_gated_bwd for d[G | U], then qlora_linear_bwd_grouped. m = 0 is a no-op.
  * Errors: NULL / ALIGN / SHAPE (as qlora_linear_fwd; w->n % 512 != 0) / UNSUPPORTED
@@ -436,7 +440,8 @@ qlora_status qlora_gated_bwd_x8(const int8_t* codes, int64_t ld, const float* sc
  *   h               : float32 m x r (m x (g r)), from the forward's h_out;
  *                     required (H is not formed again from rounded rows).
  *   ws              : qlora_linear_x8_workspace_bytes(m, n, k, g, r) bytes (g = 1
- *                     for the plain calls).
+ *                     for the plain calls); the last 2 n k, where the size counts
+ *                     them, may be left out as in qlora_linear_fwd_gated.
  * The other arguments, limits and errors are those of the calls with a 16-bit
  * input; UNSUPPORTED also for outputs or a workspace that overlap an input or
  * each other, SHAPE for a bad ldx. With r = 0 the rows are not read. */

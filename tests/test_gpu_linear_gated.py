@@ -139,6 +139,37 @@ def test_captured_with_eager_calls_between(gpu_lib):
             assert torch.equal(p, want[0]) and torch.equal(y, want[1]) and torch.equal(h, want[2])
 
 
+@pytest.mark.parametrize("m", [17, 70, 300])
+@pytest.mark.parametrize("r", [0, 8, 16, 64])
+def test_workspace_without_the_restored_weight(gpu_lib, m, r):
+    # the call restores the weight as it multiplies; both ways are within the bounds
+    t, half, k = torch.bfloat16, 512, 320
+    w, x, a, b, alpha = layer(gpu_lib, m, half, k, r, t, 31)
+    nbytes = gpu_lib.gated_workspace_bytes(m, 2 * half, k, r)
+    without = nbytes - 2 * half * k * 2
+    assert without >= 0  # these sizes restore it once
+    ws = torch.full((without + 256,), 9, dtype=torch.uint8, device="cuda")
+    g, u, _, dg, du, _ = expected(gpu_lib, w, x, a, b, alpha, t)
+    for size in (without, nbytes):
+        room = ws[:without] if size == without else torch.empty(size, dtype=torch.uint8, device="cuda")
+        p, y, _ = gpu_lib.linear_fwd_gated(w, x, a, b, alpha, OG.GELU, ws=room if size else None)
+        C.check(p, OG.fwd(g, u, OG.GELU), C.fwd_bound(g, u, OG.GELU, t, dg, du), "P")
+        v, off = np.concatenate([g, u], 1), np.concatenate([dg, du], 1)
+        C.check(y, v, np.abs(v) * C.half_step(t) * (1 + 2 ** -7) + off * 1.01 + C.tiny(t), "Y")
+    assert (ws[without:] == 9).all()
+    if without:
+        with pytest.raises(gpu_lib.QloraError, match="WORKSPACE"):
+            gpu_lib.linear_fwd_gated(w, x, a, b, alpha, ws=ws[:without - 1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,half,k,r", [(2100, 1024, 1088, 16), (1030, 2816, 256, 5), (600, 5632, 192, 0), (200, 512, 8192, 24)])
+def test_tiles_of_the_restored_weight(gpu_lib, m, half, k, r, kind):
+    t = C.TYPES[kind]
+    w, x, a, b, alpha = layer(gpu_lib, m, half, k, r, t, m)
+    compare(gpu_lib, w, x, a, b, alpha, OG.SILU, t)
+
+
 def test_no_tokens(gpu_lib):
     w, x, a, b, alpha = layer(gpu_lib, 1, 256, 64, 16, torch.bfloat16, 1)
     p, y, h = gpu_lib.linear_fwd_gated(w, x[:0], a, b, alpha)
