@@ -878,37 +878,47 @@ def _linear_bwd_x8(q, parts, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws):
         _init()
     dev = _need_packed(q)
     index = q.codes.get_device()
-    m = dy.shape[0]
+    m, n, k = dy.shape[0], q.n, q.k
     g = 1 if parts is None else len(parts)
     r = 0 if b is None else b.shape[-1]
     t16 = _half_types(dy, "dy")
-    f32 = (_torch.float32,)
-    _need(dy, "dy", (m, q.n), t16, dev)
-    _need_adapter(a, b, g * r, q.k, q.n, t16, dev, rb=r)
+    _need(dy, "dy", (m, n), t16, dev)
     ld = _need_int8(x, "x", index)
-    if x.n != m or x.k != q.k:
-        raise ValueError(f"x holds {x.n} rows of {x.k} values, expected {m} of {q.k}")
-    _need(h, "h", (m, g * r), f32, dev, optional=r == 0)
-    if dx is None and need_dx:
-        dx = dy.new_empty(m, q.k)
-    if r and da is None:
-        da = dy.new_empty(g * r, q.k, dtype=_torch.float32)
-    if r and db is None:
-        db = dy.new_empty(q.n, r, dtype=_torch.float32)
-    _need(dx, "dx", (m, q.k), t16, dev, optional=True)
-    _need(da, "da", (g * r, q.k), f32, dev, optional=r == 0)
-    _need(db, "db", (q.n, r), f32, dev, optional=r == 0)
-    _need_ws(ws, dev)
+    if x.n != m or x.k != k:
+        raise ValueError(f"x holds {x.n} rows of {x.k} values, expected {m} of {k}")
+    _need_adapter(a, b, g * r, k, n, t16, dev, rb=r)
+    if r:
+        f32 = (_torch.float32,)
+        _need(h, "h", (m, g * r), f32, dev)
+        if da is None:
+            da = dy.new_empty(g * r, k, dtype=_torch.float32)
+        else:
+            _need(da, "da", (g * r, k), f32, dev)
+        if db is None:
+            db = dy.new_empty(n, r, dtype=_torch.float32)
+        else:
+            _need(db, "db", (n, r), f32, dev)
+    else:
+        h = da = db = None
+    if dx is not None:
+        _need(dx, "dx", (m, k), t16, dev)
+    elif need_dx:
+        dx = dy.new_empty(m, k)
     if ws is None:
-        nbytes = x8_workspace_bytes(m, q.n, q.k, g, r)
+        nbytes = _LIB.qlora_linear_x8_workspace_bytes(m, n, k, g, r)
         ws = dy.new_empty(nbytes, dtype=_torch.uint8) if nbytes else None
     else:
+        _need_ws(ws, dev)
         nbytes = ws.numel()
+    f16 = dy.dtype is _torch.float16
+    if parts is None:
+        fn, lead = _LIB.qlora_linear_bwd_x8_f16 if f16 else _LIB.qlora_linear_bwd_x8, ()
+    else:
+        fn, lead = _LIB.qlora_linear_bwd_grouped_x8_f16 if f16 else _LIB.qlora_linear_bwd_grouped_x8, (g, _parts(parts))
+    at = [None if t is None else t.data_ptr() for t in (a, b, h, dx, da, db, ws)]
     wc = q.c_struct()
-    name = "qlora_linear_bwd" + ("" if parts is None else "_grouped") + "_x8" + ("_f16" if dy.dtype is _torch.float16 else "")
-    lead = () if parts is None else (g, _parts(parts))
-    _launch(getattr(_LIB, name), index, ctypes.byref(wc), *lead, x.codes.data_ptr(), ld, x.scale.data_ptr(),
-            dy.data_ptr(), m, _ptr(a), _ptr(b), r, float(alpha), _ptr(h), _ptr(dx), _ptr(da), _ptr(db), _ptr(ws), nbytes)
+    _launch(fn, index, ctypes.byref(wc), *lead, x.codes.data_ptr(), ld, x.scale.data_ptr(), dy.data_ptr(), m, at[0], at[1],
+            r, float(alpha), *at[2:], nbytes)
     return dx, da, db
 
 

@@ -442,6 +442,9 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
   const PackedW pw = view(w);
   uint16_t* dhs = nullptr;
   uint16_t* at = nullptr;
+  uint16_t* wt16 = restores ? reinterpret_cast<uint16_t*>(base + L.w16) : nullptr;
+  if (restores && r == 0)
+    QLORA_TRY(qlora::launch_restore_t(pw, wt16, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, stream, f16));
 
   if (r > 0) {
     uint16_t* bt = reinterpret_cast<uint16_t*>(base + L.bt);
@@ -459,7 +462,8 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     }
     // A^T, and B^T (block diagonal for grouped weights: part l's slots see
     // only its own output columns)
-    QLORA_TRY(qlora::launch_lora_transpose(a, b, n, k, r, rp, at, bt, stream, grp));
+    if (restores) QLORA_TRY(qlora::launch_restore_t(pw, wt16, a, b, r, rp, at, bt, grp, stream, f16));
+    else QLORA_TRY(qlora::launch_lora_transpose(a, b, n, k, r, rp, at, bt, stream, grp));
     // dH = s dY B  (contraction over n, with B^T as the r x n operand).
     // Under dropout dh32 holds dH / (1 - p), the factor both dA and the
     // masked dX update need; the frozen-weight GEMM then runs without
@@ -489,9 +493,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
       QLORA_TRY(qlora::launch_gemm_dx(pw, dy, m, nullptr, nullptr, 0, dx, stream, f16));
       QLORA_TRY(qlora::launch_masked_lora_add(dx, drop->keep, reinterpret_cast<const float*>(base + L.dh32), a, m, k,
                                               r, stream, f16));
-    } else if (x8 != nullptr && restores) {
-      uint16_t* wt16 = reinterpret_cast<uint16_t*>(base + L.w16);
-      QLORA_TRY(qlora::launch_restore_t(pw, wt16, stream, f16));
+    } else if (restores) {
       QLORA_TRY(qlora::launch_dense_dx(wt16, n, k, dy, m, dhs, at, rp, dx, stream, f16));
     } else {
       QLORA_TRY(qlora::launch_gemm_dx(pw, dy, m, dhs, at, rp, dx, stream, f16));

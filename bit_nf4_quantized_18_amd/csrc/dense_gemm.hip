@@ -15,6 +15,7 @@
 #include "dense_rule.h"
 #include "gate.h"
 #include "internal.h"
+#include "lora_transpose.h"
 #include "mfma.h"
 #include "nf4_lut.h"
 
@@ -362,14 +363,30 @@ hipError_t launch_product(DenseArgs g, bool f16, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // The restored weight's transpose (k x n), for the backward. A workgroup takes 64
 // weight rows and 4 of their 64-weight blocks: a lane restores one block of one
-// row and writes it down LDS columns, which leave as whole 128-byte runs.
+// row and writes it down LDS columns, which leave as whole 128-byte runs. The
+// adapter's transposes, which the same backward needs, are further workgroups of the
+// same launch (3 us of small calls).
 // ---------------------------------------------------------------------------
+struct Adapter {
+  const uint16_t* a;  // null: none
+  const uint16_t* b;
+  int r, rpad;
+  LoraParts parts;
+  uint16_t* at;
+  uint16_t* bt;
+};
 constexpr int kTrRows = 64, kTrBlocks = 4;
 constexpr int kTrLd = kTrRows + 8;  // elements of an LDS row: 16-byte reads stay aligned, rows shift by 4 banks
 
 template <bool kDQ, bool kF16>
-__global__ __launch_bounds__(256) void restore_t_kernel(PackedW w, uint16_t* out, Levels L) {
+__global__ __launch_bounds__(256) void restore_t_kernel(PackedW w, uint16_t* out, Levels L, int64_t blocks,
+                                                        Adapter ad) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[kTrBlocks * 64 * kTrLd];
+  static_assert(kTrTile <= kTrBlocks * 64 * kTrLd, "both transposes use the tile");
+  if (blockIdx.x >= blocks) {
+    lora_transpose_tile(tile, blockIdx.x - blocks, ad.a, ad.b, w.n, w.k, ad.r, ad.rpad, ad.parts, ad.at, ad.bt);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t nbk = w.k / 64, tiles_k = (nbk + kTrBlocks - 1) / kTrBlocks;
   const int64_t n0 = blockIdx.x / tiles_k * kTrRows, b0 = blockIdx.x % tiles_k * kTrBlocks;
@@ -406,11 +423,18 @@ hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const 
   return launch_product<true>(g, f16, st);
 }
 
-hipError_t launch_restore_t(const PackedW& w, uint16_t* out, hipStream_t st, bool f16) {
-  const int64_t grid = (w.n + kTrRows - 1) / kTrRows * ((w.k / 64 + kTrBlocks - 1) / kTrBlocks);
+hipError_t launch_restore_t(const PackedW& w, uint16_t* out, const uint16_t* a, const uint16_t* b, int r, int rpad,
+                            uint16_t* at, uint16_t* bt, const LoraParts* parts, hipStream_t st, bool f16) {
+  LoraParts one;
+  one.rpart = r;
+  one.end[0] = static_cast<int>(w.n);
+  const Adapter ad{a, b, r, rpad, parts != nullptr ? *parts : one, at, bt};
+  const int64_t blocks = (w.n + kTrRows - 1) / kTrRows * ((w.k / 64 + kTrBlocks - 1) / kTrBlocks);
   auto kern = f16 ? (w.dq ? restore_t_kernel<true, true> : restore_t_kernel<false, true>)
                   : (w.dq ? restore_t_kernel<true, false> : restore_t_kernel<false, false>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, w, out, codebook_table(w.codebook));
+  const int64_t grid = blocks + (r > 0 ? lora_transpose_tiles(w.n, w.k) : 0);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, w, out, codebook_table(w.codebook),
+                     blocks, ad);
   return hipGetLastError();
 }
 

@@ -158,7 +158,10 @@ hipError_t launch_gemm_dx(const PackedW& w, const uint16_t* dy, int64_t m, const
 hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const uint16_t* x, int64_t m,
                               const uint16_t* hs, const uint16_t* b, int rpart, int rpad, int act, uint16_t* y,
                               uint16_t* p, hipStream_t st, bool f16);
-hipError_t launch_restore_t(const PackedW& w, uint16_t* out, hipStream_t st, bool f16);
+// launch_restore_t makes the adapter's transposes too (r > 0), as
+// launch_lora_transpose does.
+hipError_t launch_restore_t(const PackedW& w, uint16_t* out, const uint16_t* a, const uint16_t* b, int r, int rpad,
+                            uint16_t* at, uint16_t* bt, const LoraParts* parts, hipStream_t st, bool f16);
 hipError_t launch_dense_dx(const uint16_t* wt16, int64_t n, int64_t k, const uint16_t* dy, int64_t m,
                            const uint16_t* dhs, const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16);
 
