@@ -418,9 +418,9 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
   if (ws != nullptr && !aligned16(ws)) return QLORA_ERR_ALIGN;
 
   const BwdLayout L = x8 != nullptr ? x8_layout(m, n, k, r, rpart) : bwd_layout(m, n, k, r, rpart);
-  // from 8-bit rows: the weight is restored once where that pays and the workspace holds it
-  const bool restores = x8 != nullptr && dx != nullptr && L.total > L.w16 && ws != nullptr &&
-                        ws_bytes >= static_cast<size_t>(L.total);
+  // From 8-bit rows: the weight is restored once where that pays and the workspace
+  // holds it (without dX not at all, but dH is then formed as it is beside it).
+  const bool restores = x8 != nullptr && L.total > L.w16 && ws != nullptr && ws_bytes >= static_cast<size_t>(L.total);
   if (x8 != nullptr &&
       !apart({span(dx, 2 * m * k), span(da, 4 * r * k), span(db, 4 * n * rpart),
               span(ws, restores ? L.total : static_cast<int64_t>(need))},
@@ -442,9 +442,10 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
   const PackedW pw = view(w);
   uint16_t* dhs = nullptr;
   uint16_t* at = nullptr;
-  uint16_t* wt16 = restores ? reinterpret_cast<uint16_t*>(base + L.w16) : nullptr;
+  uint16_t* wt16 = restores && dx != nullptr ? reinterpret_cast<uint16_t*>(base + L.w16) : nullptr;
   if (restores && r == 0)
-    QLORA_TRY(qlora::launch_restore_t(pw, wt16, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, stream, f16));
+    QLORA_TRY(qlora::launch_restore_t(pw, wt16, dy, m, nullptr, nullptr, 0, 0, nullptr, s, nullptr, nullptr, nullptr,
+                                      stream, f16));
 
   if (r > 0) {
     uint16_t* bt = reinterpret_cast<uint16_t*>(base + L.bt);
@@ -462,15 +463,19 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     }
     // A^T, and B^T (block diagonal for grouped weights: part l's slots see
     // only its own output columns)
-    if (restores) QLORA_TRY(qlora::launch_restore_t(pw, wt16, a, b, r, rp, at, bt, grp, stream, f16));
-    else QLORA_TRY(qlora::launch_lora_transpose(a, b, n, k, r, rp, at, bt, stream, grp));
+    if (restores) {
+      QLORA_TRY(qlora::launch_restore_t(pw, wt16, dy, m, a, b, r, rp, grp, s, dh32, dhs, at, stream, f16));
+    } else {
+      QLORA_TRY(qlora::launch_lora_transpose(a, b, n, k, r, rp, at, bt, stream, grp));
+    }
     // dH = s dY B  (contraction over n, with B^T as the r x n operand).
     // Under dropout dh32 holds dH / (1 - p), the factor both dA and the
     // masked dX update need; the frozen-weight GEMM then runs without
     // adapter slots.
     if (drop != nullptr) dhs = nullptr;
-    QLORA_TRY(qlora::launch_skinny_prefill(dy, bt, m, n, r, rp, drop != nullptr ? s * inv_keep : s, 1.0f, spart, dh32,
-                                           dhs, stream, f16));
+    if (!restores)
+      QLORA_TRY(qlora::launch_skinny_prefill(dy, bt, m, n, r, rp, drop != nullptr ? s * inv_keep : s, 1.0f, spart, dh32,
+                                             dhs, stream, f16));
     if (x8 != nullptr) {
       QLORA_TRY(qlora::launch_rank_grads8(dh32, x8->codes, x8->ld, x8->scale, k, h, dy, n, m, r, grp, s, part, da, db,
                                           stream, f16));
@@ -699,18 +704,15 @@ static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int6
     if (r > 0) QLORA_TRY(qlora::launch_gated_h(x, m, a, k, slots, h, stream, f16));
     return hip_status(qlora::launch_gated_gemv(pw, x, m, r > 0 ? h : nullptr, b, r, s, act, y, p, stream, f16));
   }
-  uint16_t* hs = nullptr;
-  if (r > 0) {
-    float* h32 = h_out != nullptr ? h_out : reinterpret_cast<float*>(base + L.h32);
-    hs = reinterpret_cast<uint16_t*>(base + L.hs);
-    QLORA_TRY(qlora::launch_skinny_prefill(x, a, m, k, slots, rp, 1.0f, s, reinterpret_cast<float*>(base + L.part), h32,
-                                           hs, stream, f16));
-  }
+  uint16_t* hs = r > 0 ? reinterpret_cast<uint16_t*>(base + L.hs) : nullptr;
   if (restores) {
     uint16_t* w16 = reinterpret_cast<uint16_t*>(base + L.w16);
-    QLORA_TRY(qlora::launch_dequantize(pw, f16 ? 2 : 0, w16, stream));
+    QLORA_TRY(qlora::launch_restore(pw, w16, x, m, a, slots, rp, s, h_out, hs, stream, f16));
     return hip_status(qlora::launch_dense_gated(w16, n, k, x, m, hs, b, r, rp, act, y, p, stream, f16));
   }
+  if (r > 0)
+    QLORA_TRY(qlora::launch_skinny_prefill(x, a, m, k, slots, rp, 1.0f, s, reinterpret_cast<float*>(base + L.part),
+                                           h_out, hs, stream, f16));
   return hip_status(qlora::launch_gemm_gated(pw, x, m, hs, b, r, rp, act, y, p, stream, f16));
 }
 

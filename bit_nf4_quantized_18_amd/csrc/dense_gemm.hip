@@ -361,35 +361,151 @@ hipError_t launch_product(DenseArgs g, bool f16, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// The restored weight's transpose (k x n), for the backward. A workgroup takes 64
-// weight rows and 4 of their 64-weight blocks: a lane restores one block of one
-// row and writes it down LDS columns, which leave as whole 128-byte runs. The
-// adapter's transposes, which the same backward needs, are further workgroups of the
-// same launch (3 us of small calls).
+// What a product over the restored weight needs beside its inputs, in one launch: the
+// weight (or its transpose) in 16 bits, and the adapter's narrow product, H = X A^T or
+// dH = s dY B, whose workgroups come first and end under the weight's memory traffic.
+// In launches of their own H took 12 us of a 2048 x 22016 x 4096 call and 8 of 27 us of
+// a 333 x 5120 x 1088 one.
 // ---------------------------------------------------------------------------
-struct Adapter {
-  const uint16_t* a;  // null: none
-  const uint16_t* b;
-  int r, rpad;
+constexpr int kThreads = 256;
+
+// out32[i][j] = scale sum_q p[i][q] w(j, q), out16 = 16 bits of scale2 out32 with zeros
+// behind the slots. w: slots x q, or (kCols) q x rpart, where slot j is column j mod
+// rpart of part j / rpart's rows and zero in the others'.
+struct Narrow {
+  const uint16_t* p;
+  int64_t m, q;
+  const uint16_t* w;
+  int slots, rpad;  // rpad: slots rounded up to 32; 0: none of this
   LoraParts parts;
-  uint16_t* at;
-  uint16_t* bt;
+  float scale, scale2;
+  float* out32;
+  uint16_t* out16;
 };
+
+// 16 tokens by a workgroup: its four waves take units of 64 of the contraction (whole
+// cache lines) in turn, operands straight from memory, and their sums meet in LDS in
+// wave order. kCols: a lane's eight operands are strided, 2-byte loads.
+template <bool kF16, bool kCols>
+__device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x4* red) {
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4, wave = tid >> 6;
+  const int64_t m0 = block * 16;
+  const uint16_t* prow = g.p + (m0 + i < g.m ? m0 + i : g.m - 1) * g.q;
+  for (int s0 = 0; s0 < g.rpad; s0 += 32) {
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    for (int64_t u = wave; u < (g.q + 63) / 64; u += 8) {
+      u32x4 pv[4], wv[4][2];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // halves of units u and u + 4
+        const int64_t q = 64 * (u + 4 * (c >> 1)) + 32 * (c & 1) + 8 * h;
+        const bool in = q < g.q;  // q is a multiple of 16 long: a run of 8 is whole or absent
+        const int64_t at = in ? q : 0;
+        pv[c] = ld16(prow + at);
+        if (!in) pv[c] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int slot = s0 + 16 * t + i;
+          if constexpr (!kCols) {
+            wv[c][t] = ld16(g.w + static_cast<int64_t>(slot < g.slots ? slot : 0) * g.q + at);
+          } else {
+            int part = 0;
+#pragma unroll
+            for (int l = 0; l < 3; ++l) part += (l + 1 < g.parts.g && at >= g.parts.end[l]) ? 1 : 0;
+            const int col = slot - part * g.parts.rpart;
+            const bool own = col >= 0 && col < g.parts.rpart;
+            const uint16_t* w = g.w + at * g.parts.rpart + (own ? col : 0);
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = w[e * g.parts.rpart];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wv[c][t][e] = own ? v[2 * e] | v[2 * e + 1] << 16 : 0u;
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) acc[t] = mma16<kF16>(pv[c], wv[c][t], acc[t]);
+    }
+    if (s0 > 0) __syncthreads();  // the last slots' sums have been read
+#pragma unroll
+    for (int t = 0; t < 2; ++t) red[(wave * 2 + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    // acc[t][v]: token 4 h + v, slot s0 + 16 t + i
+    const float* rf = reinterpret_cast<const float*>(red);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int l2 = tid & 63, v = tid >> 6, slot = s0 + 16 * t + (l2 & 15);
+      const int64_t m = m0 + 4 * (l2 >> 4) + v;
+      if (m >= g.m) continue;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum += rf[((w * 2 + t) * 64 + l2) * 4 + v];
+      sum = slot < g.slots ? g.scale * sum : 0.0f;
+      if (g.out32 != nullptr && slot < g.slots) g.out32[m * g.slots + slot] = sum;
+      g.out16[m * g.rpad + slot] = to16<kF16>(g.scale2 * sum);
+    }
+  }
+}
+
+// The weight as it is stored, n x k: a thread takes words of eight codes, so that the
+// lanes of a store write neighbouring 16 bytes.
+constexpr int kWords = 4;
+
+template <bool kDQ, bool kF16>
+__global__ __launch_bounds__(kThreads) void restore_kernel(PackedW w, uint16_t* out, Levels L, int narrow_blocks,
+                                                           Narrow g) {
+  __shared__ f32x4 red[4 * 2 * 64];
+  if (static_cast<int>(blockIdx.x) < narrow_blocks) {
+    narrow_tile<kF16, false>(g, blockIdx.x, red);
+    return;
+  }
+  const int64_t words = w.n * w.k / 8;  // a multiple of 128
+  const int64_t first = static_cast<int64_t>(blockIdx.x - narrow_blocks) * (kWords * kThreads) + threadIdx.x;
+  uint32_t c[kWords], code[kWords];
+  float value[kWords];
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    const int64_t at = first + j * kThreads < words ? first + j * kThreads : words - 1;
+    c[j] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(w.codes) + at);
+    const int64_t block = at / 8;
+    code[j] = kDQ ? w.scale_codes[block] : 0;
+    value[j] = kDQ ? w.group_scale[block / 256] : w.absmax[block];
+  }
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    const BlockLut lut = make_block_lut<kF16>(L.v, kDQ ? dq_unit(code[j], w.dq) * value[j] : value[j]);
+    uint32_t v[4];
+    lut8_natural_order(lut, c[j], v);
+    const int64_t at = first + j * kThreads;
+    if (at < words) st16(out + at * 8, u32x4{v[0], v[1], v[2], v[3]});
+  }
+}
+
+// The weight's transpose, k x n. A workgroup takes 64 weight rows and 4 of their
+// 64-weight blocks: a lane restores one block of one row and writes it down LDS
+// columns, which leave as whole 128-byte runs. A^T for the product's adapter slots is
+// made here too.
 constexpr int kTrRows = 64, kTrBlocks = 4;
 constexpr int kTrLd = kTrRows + 8;  // elements of an LDS row: 16-byte reads stay aligned, rows shift by 4 banks
 
 template <bool kDQ, bool kF16>
-__global__ __launch_bounds__(256) void restore_t_kernel(PackedW w, uint16_t* out, Levels L, int64_t blocks,
-                                                        Adapter ad) {
+__global__ __launch_bounds__(kThreads) void restore_t_kernel(PackedW w, uint16_t* out, Levels L, int narrow_blocks,
+                                                             Narrow g, const uint16_t* a, uint16_t* at, int at_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[kTrBlocks * 64 * kTrLd];
-  static_assert(kTrTile <= kTrBlocks * 64 * kTrLd, "both transposes use the tile");
-  if (blockIdx.x >= blocks) {
-    lora_transpose_tile(tile, blockIdx.x - blocks, ad.a, ad.b, w.n, w.k, ad.r, ad.rpad, ad.parts, ad.at, ad.bt);
+  static_assert(kTrTile <= kTrBlocks * 64 * kTrLd && 4 * 2 * 64 * 16 <= sizeof(tile), "all use the tile");
+  if (static_cast<int>(blockIdx.x) < narrow_blocks) {
+    narrow_tile<kF16, true>(g, blockIdx.x, reinterpret_cast<f32x4*>(tile));
+    return;
+  }
+  const int64_t id = blockIdx.x - narrow_blocks;
+  if (id < at_blocks) {  // the first k / 64 of its tiles are A's
+    lora_transpose_tile(tile, id, a, nullptr, w.n, w.k, g.slots, g.rpad, g.parts, at, nullptr);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t nbk = w.k / 64, tiles_k = (nbk + kTrBlocks - 1) / kTrBlocks;
-  const int64_t n0 = blockIdx.x / tiles_k * kTrRows, b0 = blockIdx.x % tiles_k * kTrBlocks;
+  const int64_t n0 = (id - at_blocks) / tiles_k * kTrRows, b0 = (id - at_blocks) % tiles_k * kTrBlocks;
   const int64_t n = n0 + lane < w.n ? n0 + lane : w.n - 1, kb = b0 + wave < nbk ? b0 + wave : nbk - 1;
   const int64_t block = n * nbk + kb;
   const u32x4 c0 = ld16(w.codes + block * 32), c1 = ld16(w.codes + block * 32 + 16);
@@ -413,6 +529,8 @@ __global__ __launch_bounds__(256) void restore_t_kernel(PackedW w, uint16_t* out
   }
 }
 
+int narrow_blocks(const Narrow& g) { return g.rpad > 0 ? static_cast<int>((g.m + 15) / 16) : 0; }
+
 }  // namespace
 
 hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const uint16_t* x, int64_t m,
@@ -423,18 +541,32 @@ hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const 
   return launch_product<true>(g, f16, st);
 }
 
-hipError_t launch_restore_t(const PackedW& w, uint16_t* out, const uint16_t* a, const uint16_t* b, int r, int rpad,
-                            uint16_t* at, uint16_t* bt, const LoraParts* parts, hipStream_t st, bool f16) {
+hipError_t launch_restore(const PackedW& w, uint16_t* w16, const uint16_t* x, int64_t m, const uint16_t* a, int slots,
+                          int rpad, float s, float* h32, uint16_t* hs, hipStream_t st, bool f16) {
+  const Narrow g{x, m, w.k, a, slots, rpad, LoraParts{}, 1.0f, s, h32, hs};
+  const int first = narrow_blocks(g);
+  const int64_t grid = first + (w.n * w.k / 8 + kWords * kThreads - 1) / (kWords * kThreads);
+  auto kern = f16 ? (w.dq ? restore_kernel<true, true> : restore_kernel<false, true>)
+                  : (w.dq ? restore_kernel<true, false> : restore_kernel<false, false>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, w, w16,
+                     codebook_table(w.codebook), first, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy, int64_t m, const uint16_t* a,
+                            const uint16_t* b, int slots, int rpad, const LoraParts* parts, float s, float* dh32,
+                            uint16_t* dhs, uint16_t* at, hipStream_t st, bool f16) {
   LoraParts one;
-  one.rpart = r;
+  one.rpart = slots;
   one.end[0] = static_cast<int>(w.n);
-  const Adapter ad{a, b, r, rpad, parts != nullptr ? *parts : one, at, bt};
-  const int64_t blocks = (w.n + kTrRows - 1) / kTrRows * ((w.k / 64 + kTrBlocks - 1) / kTrBlocks);
+  const Narrow g{dy, m, w.n, b, slots, rpad, parts != nullptr ? *parts : one, s, 1.0f, dh32, dhs};
+  const int first = narrow_blocks(g), at_blocks = rpad > 0 && wt16 != nullptr ? static_cast<int>(w.k / kTrCols) : 0;
+  const int64_t weight = (w.n + kTrRows - 1) / kTrRows * ((w.k / 64 + kTrBlocks - 1) / kTrBlocks);
+  const int64_t grid = first + at_blocks + (wt16 != nullptr ? weight : 0);
   auto kern = f16 ? (w.dq ? restore_t_kernel<true, true> : restore_t_kernel<false, true>)
                   : (w.dq ? restore_t_kernel<true, false> : restore_t_kernel<false, false>);
-  const int64_t grid = blocks + (r > 0 ? lora_transpose_tiles(w.n, w.k) : 0);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, w, out, codebook_table(w.codebook),
-                     blocks, ad);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, w, wt16,
+                     codebook_table(w.codebook), first, g, a, at, at_blocks);
   return hipGetLastError();
 }
 

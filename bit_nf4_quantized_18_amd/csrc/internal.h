@@ -151,17 +151,21 @@ hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, con
 hipError_t launch_gemm_dx(const PackedW& w, const uint16_t* dy, int64_t m, const uint16_t* dhs,
                           const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16 = false);
 
-// The product over a weight restored to 16 bits in the workspace (dense_gemm.hip):
-// w16 as launch_dequantize writes it (n2 rows of k), wt16 as launch_restore_t
-// does (k rows of n). Other arguments as launch_gemm_gated and launch_gemm_dx.
-// For sizes that dense_fits (dense_rule.h).
+// The product over a weight restored to 16 bits in the workspace (dense_gemm.hip),
+// for sizes that dense_fits (dense_rule.h); other arguments as launch_gemm_gated and
+// launch_gemm_dx.
+// launch_restore: w16 (n x k), and with slots > 0 H = X A^T (h32, m x slots, may be
+// null) and hs (m x rpad, 16 bits of s H, zero-padded).
+hipError_t launch_restore(const PackedW& w, uint16_t* w16, const uint16_t* x, int64_t m, const uint16_t* a, int slots,
+                          int rpad, float s, float* h32, uint16_t* hs, hipStream_t st, bool f16);
 hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const uint16_t* x, int64_t m,
                               const uint16_t* hs, const uint16_t* b, int rpart, int rpad, int act, uint16_t* y,
                               uint16_t* p, hipStream_t st, bool f16);
-// launch_restore_t makes the adapter's transposes too (r > 0), as
-// launch_lora_transpose does.
-hipError_t launch_restore_t(const PackedW& w, uint16_t* out, const uint16_t* a, const uint16_t* b, int r, int rpad,
-                            uint16_t* at, uint16_t* bt, const LoraParts* parts, hipStream_t st, bool f16);
+// launch_restore_t: wt16 (k x n) unless it is null, and with slots > 0 dH = s dY B (dh32, and dhs in 16
+// bits, zero-padded to rpad) and at (k x rpad, A^T).
+hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy, int64_t m, const uint16_t* a,
+                            const uint16_t* b, int slots, int rpad, const LoraParts* parts, float s, float* dh32,
+                            uint16_t* dhs, uint16_t* at, hipStream_t st, bool f16);
 hipError_t launch_dense_dx(const uint16_t* wt16, int64_t n, int64_t k, const uint16_t* dy, int64_t m,
                            const uint16_t* dhs, const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16);
 
