@@ -445,7 +445,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
   uint16_t* wt16 = restores && dx != nullptr ? reinterpret_cast<uint16_t*>(base + L.w16) : nullptr;
   if (restores && r == 0)
     QLORA_TRY(qlora::launch_restore_t(pw, wt16, dy, m, nullptr, nullptr, 0, 0, nullptr, s, nullptr, nullptr, nullptr,
-                                      stream, f16));
+                                      nullptr, stream, f16));
 
   if (r > 0) {
     uint16_t* bt = reinterpret_cast<uint16_t*>(base + L.bt);
@@ -464,7 +464,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     // A^T, and B^T (block diagonal for grouped weights: part l's slots see
     // only its own output columns)
     if (restores) {
-      QLORA_TRY(qlora::launch_restore_t(pw, wt16, dy, m, a, b, r, rp, grp, s, dh32, dhs, at, stream, f16));
+      QLORA_TRY(qlora::launch_restore_t(pw, wt16, dy, m, a, b, r, rp, grp, s, dh32, dhs, at, bt, stream, f16));
     } else {
       QLORA_TRY(qlora::launch_lora_transpose(a, b, n, k, r, rp, at, bt, stream, grp));
     }
@@ -473,7 +473,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     // masked dX update need; the frozen-weight GEMM then runs without
     // adapter slots.
     if (drop != nullptr) dhs = nullptr;
-    if (!restores)
+    if (!restores || !qlora::dense_narrow(n, r))
       QLORA_TRY(qlora::launch_skinny_prefill(dy, bt, m, n, r, rp, drop != nullptr ? s * inv_keep : s, 1.0f, spart, dh32,
                                              dhs, stream, f16));
     if (x8 != nullptr) {

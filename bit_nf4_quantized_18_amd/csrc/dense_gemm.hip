@@ -404,6 +404,7 @@ __device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x
         if (!in) pv[c] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
+          if (t > 0 && s0 + 16 >= g.slots) continue;  // uniform: no second tile
           const int slot = s0 + 16 * t + i;
           if constexpr (!kCols) {
             wv[c][t] = ld16(g.w + static_cast<int64_t>(slot < g.slots ? slot : 0) * g.q + at);
@@ -425,7 +426,8 @@ __device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) acc[t] = mma16<kF16>(pv[c], wv[c][t], acc[t]);
+        for (int t = 0; t < 2; ++t)
+          if (t == 0 || s0 + 16 < g.slots) acc[t] = mma16<kF16>(pv[c], wv[c][t], acc[t]);
     }
     if (s0 > 0) __syncthreads();  // the last slots' sums have been read
 #pragma unroll
@@ -485,13 +487,14 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(PackedW w, uint16_t* 
 // The weight's transpose, k x n. A workgroup takes 64 weight rows and 4 of their
 // 64-weight blocks: a lane restores one block of one row and writes it down LDS
 // columns, which leave as whole 128-byte runs. A^T for the product's adapter slots is
-// made here too.
+// made here too, and where dH is not, B^T.
 constexpr int kTrRows = 64, kTrBlocks = 4;
 constexpr int kTrLd = kTrRows + 8;  // elements of an LDS row: 16-byte reads stay aligned, rows shift by 4 banks
 
 template <bool kDQ, bool kF16>
 __global__ __launch_bounds__(kThreads) void restore_t_kernel(PackedW w, uint16_t* out, Levels L, int narrow_blocks,
-                                                             Narrow g, const uint16_t* a, uint16_t* at, int at_blocks) {
+                                                             Narrow g, const uint16_t* a, uint16_t* at, uint16_t* bt,
+                                                             int tr_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[kTrBlocks * 64 * kTrLd];
   static_assert(kTrTile <= kTrBlocks * 64 * kTrLd && 4 * 2 * 64 * 16 <= sizeof(tile), "all use the tile");
   if (static_cast<int>(blockIdx.x) < narrow_blocks) {
@@ -499,13 +502,13 @@ __global__ __launch_bounds__(kThreads) void restore_t_kernel(PackedW w, uint16_t
     return;
   }
   const int64_t id = blockIdx.x - narrow_blocks;
-  if (id < at_blocks) {  // the first k / 64 of its tiles are A's
-    lora_transpose_tile(tile, id, a, nullptr, w.n, w.k, g.slots, g.rpad, g.parts, at, nullptr);
+  if (id < tr_blocks) {  // the first k / 64 of its tiles are A's
+    lora_transpose_tile(tile, id, a, g.w, w.n, w.k, g.slots, g.rpad, g.parts, at, bt);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t nbk = w.k / 64, tiles_k = (nbk + kTrBlocks - 1) / kTrBlocks;
-  const int64_t n0 = (id - at_blocks) / tiles_k * kTrRows, b0 = (id - at_blocks) % tiles_k * kTrBlocks;
+  const int64_t n0 = (id - tr_blocks) / tiles_k * kTrRows, b0 = (id - tr_blocks) % tiles_k * kTrBlocks;
   const int64_t n = n0 + lane < w.n ? n0 + lane : w.n - 1, kb = b0 + wave < nbk ? b0 + wave : nbk - 1;
   const int64_t block = n * nbk + kb;
   const u32x4 c0 = ld16(w.codes + block * 32), c1 = ld16(w.codes + block * 32 + 16);
@@ -555,18 +558,23 @@ hipError_t launch_restore(const PackedW& w, uint16_t* w16, const uint16_t* x, in
 
 hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy, int64_t m, const uint16_t* a,
                             const uint16_t* b, int slots, int rpad, const LoraParts* parts, float s, float* dh32,
-                            uint16_t* dhs, uint16_t* at, hipStream_t st, bool f16) {
+                            uint16_t* dhs, uint16_t* at, uint16_t* bt, hipStream_t st, bool f16) {
   LoraParts one;
   one.rpart = slots;
   one.end[0] = static_cast<int>(w.n);
   const Narrow g{dy, m, w.n, b, slots, rpad, parts != nullptr ? *parts : one, s, 1.0f, dh32, dhs};
-  const int first = narrow_blocks(g), at_blocks = rpad > 0 && wt16 != nullptr ? static_cast<int>(w.k / kTrCols) : 0;
+  const bool narrow = dense_narrow(w.n, slots);
+  const int first = narrow ? narrow_blocks(g) : 0;
+  const int tr_blocks = rpad == 0                     ? 0
+                        : !narrow                     ? static_cast<int>(lora_transpose_tiles(w.n, w.k))
+                        : wt16 != nullptr             ? static_cast<int>(w.k / kTrCols)
+                                                      : 0;
   const int64_t weight = (w.n + kTrRows - 1) / kTrRows * ((w.k / 64 + kTrBlocks - 1) / kTrBlocks);
-  const int64_t grid = first + at_blocks + (wt16 != nullptr ? weight : 0);
+  const int64_t grid = first + tr_blocks + (wt16 != nullptr ? weight : 0);
   auto kern = f16 ? (w.dq ? restore_t_kernel<true, true> : restore_t_kernel<false, true>)
                   : (w.dq ? restore_t_kernel<true, false> : restore_t_kernel<false, false>);
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, w, wt16,
-                     codebook_table(w.codebook), first, g, a, at, at_blocks);
+                     codebook_table(w.codebook), first, g, a, at, bt, tr_blocks);
   return hipGetLastError();
 }
 

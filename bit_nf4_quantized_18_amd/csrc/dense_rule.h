@@ -10,6 +10,15 @@ namespace qlora {
 // Longest contraction of the dense kernels: 32-bit offsets in a tile of 256 rows.
 constexpr int64_t kDenseMaxK = 65536;
 
+// Whether dH = s dY B over n weight rows and `slots` adapter slots is formed beside the
+// restoring, 16 tokens a workgroup whose lanes read B in strided loads, 32 slots at a
+// time, or behind it from B^T. Whole calls, us, beside / behind, 17 and 2048 tokens:
+//   1040 x 1088, 16 slots  18.2 / 23.3, 34.5 / 39.2; 64 slots 27.3 / 28.6, 50.6 / 54.6
+//   2048 x 2048, 16 slots  22.4 / 24.1, 45.4 / 48.4; 64 slots 34.3 / 29.3, 65.3 / 65.1
+//   4096 x 4096, 16 slots  43.4 / 39.5, 95.5 / 97.6; 64 slots 65.5 / 43.6, 135.8 / 116.3
+constexpr int64_t kDenseNarrow = 2048;
+inline bool dense_narrow(int64_t n, int slots) { return n * ((slots + 31) / 32) <= kDenseNarrow; }
+
 // m tokens, `out` weight rows along the outputs (of the stored weight or of its
 // transpose), `con` elements of contraction.
 inline bool dense_fits(int64_t m, int64_t out, int64_t con) {
@@ -17,23 +26,25 @@ inline bool dense_fits(int64_t m, int64_t out, int64_t con) {
 }
 
 // The two sides' microseconds, fitted to 114 measured calls (17 .. 4096 tokens, 0.5 M
-// .. 360 M weights, forward and backward), where the smaller estimate names the slower
-// side by more than 2% once. Fused: rounds of the 256 CUs over 256 x 128 tiles, in steps
-// of 64. Dense: 2.5 bytes a weight to restore it, then the tiles of the 8-bit product,
-// whose units of 128 bytes take about as long, or reading 2 bytes a weight.
+// .. 360 M weights, forward and backward, rank 16), where the smaller estimate names the
+// slower side by more than 2% twice (3% and 4%). Fused: rounds of the 256 CUs over 256 x
+// 128 tiles, in steps of 64, and H or dH in launches of their own. Dense: 2.5 bytes a
+// weight to restore it, then the tiles of the 8-bit product, whose units of 128 bytes
+// take about as long, or reading 2 bytes a weight.
 // Some of the calls, fused / dense, us:
 //   tokens                            64           333          2048         4096
-//   forward 22016 x 4096          65 / 96     123 / 147     382 / 360    712 / 635
-//   forward 2560 x 5120           75 / 47       79 / 44       81 / 95    159 / 133
-//   forward 5120 x 1088           31 / 25       32 / 29       55 / 51      78 / 85
+//   forward 22016 x 4096          65 / 71     123 / 121     392 / 350    745 / 647
+//   forward 44032 x 8192        221 / 350                 1389 / 1279
+//   forward 2560 x 5120           75 / 41       79 / 42       81 / 78    158 / 121
+//   forward 5120 x 1088           30 / 18       31 / 23       55 / 43      83 / 73
 //   tokens                            64           256          1024         4096
-//   backward 22016 x 4096       278 / 129     282 / 155     296 / 280    711 / 627
-//   backward 4096 x 11008         73 / 57       74 / 71     141 / 126    402 / 334
-//   backward 8192 x 22016       119 / 227     123 / 261     370 / 468
+//   backward 22016 x 4096       278 / 108     282 / 136     294 / 258    735 / 650
+//   backward 4096 x 11008         72 / 53       74 / 66     141 / 121    409 / 347
+//   backward 8192 x 22016       119 / 222     123 / 253     382 / 462
 inline bool dense_pays(int64_t m, int64_t out, int64_t con) {
   if (!dense_fits(m, out, con)) return false;
   const int64_t tiles = ((m + 255) / 256) * ((out + 127) / 128);
-  const double fused = static_cast<double>((tiles + 255) / 256) * (6 + 0.9 * static_cast<double>((con + 63) / 64));
+  const double fused = 6 + static_cast<double>((tiles + 255) / 256) * (6 + 0.9 * static_cast<double>((con + 63) / 64));
   const double weights = static_cast<double>(out) * static_cast<double>(con);
   const double product = pick_shape(m, out, 2 * con).us, read = weights * 2 / 3.0e6;
   return weights * 2.5 / 5.0e6 + (product > read ? product : read) < fused;

@@ -161,11 +161,12 @@ hipError_t launch_restore(const PackedW& w, uint16_t* w16, const uint16_t* x, in
 hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const uint16_t* x, int64_t m,
                               const uint16_t* hs, const uint16_t* b, int rpart, int rpad, int act, uint16_t* y,
                               uint16_t* p, hipStream_t st, bool f16);
-// launch_restore_t: wt16 (k x n) unless it is null, and with slots > 0 dH = s dY B (dh32, and dhs in 16
-// bits, zero-padded to rpad) and at (k x rpad, A^T).
+// launch_restore_t: wt16 (k x n) unless it is null, and with slots > 0 A^T (at, k x
+// rpad, with wt16) and, where dense_narrow(w.n, slots), dH = s dY B (dh32, and dhs in 16 bits,
+// zero-padded to rpad); otherwise B^T (bt, rpad x n), for launch_skinny_prefill.
 hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy, int64_t m, const uint16_t* a,
                             const uint16_t* b, int slots, int rpad, const LoraParts* parts, float s, float* dh32,
-                            uint16_t* dhs, uint16_t* at, hipStream_t st, bool f16);
+                            uint16_t* dhs, uint16_t* at, uint16_t* bt, hipStream_t st, bool f16);
 hipError_t launch_dense_dx(const uint16_t* wt16, int64_t n, int64_t k, const uint16_t* dy, int64_t m,
                            const uint16_t* dhs, const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16);
 

@@ -4,8 +4,10 @@
 // as one launch over two problems out[j][c] = sum_m U[m][j] V[m][c], U float32
 // (dH times the row's scale; H) and V the codes (exact in bf16) or dY.
 //
-// Bound by reading V once: k + 2 n bytes a token, half the 16-bit input's.
-// 2048 tokens: k = 11008, n = 4096 holds 39 MB.
+// Bound by reading V once: k + 2 n bytes a token. 2048 tokens, rank 16: k = 11008, n =
+// 4096 holds 39 MB and takes 13.7 us (2.9 TB/s), and 5 for the sums of two splits; k =
+// 4096, n = 22016 in two parts 99 MB in 32 us (3.1 TB/s). With what a step computes from
+// its loads in front of the step before it, whose loads then wait for it, 25 us for 14.
 //
 // Matrix cores in bf16 with float32 sums (v_mfma_f32_16x16x32_bf16), every
 // float32 U split into three bf16 terms that hold all of its 24 bits (the low 16
@@ -123,38 +125,44 @@ __device__ __forceinline__ void solve(const Problem& p, int64_t M, int id, int s
 #pragma unroll
     for (int t = 0; t < 8; ++t) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Rows past the last are read from it and multiplied by zeros.
+  // A step's operands as loaded; nothing is computed from them before the step, so
+  // that the next one's loads are in flight under it. Rows past the last are read
+  // from it and multiplied by zeros.
   typedef typename Block<kKind>::Word Word;
-  auto load = [&](int64_t m0, Block<kKind>& b, float (&uv)[RT][8]) {
+  struct Step {
+    Block<kKind> b;
+    float u[RT][8], scale[kKind == kCodes ? 8 : 1];
+  };
+  auto load = [&](int64_t m0, Step& s) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int64_t m = m0 + 8 * g + e;
       const int64_t mr = m < M ? m : M - 1;
       const char* row = static_cast<const char*>(p.v) + (mr * p.ldv + col) * (kKind == kCodes ? 1 : 2);
-      b.w[e] = *reinterpret_cast<const Word*>(row);
-      const float sc = p.uscale != nullptr ? p.uscale[mr] : 1.0f;
+      s.b.w[e] = *reinterpret_cast<const Word*>(row);
+      if (kKind == kCodes) s.scale[e] = p.uscale[mr];
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
         const int j = j0 + 16 * a + i;
-        const float f = u[mr * p.ldu + (j < p.slots ? j : 0)];
-        uv[a][e] = m < me && j < p.slots ? f * sc : 0.0f;
+        s.u[a][e] = u[mr * p.ldu + (j < p.slots ? j : 0)];
       }
     }
   };
-  Block<kKind> b, nb;
-  float uv[RT][8], nu[RT][8];
-  int64_t m0 = mb + wave * kRows;
-  if (m0 < me) load(m0, b, uv);
-  for (; m0 < me; m0 += kWaves * kRows) {
-    const bool more = m0 + kWaves * kRows < me;
-    if (more) load(m0 + kWaves * kRows, nb, nu);
+  auto multiply = [&](int64_t m0, const Step& s) {
     Terms terms[RT];
 #pragma unroll
-    for (int a = 0; a < RT; ++a) terms[a] = split3(uv[a]);
+    for (int a = 0; a < RT; ++a) {
+      float uv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        uv[e] = m0 + 8 * g + e < me && j0 + 16 * a + i < p.slots ? (kKind == kCodes ? s.u[a][e] * s.scale[e] : s.u[a][e])
+                                                                 : 0.0f;
+      terms[a] = split3(uv);
+    }
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       u32x4 low;
-      const u32x4 v = operand<kKind>(b, t, &low);
+      const u32x4 v = operand<kKind>(s.b, t, &low);
 #pragma unroll
       for (int a = 0; a < RT; ++a)
 #pragma unroll
@@ -162,14 +170,23 @@ __device__ __forceinline__ void solve(const Problem& p, int64_t M, int id, int s
           acc[a][t] = mma16<false>(terms[a].t[q], v, acc[a][t]);
           if (kKind == kHalf) acc[a][t] = mma16<false>(terms[a].t[q], low, acc[a][t]);
         }
+      if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two operands in registers at a time, not all eight
     }
-    if (more) {
-      b = nb;
-#pragma unroll
-      for (int a = 0; a < RT; ++a)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) uv[a][e] = nu[a][e];
-    }
+  };
+  constexpr int kStride = kWaves * kRows;
+  Step s0, s1;
+  int64_t m0 = mb + wave * kRows;
+  if (m0 < me) load(m0, s0);
+  for (; m0 < me; m0 += 2 * kStride) {
+    if (m0 + kStride < me) load(m0 + kStride, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(m0, s0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (m0 + kStride >= me) break;
+    if (m0 + 2 * kStride < me) load(m0 + 2 * kStride, s0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(m0 + kStride, s1);
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // acc[a][t][v]: slot j0 + 16 a + 4 g + v, column c0 + 8 i + t. Thread q sums
@@ -231,18 +248,22 @@ __global__ __launch_bounds__(256) void rank_grad8_final_kernel(const float* part
   db[c * r + j] = scale * sum;
 }
 
-int slot_tiles(int slots) { return slots > 16 ? 2 : 1; }  // of a workgroup
+// 16-slot tiles of a workgroup, by the rank of a part: grouped calls read the codes
+// once for every 16 of their slots, which are few next to dY.
+int slot_tiles(int r) { return r > 16 ? 2 : 1; }
 
-int64_t workgroups(int64_t n, int64_t k, int slots, int r, int rt) {
-  return (k + kCols - 1) / kCols * ((slots + 16 * rt - 1) / (16 * rt)) +
-         (n + kCols - 1) / kCols * ((r + 16 * rt - 1) / (16 * rt));
+int tiles_of(int slots, int rt) { return (slots + 16 * rt - 1) / (16 * rt); }
+int64_t workgroups(int64_t n, int64_t k, int slots, int r) {
+  return (k + kCols - 1) / kCols * tiles_of(slots, slot_tiles(r)) + (n + kCols - 1) / kCols * tiles_of(r, slot_tiles(r));
 }
 
 }  // namespace
 
 int rank_grad8_splits(int64_t m, int64_t n, int64_t k, int slots, int r) {
-  // about two workgroups a CU, a step at least for each of a workgroup's waves
-  int64_t s = 512 / workgroups(n, k, slots, r, slot_tiles(slots));
+  // About a workgroup a CU, a step at least for each of its waves. 2048 tokens, n = 4096,
+  // k = 11008: 13.7 us with two splits, 16.0 with four; k = 4096, n = 22016 in two parts:
+  // 32 us and no second launch with one, 33 and 6 with two.
+  int64_t s = 256 / workgroups(n, k, slots, r);
   const int64_t by_rows = m / (kWaves * kRows);
   if (s > by_rows) s = by_rows;
   if (s > 16) s = 16;
@@ -255,17 +276,16 @@ hipError_t launch_rank_grads8(const float* dh, const int8_t* x, int64_t ldx, con
                               bool f16) {
   const int r = parts != nullptr ? parts->rpart : slots;
   const int splits = rank_grad8_splits(m, n, k, slots, r);
-  const int rt = slot_tiles(slots);
   const int64_t per = ((m + splits - 1) / splits + kRows - 1) / kRows * kRows;
   float* part1 = part + static_cast<int64_t>(splits) * slots * k;
   auto strips = [](int64_t c) { return static_cast<int>((c + kCols - 1) / kCols); };
   const Problem pa{dh, xscale, x, splits == 1 ? da : part, nullptr, 1.0f, k, ldx, slots, slots, strips(k),
-                   (slots + 16 * rt - 1) / (16 * rt), LoraParts{}};
+                   tiles_of(slots, slot_tiles(r)), LoraParts{}};
   const Problem pb{h, nullptr, dy, part1, splits == 1 ? db : nullptr, scale, n, n, slots, r, strips(n),
-                   (r + 16 * rt - 1) / (16 * rt), parts != nullptr ? *parts : LoraParts{}};
-  const unsigned grid = static_cast<unsigned>(workgroups(n, k, slots, r, rt) * splits);
-  auto kern = rt == 1 ? (f16 ? rank_grad8_kernel<true, 1> : rank_grad8_kernel<false, 1>)
-                      : (f16 ? rank_grad8_kernel<true, 2> : rank_grad8_kernel<false, 2>);
+                   tiles_of(r, slot_tiles(r)), parts != nullptr ? *parts : LoraParts{}};
+  const unsigned grid = static_cast<unsigned>(workgroups(n, k, slots, r) * splits);
+  auto kern = slot_tiles(r) == 1 ? (f16 ? rank_grad8_kernel<true, 1> : rank_grad8_kernel<false, 1>)
+                                 : (f16 ? rank_grad8_kernel<true, 2> : rank_grad8_kernel<false, 2>);
   hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), 0, st, pa, pb, m, splits, per);
   if (splits > 1) {
     const int64_t na = static_cast<int64_t>(slots) * k, total = na + n * r;
