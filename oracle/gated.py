@@ -31,10 +31,10 @@ def value(g, act):
 
 def slope(g, act):
     g = np.asarray(g, dtype=np.float64)
-    t = np.clip(g, -200.0, 200.0)  # beyond, sigma (1 - sigma) is 0 next to any factor here
+    t = np.clip(g, -200.0, 200.0)  # beyond, act' is within 1e-84 of its limits, 0 and 1
     z, tz = _z(t, act)
     s, r = _sigma(z), _sigma(-z)
-    return np.where(np.isnan(g), np.nan, s + tz * s * r)
+    return np.where(np.isnan(g), np.nan, np.where(g < -200.0, 0.0, s + tz * s * r))
 
 
 def fwd(g, u, act):

@@ -1,0 +1,244 @@
+"""Host checks of the gated-block calls and of the backward calls from 8-bit rows (no GPU): the C ABI and the binding
+refuse what they do not take, before any launch. Fake aligned addresses, far apart, and CPU tensors stand in."""
+import ctypes
+
+import pytest
+import torch
+
+from bit_nf4_quantized_18_amd import binding as B
+
+G = 1 << 32  # buffers stand this far apart
+AT = {name: (i + 1) * G for i, name in enumerate(
+    ("codes", "sc", "gs", "x", "a", "b", "y", "p", "h", "ws", "dy", "dx", "da", "db", "xs"))}
+BF16, F32, F16 = B.QLORA_BF16, B.QLORA_F32, B.QLORA_F16
+
+
+def weight(n=512, k=128, dq=1):
+    return B.NF4WeightC(n, k, AT["codes"], AT["sc"], AT["gs"], None, dq, 0)
+
+
+def gated_call(w=None, f16=False, **over):
+    v = {**AT, "m": 40, "r": 16, "act": 0, "n": 512, "k": 128, **over}
+    w = weight(v["n"], v["k"]) if w is None else w
+    need = B.gated_workspace_bytes(v["m"], v["n"], v["k"], v["r"])
+    fn = B.load().qlora_linear_fwd_gated_f16 if f16 else B.load().qlora_linear_fwd_gated
+    return fn(ctypes.byref(w), v["x"], v["m"], v["a"], v["b"], v["r"], 32.0, v["act"], v["y"], v["p"], v["h"], v["ws"],
+              v.get("bytes", need), None)
+
+
+def test_gated_forward_refuses():
+    for f16 in (False, True):
+        call = lambda **v: gated_call(f16=f16, **v)  # noqa: E731
+        assert call(act=2) == -4 and call(act=-1) == -4 and call(r=65) == -4 and call(r=-1) == -2
+        assert call(n=256) == -2 and call(n=768) == -2 and call(k=100) == -2 and call(m=-1) == -2
+        assert call(m=(1 << 31) + 1) == -2
+        for name in ("x", "a", "b", "p"):
+            assert call(**{name: None}) == -1, name
+        for name in ("x", "a", "b", "p", "y", "h", "ws"):
+            assert call(**{name: AT[name] + 8}) == -3, name
+        assert call(ws=None) == -5 and call(bytes=10) == -5
+        for m in (1, 16):
+            assert call(m=m, bytes=4 * m * 32 - 1) == -5
+        assert call(m=0, x=None, p=None, ws=None) == 0
+        assert call(m=0, n=768) == -2
+        # outputs over inputs, over each other, over the workspace
+        for a, b in (("p", "x"), ("y", "x"), ("h", "x"), ("ws", "x"), ("p", "a"), ("p", "b"), ("y", "codes"), ("p", "y"),
+                     ("h", "p"), ("ws", "p"), ("ws", "y"), ("ws", "h")):
+            assert call(**{a: AT[b]}) == -4, (a, b)
+        assert call(p=AT["y"] + 40 * 1024 - 16) == -4 and call(p=AT["x"] - 40 * 512 + 16) == -4
+    assert gated_call(w=weight(dq=3)) == -4
+
+
+def test_gated_workspace_sizes():
+    ws = B.gated_workspace_bytes
+    assert ws(0, 512, 128, 16) == 0 and ws(10, 512, 128, 65) == 0 and ws(10, 512, 128, -1) == 0
+    assert ws(1, 22016, 4096, 0) == 0 and ws(16, 22016, 4096, 16) == 16 * 32 * 4
+    assert ws(333, 5120, 1088, 0) == 2 * 5120 * 1088  # the restored weight alone
+    assert ws(64, 44032, 8192, 0) == 0  # restored as it is multiplied
+    x8 = B.x8_workspace_bytes
+    assert x8(10, 512, 128, 5, 16) == 0 and x8(10, 512, 128, 3, 64) == 0 and x8(10, 512, 128, 0, 16) == 0
+    assert x8(77, 1040, 1088, 1, 0) == 2 * 1040 * 1088
+
+
+def test_elementwise_refuses():
+    lib = B.load()
+    Y, P, D, C, S = G, 2 * G, 3 * G, 4 * G, 5 * G
+
+    def fwd(y=Y, t=BF16, m=4, n=100, act=0, p=P):
+        return lib.qlora_gated_fwd(y, t, m, n, act, p, None)
+
+    def fwd8(c=C, ld=128, s=S, t=BF16, m=4, n=100, act=0, p=P):
+        return lib.qlora_gated_fwd_x8(c, ld, s, t, m, n, act, p, None)
+
+    def bwd(y=Y, d=D, t=BF16, m=4, n=100, act=0, p=P):
+        return lib.qlora_gated_bwd(y, d, t, m, n, act, p, None)
+
+    def bwd8(c=C, ld=128, s=S, d=D, t=BF16, m=4, n=100, act=0, p=P):
+        return lib.qlora_gated_bwd_x8(c, ld, s, d, t, m, n, act, p, None)
+
+    for f in (fwd, fwd8, bwd, bwd8):
+        assert f(t=3) == -4 and f(act=2) == -4 and f(n=0) == -2 and f(m=-1) == -2 and f(m=1 << 30) == -2
+        assert f(n=(1 << 22) + 1) == -2 and f(p=None) == -1 and f(p=P + 4) == -3
+        assert f(m=0, p=None) == 0
+    for f in (fwd8, bwd8):
+        assert f(ld=64) == -2 and f(ld=120) == -2 and f(c=None) == -1 and f(s=None) == -1
+        assert f(c=C + 8) == -3 and f(s=S + 4) == -3
+        assert f(p=C) == -4 and f(p=S) == -4
+    for f in (fwd, bwd):
+        assert f(y=None) == -1 and f(y=Y + 2) == -3
+    for f in (bwd, bwd8):
+        assert f(d=None) == -1 and f(d=D + 2) == -3 and f(p=D) == -4 and f(p=D - 16) == -4
+    assert fwd(p=Y) == -4  # a row of P lies over the next rows of [G | U]
+    assert bwd(p=Y + 16) == -4 and bwd(p=Y - 16) == -4
+
+
+def test_int8_block_refuses():
+    lib = B.load()
+    W, SW, X, SX, P = (i * G for i in range(1, 6))
+
+    def f(w=W, sw=SW, n=64, k=128, x=X, sx=SX, m=4, act=0, t=BF16, p=P):
+        return lib.qlora_int8_linear_fwd_gated(w, sw, n, k, x, sx, m, act, t, p, None)
+
+    assert f(t=9) == -4 and f(act=2) == -4
+    for name in ("w", "sw", "x", "sx", "p"):
+        assert f(**{name: None}) == -1 and f(**{name: {"w": W, "sw": SW, "x": X, "sx": SX, "p": P}[name] + 4}) == -3
+    assert f(n=0) == -2 and f(n=(1 << 21) + 1) == -2 and f(k=100) == -2 and f(k=131072) == -2 and f(m=-1) == -2
+    assert f(m=0, x=None, p=None) == 0
+    for at in (W, SW, X, SX, W - 16, W + 2 * 64 * 128 - 16):
+        assert f(p=at) == -4
+
+
+def x8_call(grouped=False, f16=False, **over):
+    v = {**AT, "m": 40, "r": 16, "n": 512, "k": 128, "ld": 128, "g": 2, "parts": (256, 256), **over}
+    need = B.x8_workspace_bytes(v["m"], v["n"], v["k"], v["g"] if grouped else 1, v["r"])
+    name = "qlora_linear_bwd" + ("_grouped" if grouped else "") + "_x8" + ("_f16" if f16 else "")
+    lead = (v["g"], None if v["parts"] is None else B._parts(v["parts"])) if grouped else ()
+    return getattr(B.load(), name)(ctypes.byref(weight(v["n"], v["k"])), *lead, v["x"], v["ld"], v["xs"], v["dy"], v["m"],
+                                   v["a"], v["b"], v["r"], 32.0, v["h"], v["dx"], v["da"], v["db"], v["ws"],
+                                   v.get("bytes", need), None)
+
+
+def test_backward_from_rows_refuses():
+    for grouped in (False, True):
+        for f16 in (False, True):
+            call = lambda **v: x8_call(grouped, f16, **v)  # noqa: E731
+            for name in ("x", "xs", "h", "dy", "a", "b", "da", "db"):
+                assert call(**{name: None}) == -1, name
+            for name in ("x", "xs", "h", "dy", "a", "b", "da", "db", "dx", "ws"):
+                assert call(**{name: AT[name] + 4}) == -3, name
+            assert call(ld=64) == -2 and call(ld=130) == -2 and call(ld=(1 << 22) + 64) == -2
+            assert call(k=100) == -2 and call(m=-1) == -2
+            assert call(ws=None) == -5 and call(bytes=100) == -5
+            for a, b in (("dx", "dy"), ("dx", "x"), ("da", "x"), ("db", "h"), ("da", "xs"), ("ws", "dy"), ("dx", "da"),
+                         ("da", "db"), ("ws", "dx"), ("dx", "codes"), ("db", "b"), ("da", "a")):
+                assert call(**{a: AT[b]}) == -4, (a, b)
+    assert x8_call(r=129) == -4 and x8_call(r=-1) == -2
+    assert x8_call(True, r=8) == -4 and x8_call(True, parts=(256, 128)) == -2 and x8_call(True, parts=None) == -1
+    assert x8_call(True, g=5) == -2
+
+
+def packed(n=512, k=128):
+    return B.PackedNF4(n, k, torch.zeros(n * k // 2, dtype=torch.uint8), True, torch.zeros(n * k // 64, dtype=torch.uint8),
+                       torch.zeros(-(-n * k // 16384)))
+
+
+def rows(n, k, ld=None):
+    return B.PackedInt8(n, k, torch.zeros(n, ld or -(-k // 64) * 64, dtype=torch.int8), torch.zeros(n))
+
+
+def test_binding_refuses_gated_tensors():
+    t = torch.bfloat16
+    q, x, a, b = packed(), torch.zeros(3, 128, dtype=t), torch.zeros(32, 128, dtype=t), torch.zeros(512, 16, dtype=t)
+    f = B.linear_fwd_gated
+    with pytest.raises(TypeError, match="x must be"):
+        f(q, x.float(), a, b, 2.0)
+    with pytest.raises(ValueError, match="x has shape"):
+        f(q, x[:, :64].contiguous(), a, b, 2.0)
+    with pytest.raises(ValueError, match="a has shape"):
+        f(q, x, a[:16], b, 2.0)
+    with pytest.raises(ValueError, match="together"):
+        f(q, x, None, b, 2.0)
+    with pytest.raises(TypeError, match="b has dtype"):
+        f(q, x, a, b.half(), 2.0)
+    with pytest.raises(ValueError, match="out has shape"):
+        f(q, x, a, b, 2.0, out=torch.zeros(3, 512, dtype=t))
+    with pytest.raises(ValueError, match="y_out must be contiguous"):
+        f(q, x, a, b, 2.0, y_out=torch.zeros(512, 3, dtype=t).t())
+    with pytest.raises(TypeError, match="h_out has dtype"):
+        f(q, x, a, b, 2.0, h_out=torch.zeros(3, 32, dtype=t))
+    with pytest.raises(ValueError, match="ws must be"):
+        f(q, x, a, b, 2.0, ws=torch.zeros(4))
+    with pytest.raises(ValueError, match="on the GPU"):
+        f(q, x, a, b, 2.0)
+
+
+def test_binding_refuses_elementwise_tensors():
+    y = torch.zeros(3, 20)
+    with pytest.raises(ValueError, match="columns"):
+        B.gated_fwd(torch.zeros(3, 21))
+    with pytest.raises(ValueError, match="contiguous"):
+        B.gated_fwd(torch.zeros(20, 3).t())
+    with pytest.raises(TypeError, match="must be bfloat16"):
+        B.gated_fwd(y.double())
+    with pytest.raises(TypeError, match="must agree"):
+        B.gated_fwd(y, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="out has shape"):
+        B.gated_fwd(y, out=torch.zeros(3, 20))
+    with pytest.raises(ValueError, match="two a token"):
+        B.gated_fwd(rows(5, 10))
+    with pytest.raises(TypeError, match="dtype must be"):
+        B.gated_fwd(rows(4, 10), dtype=torch.int8)
+    with pytest.raises(ValueError, match="dp must have shape"):
+        B.gated_bwd(y, torch.zeros(3, 9))
+    with pytest.raises(TypeError, match="dp has dtype"):
+        B.gated_bwd(y, torch.zeros(3, 10, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="dp must be contiguous"):
+        B.gated_bwd(y, torch.zeros(10, 3).t())
+    with pytest.raises(TypeError, match="out has dtype"):
+        B.gated_bwd(y, torch.zeros(3, 10), out=torch.zeros(3, 20, dtype=torch.bfloat16))
+    for call in (lambda: B.gated_fwd(y), lambda: B.gated_bwd(y, torch.zeros(3, 10)), lambda: B.gated_fwd(rows(4, 10))):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
+
+
+def test_binding_refuses_int8_block():
+    f = B.int8_linear_fwd_gated
+    with pytest.raises(ValueError, match="as many of up's"):
+        f(rows(7, 100), rows(3, 100))
+    with pytest.raises(ValueError, match="rows of 99"):
+        f(rows(8, 100), rows(3, 99))
+    with pytest.raises(ValueError, match="padded to the same length"):
+        f(rows(8, 100), rows(3, 100, 192))
+    with pytest.raises(ValueError, match="out has shape"):
+        f(rows(8, 100), rows(3, 100), out=torch.zeros(3, 8, dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="dtype must be"):
+        f(rows(8, 100), rows(3, 100), dtype=torch.float64)
+    with pytest.raises(ValueError, match="on the GPU"):
+        f(rows(8, 100), rows(3, 100))
+
+
+def test_binding_refuses_backward_tensors():
+    t = torch.bfloat16
+    q, x, dy = packed(), rows(3, 128), torch.zeros(3, 512, dtype=t)
+    a, b, h = torch.zeros(16, 128, dtype=t), torch.zeros(512, 16, dtype=t), torch.zeros(3, 16)
+    f = B.linear_bwd
+    with pytest.raises(ValueError, match="h is required"):
+        f(q, x, dy, a, b, 2.0)
+    with pytest.raises(ValueError, match="x holds"):
+        f(q, rows(4, 128), dy, a, b, 2.0, h=h)
+    with pytest.raises(ValueError, match="x holds"):
+        f(q, rows(3, 64), dy, a, b, 2.0, h=h)
+    with pytest.raises(TypeError, match="a has dtype"):
+        f(q, x, dy, a.half(), b.half(), 2.0, h=h)
+    with pytest.raises(ValueError, match="h has shape"):
+        f(q, x, dy, a, b, 2.0, h=h[:2])
+    with pytest.raises(ValueError, match="da has shape"):
+        f(q, x, dy, a, b, 2.0, h=h, da=torch.zeros(128, 16))
+    with pytest.raises(ValueError, match="dx has shape"):
+        f(q, x, dy, a, b, 2.0, h=h, dx=torch.zeros(3, 64, dtype=t))
+    with pytest.raises(ValueError, match="a has shape"):
+        B.linear_bwd_grouped(q, [256, 256], x, dy, a, b, 2.0, h=torch.zeros(3, 32))
+    for call in (lambda: f(q, x, dy, a, b, 2.0, h=h), lambda: f(q, x, dy),
+                 lambda: B.linear_bwd_grouped(q, [256, 256], x, dy, torch.zeros(32, 128, dtype=t), b, 2.0, h=torch.zeros(3, 32))):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
