@@ -198,6 +198,9 @@ bool meet(Span a, Span b) {  // an empty buffer meets nothing
   return (a.at > b.at ? a.at : b.at) < (a.end < b.end ? a.end : b.end);
 }
 
+// Of the scales of a weight's groups of 256 blocks.
+int64_t group_bytes(int64_t n, int64_t k) { return (n * k / 64 + 255) / 256 * 4; }
+
 // The outputs meet neither an input nor each other.
 bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
   for (auto o = outputs.begin(); o != outputs.end(); ++o) {
@@ -426,7 +429,8 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
               span(ws, restores ? L.total : static_cast<int64_t>(need))},
              {span(r > 0 ? x8->codes : nullptr, m * x8->ld), span(r > 0 ? x8->scale : nullptr, 4 * m),
               span(dy, 2 * m * n), span(h_saved, 4 * m * r), span(a, 2 * r * k), span(b, 2 * n * rpart),
-              span(w->codes, n * k / 2)}))
+              span(w->codes, n * k / 2), span(w->scale_codes, n * k / 64), span(w->group_scale, group_bytes(n, k)),
+              span(w->absmax, n * k / 16)}))
     return QLORA_ERR_UNSUPPORTED;
 
   char* base = static_cast<char*>(ws);
@@ -692,7 +696,8 @@ static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int6
   if (r == 0) h_out = nullptr;
   const bool restores = L.total > L.w16 && ws != nullptr && ws_bytes >= static_cast<size_t>(L.total);
   if (!apart({span(p, m * n), span(y, 2 * m * n), span(h_out, 4 * m * slots), span(ws, restores ? L.total : need)},
-             {span(x, 2 * m * k), span(a, 2 * slots * k), span(b, 2 * n * r), span(w->codes, n * k / 2)}))
+             {span(x, 2 * m * k), span(a, 2 * slots * k), span(b, 2 * n * r), span(w->codes, n * k / 2),
+              span(w->scale_codes, n * k / 64), span(w->group_scale, group_bytes(n, k)), span(w->absmax, n * k / 16)}))
     return QLORA_ERR_UNSUPPORTED;
 
   char* base = static_cast<char*>(ws);

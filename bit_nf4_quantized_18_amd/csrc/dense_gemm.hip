@@ -116,16 +116,17 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void dense_kernel(DenseArgs g, i
   // Rows past the tile's last lie past its range.
   const int lr = lane >> 3, lc = lane & 7;
   const int k32 = static_cast<int>(g.kb);
-  int xc[LX], wo[LW];  // byte in the row's unit; offset without rows of blocks
+  int xc[LX], wc[LW], wo[LW];  // byte in the row's unit; offset without rows of blocks
 #pragma unroll
   for (int l = 0; l < LX; ++l) xc[l] = 16 * (lc ^ ((lr >> 1) + 4 * ((l * kWaves + wave) & 1)));
 #pragma unroll
-  for (int l = 0; l < LW; ++l)
-    wo[l] = ((kGated ? 8 * (wave >> 1) : 8 * wave) + lr) * k32 + 16 * (lc ^ (2 * (((l * kWaves + wave) >> 1) & 3) + ((lr >> 1) & 1)));
+  for (int l = 0; l < LW; ++l) {
+    wc[l] = 16 * (lc ^ (2 * (((l * kWaves + wave) >> 1) & 3) + ((lr >> 1) & 1)));
+    wo[l] = ((kGated ? 8 * (wave >> 1) : 8 * wave) + lr) * k32 + wc[l];
+  }
   const int xrow = (8 * wave + lr) * k32;
-  // Codes behind the contraction's end (in the second half of its last unit,
-  // and in units past it) become zeros on the tokens' side, so their products
-  // vanish whatever the channels' side holds.
+  // What stands behind the contraction's end (in its last unit, and in units past
+  // it) becomes zeros on both sides: the next row's infinities and NaN stay out.
   auto copy_x = [&](uint8_t* to, int u) {
     const int q = (u0 + u) * kUnit;
 #pragma unroll
@@ -135,11 +136,14 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void dense_kernel(DenseArgs g, i
     }
   };
   auto copy_w = [&](uint8_t* to, int u) {
-    const int q = (u0 + u < units ? u0 + u : units - 1) * kUnit;
+    const int q = (u0 + u) * kUnit;
 #pragma unroll
-    for (int l = 0; l < LW; ++l)
+    for (int l = 0; l < LW; ++l) {
+      // a gated weight's rows are whole units
+      const bool in = kGated ? u0 + u < units : wc[l] < k32 - q;
       copy_1k(kGated && !kEven && (l & 1) ? ur : wr, to + (group * BN / 8 + l * kWaves + wave) * 1024,
-              wo[l] + (8 * (kGated ? l * kWaves >> 1 : l * kWaves) * k32 + q));
+              (in ? wo[l] : kNowhere) + (8 * (kGated ? l * kWaves >> 1 : l * kWaves) * k32 + q));
+    }
   };
   // Fragments of a unit's first or second 64 codes. Token tile t reads rows
   // 16 t + i; channel tile t rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4,

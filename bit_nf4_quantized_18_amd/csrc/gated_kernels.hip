@@ -93,7 +93,7 @@ struct Run {
       for (int e = 0; e < 8; ++e) {
         float slope;
         const float v = act_both<kFine>(a[e], g.act, &slope);
-        a[e] = d[e] * u[e] * slope;
+        a[e] = d[e] * (u[e] * slope);  // |slope| < 1.13: no overflow that the result has not
         u[e] = d[e] * v;
       }
     } else {

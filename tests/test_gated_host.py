@@ -42,7 +42,7 @@ def test_gated_forward_refuses():
         assert call(m=0, x=None, p=None, ws=None) == 0
         assert call(m=0, n=768) == -2
         # outputs over inputs, over each other, over the workspace
-        for a, b in (("p", "x"), ("y", "x"), ("h", "x"), ("ws", "x"), ("p", "a"), ("p", "b"), ("y", "codes"), ("p", "y"),
+        for a, b in (("p", "x"), ("y", "x"), ("h", "x"), ("ws", "x"), ("p", "a"), ("p", "b"), ("y", "codes"), ("p", "y"), ("y", "sc"), ("p", "gs"),
                      ("h", "p"), ("ws", "p"), ("ws", "y"), ("ws", "h")):
             assert call(**{a: AT[b]}) == -4, (a, b)
         assert call(p=AT["y"] + 40 * 1024 - 16) == -4 and call(p=AT["x"] - 40 * 512 + 16) == -4
@@ -130,7 +130,7 @@ def test_backward_from_rows_refuses():
             assert call(k=100) == -2 and call(m=-1) == -2
             assert call(ws=None) == -5 and call(bytes=100) == -5
             for a, b in (("dx", "dy"), ("dx", "x"), ("da", "x"), ("db", "h"), ("da", "xs"), ("ws", "dy"), ("dx", "da"),
-                         ("da", "db"), ("ws", "dx"), ("dx", "codes"), ("db", "b"), ("da", "a")):
+                         ("da", "db"), ("ws", "dx"), ("dx", "codes"), ("da", "sc"), ("dx", "gs"), ("db", "b"), ("da", "a")):
                 assert call(**{a: AT[b]}) == -4, (a, b)
     assert x8_call(r=129) == -4 and x8_call(r=-1) == -2
     assert x8_call(True, r=8) == -4 and x8_call(True, parts=(256, 128)) == -2 and x8_call(True, parts=None) == -1
