@@ -156,7 +156,10 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
     uint32_t code;
     float value;
   } sc[kAhead];
+  // A wave whose slice lies behind the row's end has nothing to copy or multiply.
+  auto live = [&](int pass) { return pass * 64 + 4 * wave < nbk; };
   auto stage = [&](int q, int pass, int slot) {
+    if (!live(pass)) return;
     const int first = group_of(q) * 8;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -180,6 +183,7 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   // the last read zeros.
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, static_cast<int64_t>(a.M) * K * 2);
   auto copy_x = [&](unsigned char* to, int r0, int pass) {
+    if (!live(pass)) return;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int row = 2 * t + (lane >> 5);
@@ -299,19 +303,21 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   f32x4 acc[kGroups];
   // A batch's groups from q0 on in one pass, whose first codes are on their way.
   auto multiply = [&](int q0, int pass) {
+    const int have = live(pass) ? mine - q0 : 0;  // of the batch
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
+      if (q >= have) break;
       const int slot = q % kAhead;
-      constexpr int kMost = kAhead - 1;
       __builtin_amdgcn_sched_barrier(0);
-      if (kGroups - 1 - q >= kMost) wait_vmcnt<kMost * kOps>();
-      else if (kGroups - 1 - q == 1) wait_vmcnt<kOps>();
+      // the first three groups are copied whether they exist or not
+      if (q < kGroups - 2 && (q == 0 || q + 2 < have)) wait_vmcnt<2 * kOps>();
+      else if (q < kGroups - 1 && (q <= 1 || q + 1 < have)) wait_vmcnt<kOps>();
       else wait_vmcnt<0>();
       __builtin_amdgcn_sched_barrier(0);
       const u32x4 c0 = ld16(ring[slot] + codes + 16 * place);
       const u32x4 c1 = ld16(ring[slot] + codes + 16 * (place ^ 1));
       const float s = kDQ ? dq_unit(sc[slot].code, a.w.dq) * sc[slot].value : sc[slot].value;
-      if (q + kAhead < kGroups) {
+      if (q + kAhead < kGroups && q + kAhead < have) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the codes have left the slot
         __builtin_amdgcn_sched_barrier(0);
@@ -334,6 +340,7 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    wait_vmcnt<0>();  // copies of groups that do not exist
   };
   // A batch's sums and outputs.
   auto finish = [&](int q0) {
