@@ -89,7 +89,7 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
 FwdLayout gated_layout(int64_t m, int64_t n, int64_t k, int slots) {
   Carve c;
   FwdLayout L{};
-  if (m <= kGemvMaxM) {
+  if (qlora::gated_decodes(m, n, k)) {
     L.h32 = c.take(m * slots * 4);
     L.w16 = c.off;
     L.total = c.off;
@@ -704,7 +704,7 @@ static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int6
   const float s = r == 0 ? 0.0f : alpha / static_cast<float>(r);
   const int rp = rank_pad(slots);
   const PackedW pw = view(w);
-  if (m <= kGemvMaxM) {
+  if (qlora::gated_decodes(m, n, k)) {
     float* h = h_out != nullptr ? h_out : reinterpret_cast<float*>(base + L.h32);
     if (r > 0) QLORA_TRY(qlora::launch_gated_h(x, m, a, k, slots, h, stream, f16));
     return hip_status(qlora::launch_gated_gemv(pw, x, m, r > 0 ? h : nullptr, b, r, s, act, y, p, stream, f16));

@@ -42,13 +42,35 @@ inline bool dense_fits(int64_t m, int64_t out, int64_t con) {
 //   backward 22016 x 4096       278 / 108     282 / 136     294 / 258    735 / 650
 //   backward 4096 x 11008         72 / 53       74 / 66     141 / 121    409 / 347
 //   backward 8192 x 22016       119 / 222     123 / 253     382 / 462
-inline bool dense_pays(int64_t m, int64_t out, int64_t con) {
-  if (!dense_fits(m, out, con)) return false;
+inline double fused_us(int64_t m, int64_t out, int64_t con) {
   const int64_t tiles = ((m + 255) / 256) * ((out + 127) / 128);
-  const double fused = 6 + static_cast<double>((tiles + 255) / 256) * (6 + 0.9 * static_cast<double>((con + 63) / 64));
+  return 6 + static_cast<double>((tiles + 255) / 256) * (6 + 0.9 * static_cast<double>((con + 63) / 64));
+}
+
+inline double dense_us(int64_t m, int64_t out, int64_t con) {
   const double weights = static_cast<double>(out) * static_cast<double>(con);
   const double product = pick_shape(m, out, 2 * con).us, read = weights * 2 / 3.0e6;
-  return weights * 2.5 / 5.0e6 + (product > read ? product : read) < fused;
+  return weights * 2.5 / 5.0e6 + (product > read ? product : read);
+}
+
+inline bool dense_pays(int64_t m, int64_t out, int64_t con) {
+  return dense_fits(m, out, con) && dense_us(m, out, con) < fused_us(m, out, con);
+}
+
+// Whether a gated block of n weight rows takes its tokens 16 at a time through the
+// decode kernel, which reads the packed weight again for each 16: always up to 16, and
+// up to 32 where two launches cost less than the better product above. Bounded to what
+// the kernel does in one batch of row groups and one pass (n <= 24576 on 256 CUs, k <=
+// 4096); there two launches and H take about 17 us and 0.27 a million weights. 32
+// tokens, two launches / the product, us:
+//   5120 x 1088   19 / 15      11264 x 2048  23 / 31      10240 x 2560  24 / 35
+//   16384 x 4096  33 / 63      22016 x 4096  39 / 63
+// (33 tokens in three: 22016 x 4096  61 / 62), and beyond the bounds 28672 x 4096  72 / 66, 27648 x 5120  99 / 76.
+inline bool gated_decodes(int64_t m, int64_t n, int64_t k) {
+  if (m <= 16) return true;
+  if (m > 32 || n > 24576 || k > 4096) return false;
+  const double fused = fused_us(m, n, k), dense = dense_fits(m, n, k) ? dense_us(m, n, k) : fused;
+  return 17 + 0.27e-6 * static_cast<double>(n) * static_cast<double>(k) < (dense < fused ? dense : fused);
 }
 
 }  // namespace qlora

@@ -1,4 +1,4 @@
-// Decode path of the gated feed-forward block, 1 to 16 tokens: P = act(G) U with
+// Decode path of the gated feed-forward block, 1 to 16 tokens a launch: P = act(G) U with
 // [G | U] = X W16^T + s [H_1 B_1^T | H_2 B_2^T], W read straight from its packed
 // NF4 form in one pass.
 //
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   }
 }
 
-// H = X A^T for 1 to 16 tokens: a workgroup a row of A, whose threads' sums of each
+// H = X A^T: a workgroup a row of A and up to 16 tokens, whose threads' sums of each
 // token meet in LDS (16 wave sums by lane exchanges took 4 us of 7).
 template <bool kF16>
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
@@ -425,6 +425,10 @@ constexpr int kHThreads = 512;
 template <bool kF16, int kTokens>
 __global__ __launch_bounds__(kHThreads) void gated_h_kernel(const uint16_t* x, int M, const uint16_t* a, int64_t K,
                                                             float* h) {
+  // 16 tokens a grid row
+  x += blockIdx.y * 16 * K;
+  M -= blockIdx.y * 16;
+  h += blockIdx.y * 16 * gridDim.x;
   __shared__ float part[kTokens][kHThreads + 1];
   const int tid = threadIdx.x;
   float sum[kTokens];
@@ -460,29 +464,39 @@ hipError_t launch_gated_h(const uint16_t* x, int64_t m, const uint16_t* a, int64
                           hipStream_t st, bool f16) {
   auto kern = m <= 2 ? (f16 ? gated_h_kernel<true, 2> : gated_h_kernel<false, 2>)
                      : (f16 ? gated_h_kernel<true, 16> : gated_h_kernel<false, 16>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(slots)), dim3(kHThreads), 0, st, x, static_cast<int>(m), a, k, h);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(slots), static_cast<unsigned>((m + 15) / 16)), dim3(kHThreads), 0, st,
+                     x, static_cast<int>(m), a, k, h);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_gemv(const PackedW& w, const uint16_t* x, int64_t m, const float* h, const uint16_t* b,
                              int rpart, float s, int act, uint16_t* y, uint16_t* p, hipStream_t st, bool f16) {
-  const Args a{w, x, static_cast<int>(m), h, b, rpart, s, y, p, act, codebook_table(w.codebook)};
+  Args a{w, x, 0, h, b, rpart, s, y, p, act, codebook_table(w.codebook)};
   const int64_t nrg = w.n / 16;
   const unsigned grid = static_cast<unsigned>(nrg < device_cus() ? nrg : device_cus());
   auto launch = [&](auto dq, auto half) {
     constexpr bool D = decltype(dq)::value, H = decltype(half)::value;
-    auto kern = w.k > 4096 ? (m > 8 ? gated_gemv_kernel<D, H, true, true> : gated_gemv_kernel<D, H, true, false>)
-                           : (m > 8 ? gated_gemv_kernel<D, H, false, true> : gated_gemv_kernel<D, H, false, false>);
+    auto kern = w.k > 4096 ? (a.M > 8 ? gated_gemv_kernel<D, H, true, true> : gated_gemv_kernel<D, H, true, false>)
+                           : (a.M > 8 ? gated_gemv_kernel<D, H, false, true> : gated_gemv_kernel<D, H, false, false>);
     hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), 0, st, a);
   };
-  if (f16) {
-    if (w.dq) launch(std::true_type{}, std::true_type{});
-    else launch(std::false_type{}, std::true_type{});
-  } else {
-    if (w.dq) launch(std::true_type{}, std::false_type{});
-    else launch(std::false_type{}, std::false_type{});
+  for (int64_t t = 0; t < m; t += 16) {  // a launch for every 16 tokens
+    a.M = static_cast<int>(m - t < 16 ? m - t : 16);
+    a.x = x + t * w.k;
+    a.h = h != nullptr ? h + t * 2 * rpart : nullptr;
+    a.y = y != nullptr ? y + t * w.n : nullptr;
+    a.p = p + t * (w.n / 2);
+    if (f16) {
+      if (w.dq) launch(std::true_type{}, std::true_type{});
+      else launch(std::false_type{}, std::true_type{});
+    } else {
+      if (w.dq) launch(std::true_type{}, std::false_type{});
+      else launch(std::false_type{}, std::false_type{});
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace qlora

@@ -30,12 +30,19 @@ def test_choices_follow_the_measured_sides(rule):
                 (64, 11008, 4096): 1, (256, 11008, 4096): 1, (1024, 11008, 4096): 1, (4096, 11008, 4096): 1,
                 (64, 22016, 8192): 0, (256, 22016, 8192): 0, (1024, 22016, 8192): 0, (2048, 4096, 22016): 0}
     got = rule(list(measured))
-    assert [g for _, g in got] == list(measured.values())
-    assert all(f for f, _ in got)
+    assert [g for _, g, _ in got] == list(measured.values())
+    assert all(f for f, _, _ in got)
 
 
 def test_bounds(rule):
-    (fits, _), (long_fits, long_pays), most, more = rule([(17, 512, 65536), (17, 512, 65600), ((1 << 28) - 1, 512, 64),
+    (fits, _, _), (long_fits, long_pays, _), most, more = rule([(17, 512, 65536), (17, 512, 65600), ((1 << 28) - 1, 512, 64),
                                                           (1 << 28, 512, 64)])
     assert fits == 1 and long_fits == 0 and long_pays == 0
-    assert most[0] == 1 and more == (0, 0)  # a launch of 2^32 threads
+    assert most[0] == 1 and more[:2] == (0, 0)  # a launch of 2^32 threads
+
+
+def test_tokens_by_sixteen_where_that_was_measured_to_be_faster(rule):
+    cases = {(16, 512, 64): 1, (16, 44032, 8192): 1, (17, 1024, 1024): 0, (32, 5120, 1088): 0, (32, 11264, 2048): 1,
+             (17, 10240, 2560): 1, (32, 16384, 4096): 1, (32, 22016, 4096): 1, (33, 22016, 4096): 0, (32, 28672, 4096): 0,
+             (32, 27648, 5120): 0}
+    assert [d for _, _, d in rule(list(cases))] == list(cases.values())

@@ -111,6 +111,19 @@ def test_many_outputs_of_few_tokens(gpu_lib, m, k):
     C.check(p[:, pick.cuda()], OG.fwd(g, u, OG.SILU), C.fwd_bound(g, u, OG.SILU, T, off[:, :len(pick)], off[:, len(pick):]), "P")
 
 
+# enough weights that 17 to 32 tokens are two decode launches
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,r", [(17, 16), (29, 5), (32, 0)])
+def test_tokens_by_sixteen(gpu_lib, m, r, kind):
+    half, k, t = 5632, 2048, C.TYPES[kind]
+    assert gpu_lib.gated_workspace_bytes(m, 2 * half, k, r) < 2 * half * k
+    w, x, a, b, alpha = L.layer(gpu_lib, m, half, k, r, t, m)
+    L.compare(gpu_lib, w, x, a, b, alpha, OG.SILU, t)
+    p, y, h = gpu_lib.linear_fwd_gated(w, x, a, b, alpha)
+    q = gpu_lib.linear_fwd_gated(w, x[16:].contiguous(), a, b, alpha)
+    assert torch.equal(p[16:], q[0]) and torch.equal(y[16:], q[1]) and (r == 0 or torch.equal(h[16:], q[2]))
+
+
 def test_products_past_32_bit_offsets(gpu_lib):
     # 9.8e9 products, in launches of 2^30 runs of eight
     m, n = 600_000, 16384
