@@ -178,12 +178,21 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
+  // The lane, opaque to the compiler: addresses formed from it are formed anew in
+  // every batch. Formed in front of the loop they are spilled, 50 MB of stores (6 us).
+  auto fresh_lane = [&]() {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+
   // X: the wave's 256 k of 8 tokens, two tokens a copy; lane l moves the piece (16
   // bytes) that belongs at its place: piece p of row r stands at p ^ r. Tokens past
   // the last read zeros.
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, static_cast<int64_t>(a.M) * K * 2);
   auto copy_x = [&](unsigned char* to, int r0, int pass) {
     if (!live(pass)) return;
+    const int lane = fresh_lane();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int row = 2 * t + (lane >> 5);
@@ -193,6 +202,7 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   };
   u32x4 xa[8];
   auto read_x = [&](const unsigned char* from, int r0, int pass) {
+    const int l = fresh_lane(), i = l & 15, g = l >> 4;
     if ((i & 8) != r0) return;
     const bool has = r0 + (i & 7) < a.M && pass * 64 + 4 * wave + g < nbk;
 #pragma unroll
@@ -206,6 +216,7 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   // eight have a lane's slots in one part, and 16-byte loads.
   const bool wide = a.rb % 8 == 0;
   auto load_slots = [&](int q, int j0) {
+    const int l = fresh_lane(), i = l & 15, g = l >> 4, lane_row = (i & 7) + (i >> 3) * half;
     Slots v;
     const int j = j0 + 8 * g, jb = j - (i >> 3) * a.rb;
     const float* hr = a.h + (i < a.M ? i : a.M - 1) * slots;
@@ -228,6 +239,7 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   // s H B^T of the group that this wave sums
   const int own = wave < kGroups ? wave : 0;
   auto adapter = [&](Slots v, int q) {
+    const int l = fresh_lane(), i = l & 15, g = l >> 4;
     f32x4 lo = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < slots; j0 += 32) {
       if (j0 > 0) v = load_slots(q, j0);
@@ -342,20 +354,32 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
     }
     wait_vmcnt<0>();  // copies of groups that do not exist
   };
-  // A batch's sums and outputs.
+  // A batch's sums and outputs; in one pass the next batch's first codes are on their
+  // way before the outputs.
   auto finish = [&](int q0) {
     // acc[q][v]: token 4 g + v, row i of group q
-    __syncthreads();  // the ring has been read
+    meet();  // the ring has been read
+    const int lane = fresh_lane();
     auto sums = [&](int q) { return reinterpret_cast<f32x4*>(ring[q >> 1]) + (q & 1) * (kWaves * 64) + lane; };
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) sums(q)[wave * 64] = acc[q];
-    __syncthreads();
-    if (wave < kGroups && q0 + wave < mine) {  // wave q sums group q
+    meet();
+    const bool owns = wave < kGroups && q0 + wave < mine;  // wave q sums group q
+    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (owns) {
       const f32x4* red = reinterpret_cast<const f32x4*>(wave < 2 ? slot0 : wave < 4 ? slot1 : slot2) +
                          (wave & 1) * (kWaves * 64) + lane;
-      f32x4 sum = red[0];
+      sum = red[0];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) sum += red[w * 64];
+    }
+    if (!kLong && q0 + kGroups < mine) {
+      meet();  // the sums have been read
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) stage(q0 + kGroups + q, 0, q);
+    }
+    if (owns) {
+      const int l = fresh_lane(), i = l & 15, g = l >> 4;
       const int out = group_of(q0 + wave) * 8 + (i & 7);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -388,22 +412,18 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
     for (int q = 0; q < kGroups; ++q) acc[q] = q == wave ? lora : f32x4{0.f, 0.f, 0.f, 0.f};
   };
 
-  begin(lora);
-  multiply(0, 0);
-  for (int pass = 1; pass < passes; ++pass) {
-    restart(0, pass);
-    multiply(0, pass);
-  }
-  finish(0);
-  for (int q0 = kGroups; q0 < mine; q0 += kGroups) {
-    lora = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (a.rb > 0 && wave < kGroups) lora = adapter(load_slots(q0 + own, 0), q0 + own);
+  // one copy of the loop's code, whose fetching from memory would cost as much as a batch
+  for (int q0 = 0;;) {
     begin(lora);
     for (int pass = 0; pass < passes; ++pass) {
-      restart(q0, pass);
+      if (kLong && q0 + pass > 0) restart(q0, pass);
       multiply(q0, pass);
     }
     finish(q0);
+    q0 += kGroups;
+    if (q0 >= mine) return;
+    lora = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.rb > 0 && wave < kGroups) lora = adapter(load_slots(q0 + own, 0), q0 + own);
   }
 }
 
