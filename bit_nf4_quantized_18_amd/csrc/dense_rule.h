@@ -59,18 +59,18 @@ inline bool dense_pays(int64_t m, int64_t out, int64_t con) {
 
 // Whether a gated block of n weight rows takes its tokens 16 at a time through the
 // decode kernel, which reads the packed weight again for each 16: always up to 16, and
-// up to 32 where two launches cost less than the better product above. Bounded to what
-// the kernel does in one batch of row groups and one pass (n <= 24576 on 256 CUs, k <=
-// 4096); there two launches and H take about 17 us and 0.27 a million weights. 32
-// tokens, two launches / the product, us:
+// up to 32 where two launches, about 17 us and 0.3 a million weights with H, cost less
+// than the better product above. 32 tokens, two launches / the product, us:
 //   5120 x 1088   19 / 15      11264 x 2048  23 / 31      10240 x 2560  24 / 35
-//   16384 x 4096  33 / 63      22016 x 4096  39 / 63
-// (33 tokens in three: 22016 x 4096  61 / 62), and beyond the bounds 28672 x 4096  72 / 66, 27648 x 5120  99 / 76.
+//   16384 x 4096  33 / 63      22016 x 4096  39 / 63      28672 x 4096  51 / 66
+//   27648 x 5120  72 / 76      44032 x 8192  138 / 218
+// (2560 x 5120, 31 / 40, is left to the product), and 33 tokens in three: 22016 x 4096
+// 61 / 62, 28672 x 4096  77 / 66.
 inline bool gated_decodes(int64_t m, int64_t n, int64_t k) {
   if (m <= 16) return true;
-  if (m > 32 || n > 24576 || k > 4096) return false;
+  if (m > 32) return false;
   const double fused = fused_us(m, n, k), dense = dense_fits(m, n, k) ? dense_us(m, n, k) : fused;
-  return 17 + 0.27e-6 * static_cast<double>(n) * static_cast<double>(k) < (dense < fused ? dense : fused);
+  return 17 + 0.3e-6 * static_cast<double>(n) * static_cast<double>(k) < (dense < fused ? dense : fused);
 }
 
 }  // namespace qlora
