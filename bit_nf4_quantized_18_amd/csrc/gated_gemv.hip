@@ -21,6 +21,10 @@
 //     depend on scheduling.
 // H comes from a kernel of its own: formed in every workgroup it would read all of
 // A 256 times.
+// One token, 22016 x 4096 (46.5 MB): 16.0 us alone (2.9 TB/s; 10 at a copy's rate), 18.4
+// with H, 13 tokens 17.5 and 22.3; 1024 x 1024 without an adapter 5.9, of which the
+// start, the table and the end are most. 44032 x 8192 in two passes and two batches: 59.5
+// (3.1 TB/s).
 #include <type_traits>
 
 #include "bufmem.h"
