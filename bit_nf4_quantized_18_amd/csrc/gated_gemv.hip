@@ -22,7 +22,7 @@
 // H comes from a kernel of its own: formed in every workgroup it would read all of
 // A 256 times.
 // One token, 22016 x 4096 (46.5 MB): 16.0 us alone (2.9 TB/s; 10 at a copy's rate), 18.4
-// with H, 13 tokens 17.5 and 22.3; 1024 x 1024 without an adapter 5.9, of which the
+// with H, 16 tokens 17.6 and 21.3; 1024 x 1024 without an adapter 5.9, of which the
 // start, the table and the end are most. 44032 x 8192 in two passes and two batches: 59.5
 // (3.1 TB/s).
 #include <type_traits>
@@ -431,8 +431,9 @@ __global__ __launch_bounds__(kThreads) void gated_gemv_kernel(Args a) {
   }
 }
 
-// H = X A^T: a workgroup a row of A and up to 16 tokens, whose threads' sums of each
-// token meet in LDS (16 wave sums by lane exchanges took 4 us of 7).
+// H = X A^T: a workgroup a row of A and up to 4 tokens, whose threads' sums of each
+// token meet in LDS (16 wave sums by lane exchanges took 4 us of 7). 16 tokens, 32 rows of
+// 4096: 3.4 us; 16 tokens a workgroup 4.8.
 template <bool kF16>
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
   if constexpr (kF16) {
@@ -449,10 +450,9 @@ constexpr int kHThreads = 512;
 template <bool kF16, int kTokens>
 __global__ __launch_bounds__(kHThreads) void gated_h_kernel(const uint16_t* x, int M, const uint16_t* a, int64_t K,
                                                             float* h) {
-  // 16 tokens a grid row
-  x += blockIdx.y * 16 * K;
-  M -= blockIdx.y * 16;
-  h += blockIdx.y * 16 * gridDim.x;
+  x += blockIdx.y * kTokens * K;
+  M -= blockIdx.y * kTokens;
+  h += blockIdx.y * kTokens * gridDim.x;
   __shared__ float part[kTokens][kHThreads + 1];
   const int tid = threadIdx.x;
   float sum[kTokens];
@@ -486,10 +486,11 @@ __global__ __launch_bounds__(kHThreads) void gated_h_kernel(const uint16_t* x, i
 
 hipError_t launch_gated_h(const uint16_t* x, int64_t m, const uint16_t* a, int64_t k, int slots, float* h,
                           hipStream_t st, bool f16) {
+  const int tokens = m <= 2 ? 2 : 4;
   auto kern = m <= 2 ? (f16 ? gated_h_kernel<true, 2> : gated_h_kernel<false, 2>)
-                     : (f16 ? gated_h_kernel<true, 16> : gated_h_kernel<false, 16>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(slots), static_cast<unsigned>((m + 15) / 16)), dim3(kHThreads), 0, st,
-                     x, static_cast<int>(m), a, k, h);
+                     : (f16 ? gated_h_kernel<true, 4> : gated_h_kernel<false, 4>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(slots), static_cast<unsigned>((m + tokens - 1) / tokens)),
+                     dim3(kHThreads), 0, st, x, static_cast<int>(m), a, k, h);
   return hipGetLastError();
 }
 
