@@ -373,7 +373,8 @@ hipError_t launch_product(DenseArgs g, bool f16, hipStream_t s) {
 // In launches of their own H took 12 us of a 2048 x 22016 x 4096 call and 8 of 27 us of
 // a 333 x 5120 x 1088 one.
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;    // with the transpose
+constexpr int kRowThreads = 1024;  // of the weight as it is stored
 
 // out32[i][j] = scale sum_q p[i][q] w(j, q), out16 = 16 bits of scale2 out32 with zeros
 // behind the slots. w: slots x q, or (kCols) q x rpart, where slot j is column j mod
@@ -389,70 +390,66 @@ struct Narrow {
   uint16_t* out16;
 };
 
-// 16 tokens by a workgroup: its four waves take units of 64 of the contraction (whole
-// cache lines) in turn, operands straight from memory, and their sums meet in LDS in
-// wave order. kCols: a lane's eight operands are strided, 2-byte loads.
-template <bool kF16, bool kCols>
+// 16 tokens and 16 slots by a workgroup: its kW waves take units of 64 of the
+// contraction (whole cache lines) in turn, operands straight from memory, and their sums
+// meet in LDS in wave order. kCols: a lane's eight operands are strided, 2-byte loads.
+// Bound by the lines that its loads touch, 16 for a kilobyte, at 16 bytes a cycle of its
+// CU: 32 slots by a workgroup took 6.4 us for 1728 of contraction and 22 for 8128, and
+// twice that for 64.
+template <bool kF16, bool kCols, int kW>
 __device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x4* red) {
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, h = lane >> 4, wave = tid >> 6;
-  const int64_t m0 = block * 16;
+  const int tiles = g.rpad / 16;
+  const int64_t m0 = block / tiles * 16;
+  const int slot = static_cast<int>(block % tiles) * 16 + i;
+  if (slot - i >= g.slots) {  // zeros alone
+    for (int o = wave; o < 4; o += kW)
+      if (m0 + 4 * h + o < g.m) g.out16[(m0 + 4 * h + o) * g.rpad + slot] = 0;
+    return;
+  }
   const uint16_t* prow = g.p + (m0 + i < g.m ? m0 + i : g.m - 1) * g.q;
-  for (int s0 = 0; s0 < g.rpad; s0 += 32) {
-    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    for (int64_t u = wave; u < (g.q + 63) / 64; u += 8) {
-      u32x4 pv[4], wv[4][2];
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int64_t u = wave; u < (g.q + 63) / 64; u += 2 * kW) {
+    u32x4 pv[4], wv[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // halves of units u and u + 4
-        const int64_t q = 64 * (u + 4 * (c >> 1)) + 32 * (c & 1) + 8 * h;
-        const bool in = q < g.q;  // q is a multiple of 16 long: a run of 8 is whole or absent
-        const int64_t at = in ? q : 0;
-        pv[c] = ld16(prow + at);
-        if (!in) pv[c] = u32x4{0, 0, 0, 0};
+    for (int c = 0; c < 4; ++c) {  // halves of units u and u + kW
+      const int64_t q = 64 * (u + kW * (c >> 1)) + 32 * (c & 1) + 8 * h;
+      const bool in = q < g.q;  // q is a multiple of 16 long: a run of 8 is whole or absent
+      const int64_t at = in ? q : 0;
+      pv[c] = ld16(prow + at);
+      if (!in) pv[c] = u32x4{0, 0, 0, 0};
+      if constexpr (!kCols) {
+        wv[c] = ld16(g.w + static_cast<int64_t>(slot < g.slots ? slot : 0) * g.q + at);
+      } else {
+        int part = 0;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t > 0 && s0 + 16 >= g.slots) continue;  // uniform: no second tile
-          const int slot = s0 + 16 * t + i;
-          if constexpr (!kCols) {
-            wv[c][t] = ld16(g.w + static_cast<int64_t>(slot < g.slots ? slot : 0) * g.q + at);
-          } else {
-            int part = 0;
+        for (int l = 0; l < 3; ++l) part += (l + 1 < g.parts.g && at >= g.parts.end[l]) ? 1 : 0;
+        const int col = slot - part * g.parts.rpart;
+        const bool own = col >= 0 && col < g.parts.rpart;
+        const uint16_t* w = g.w + at * g.parts.rpart + (own ? col : 0);
+        uint32_t v[8];
 #pragma unroll
-            for (int l = 0; l < 3; ++l) part += (l + 1 < g.parts.g && at >= g.parts.end[l]) ? 1 : 0;
-            const int col = slot - part * g.parts.rpart;
-            const bool own = col >= 0 && col < g.parts.rpart;
-            const uint16_t* w = g.w + at * g.parts.rpart + (own ? col : 0);
-            uint32_t v[8];
+        for (int e = 0; e < 8; ++e) v[e] = w[e * g.parts.rpart];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = w[e * g.parts.rpart];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) wv[c][t][e] = own ? v[2 * e] | v[2 * e + 1] << 16 : 0u;
-          }
-        }
+        for (int e = 0; e < 4; ++e) wv[c][e] = own ? v[2 * e] | v[2 * e + 1] << 16 : 0u;
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (t == 0 || s0 + 16 < g.slots) acc[t] = mma16<kF16>(pv[c], wv[c][t], acc[t]);
     }
-    if (s0 > 0) __syncthreads();  // the last slots' sums have been read
 #pragma unroll
-    for (int t = 0; t < 2; ++t) red[(wave * 2 + t) * 64 + lane] = acc[t];
-    __syncthreads();
-    // acc[t][v]: token 4 h + v, slot s0 + 16 t + i
-    const float* rf = reinterpret_cast<const float*>(red);
+    for (int c = 0; c < 4; ++c) acc = mma16<kF16>(pv[c], wv[c], acc);
+  }
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  // acc[v]: token 4 h + v, slot
+  const float* rf = reinterpret_cast<const float*>(red);
+  for (int v = wave; v < 4; v += kW) {
+    const int64_t m = m0 + 4 * h + v;
+    if (m >= g.m) continue;
+    float sum = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int l2 = tid & 63, v = tid >> 6, slot = s0 + 16 * t + (l2 & 15);
-      const int64_t m = m0 + 4 * (l2 >> 4) + v;
-      if (m >= g.m) continue;
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) sum += rf[((w * 2 + t) * 64 + l2) * 4 + v];
-      sum = slot < g.slots ? g.scale * sum : 0.0f;
-      if (g.out32 != nullptr && slot < g.slots) g.out32[m * g.slots + slot] = sum;
-      g.out16[m * g.rpad + slot] = to16<kF16>(g.scale2 * sum);
-    }
+    for (int w = 0; w < kW; ++w) sum += rf[(w * 64 + lane) * 4 + v];
+    sum = slot < g.slots ? g.scale * sum : 0.0f;
+    if (g.out32 != nullptr && slot < g.slots) g.out32[m * g.slots + slot] = sum;
+    g.out16[m * g.rpad + slot] = to16<kF16>(g.scale2 * sum);
   }
 }
 
@@ -461,11 +458,12 @@ __device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x
 constexpr int kWords = 4;
 
 template <bool kDQ, bool kF16>
-__global__ __launch_bounds__(kThreads) void restore_kernel(PackedW w, uint16_t* out, Levels L, int narrow_blocks,
-                                                           Narrow g) {
-  __shared__ f32x4 red[4 * 2 * 64];
+__global__ __launch_bounds__(kRowThreads) void restore_kernel(PackedW w, uint16_t* out, Levels L, int narrow_blocks,
+                                                              Narrow g) {
+  constexpr int kThreads = kRowThreads;
+  __shared__ f32x4 red[kThreads];
   if (static_cast<int>(blockIdx.x) < narrow_blocks) {
-    narrow_tile<kF16, false>(g, blockIdx.x, red);
+    narrow_tile<kF16, false, kThreads / 64>(g, blockIdx.x, red);
     return;
   }
   const int64_t words = w.n * w.k / 8;  // a multiple of 128
@@ -502,9 +500,9 @@ __global__ __launch_bounds__(kThreads) void restore_t_kernel(PackedW w, uint16_t
                                                              Narrow g, const uint16_t* a, uint16_t* at, uint16_t* bt,
                                                              int tr_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[kTrBlocks * 64 * kTrLd];
-  static_assert(kTrTile <= kTrBlocks * 64 * kTrLd && 4 * 2 * 64 * 16 <= sizeof(tile), "all use the tile");
+  static_assert(kTrTile <= kTrBlocks * 64 * kTrLd && 4 * 64 * 16 <= sizeof(tile), "all use the tile");
   if (static_cast<int>(blockIdx.x) < narrow_blocks) {
-    narrow_tile<kF16, true>(g, blockIdx.x, reinterpret_cast<f32x4*>(tile));
+    narrow_tile<kF16, true, 4>(g, blockIdx.x, reinterpret_cast<f32x4*>(tile));
     return;
   }
   const int64_t id = blockIdx.x - narrow_blocks;
@@ -538,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void restore_t_kernel(PackedW w, uint16_t
   }
 }
 
-int narrow_blocks(const Narrow& g) { return g.rpad > 0 ? static_cast<int>((g.m + 15) / 16) : 0; }
+int narrow_blocks(const Narrow& g) { return static_cast<int>((g.m + 15) / 16) * (g.rpad / 16); }
 
 }  // namespace
 
@@ -554,10 +552,10 @@ hipError_t launch_restore(const PackedW& w, uint16_t* w16, const uint16_t* x, in
                           int rpad, float s, float* h32, uint16_t* hs, hipStream_t st, bool f16) {
   const Narrow g{x, m, w.k, a, slots, rpad, LoraParts{}, 1.0f, s, h32, hs};
   const int first = narrow_blocks(g);
-  const int64_t grid = first + (w.n * w.k / 8 + kWords * kThreads - 1) / (kWords * kThreads);
+  const int64_t grid = first + (w.n * w.k / 8 + kWords * kRowThreads - 1) / (kWords * kRowThreads);
   auto kern = f16 ? (w.dq ? restore_kernel<true, true> : restore_kernel<false, true>)
                   : (w.dq ? restore_kernel<true, false> : restore_kernel<false, false>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, w, w16,
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), 0, st, w, w16,
                      codebook_table(w.codebook), first, g);
   return hipGetLastError();
 }

@@ -20,10 +20,10 @@ constexpr int64_t kDenseNarrow = 2048;
 inline bool dense_narrow(int64_t n, int slots) { return n * ((slots + 31) / 32) <= kDenseNarrow; }
 
 // m tokens, `out` weight rows along the outputs (of the stored weight or of its
-// transpose), `con` elements of contraction. A launch has under 2^32 threads, 256 for
-// every 16 tokens of H or dH.
+// transpose), `con` elements of contraction. A launch has under 2^32 threads, up to
+// 512 a token for H or dH.
 inline bool dense_fits(int64_t m, int64_t out, int64_t con) {
-  return con <= kDenseMaxK && m < (INT64_C(1) << 28) && pick_shape(m, out, 2 * con).shape >= 0;
+  return con <= kDenseMaxK && m < (INT64_C(1) << 22) && pick_shape(m, out, 2 * con).shape >= 0;
 }
 
 // The two sides' microseconds, fitted to 114 measured calls (17 .. 4096 tokens, 0.5 M

@@ -35,8 +35,8 @@ def test_choices_follow_the_measured_sides(rule):
 
 
 def test_bounds(rule):
-    (fits, _, _), (long_fits, long_pays, _), most, more = rule([(17, 512, 65536), (17, 512, 65600), ((1 << 28) - 1, 512, 64),
-                                                          (1 << 28, 512, 64)])
+    (fits, _, _), (long_fits, long_pays, _), most, more = rule([(17, 512, 65536), (17, 512, 65600), ((1 << 22) - 1, 512, 64),
+                                                          (1 << 22, 512, 64)])
     assert fits == 1 and long_fits == 0 and long_pays == 0
     assert most[0] == 1 and more[:2] == (0, 0)  # a launch of 2^32 threads
 
