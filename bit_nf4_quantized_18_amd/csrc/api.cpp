@@ -477,7 +477,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     // masked dX update need; the frozen-weight GEMM then runs without
     // adapter slots.
     if (drop != nullptr) dhs = nullptr;
-    if (!restores || !qlora::dense_narrow(n, r))
+    if (!restores || !qlora::dense_narrow(n))
       QLORA_TRY(qlora::launch_skinny_prefill(dy, bt, m, n, r, rp, drop != nullptr ? s * inv_keep : s, 1.0f, spart, dh32,
                                              dhs, stream, f16));
     if (x8 != nullptr) {

@@ -567,7 +567,7 @@ hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy
   one.rpart = slots;
   one.end[0] = static_cast<int>(w.n);
   const Narrow g{dy, m, w.n, b, slots, rpad, parts != nullptr ? *parts : one, s, 1.0f, dh32, dhs};
-  const bool narrow = dense_narrow(w.n, slots);
+  const bool narrow = dense_narrow(w.n);
   const int first = narrow ? narrow_blocks(g) : 0;
   const int tr_blocks = rpad == 0                     ? 0
                         : !narrow                     ? static_cast<int>(lora_transpose_tiles(w.n, w.k))

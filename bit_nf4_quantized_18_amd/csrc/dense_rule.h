@@ -10,14 +10,15 @@ namespace qlora {
 // Longest contraction of the dense kernels: 32-bit offsets in a tile of 256 rows.
 constexpr int64_t kDenseMaxK = 65536;
 
-// Whether dH = s dY B over n weight rows and `slots` adapter slots is formed beside the
-// restoring, 16 tokens a workgroup whose lanes read B in strided loads, 32 slots at a
-// time, or behind it from B^T. Whole calls, us, beside / behind, 17 and 2048 tokens:
-//   1040 x 1088, 16 slots  18.2 / 23.3, 34.5 / 39.2; 64 slots 27.3 / 28.6, 50.6 / 54.6
-//   2048 x 2048, 16 slots  22.4 / 24.1, 45.4 / 48.4; 64 slots 34.3 / 29.3, 65.3 / 65.1
-//   4096 x 4096, 16 slots  43.4 / 39.5, 95.5 / 97.6; 64 slots 65.5 / 43.6, 135.8 / 116.3
-constexpr int64_t kDenseNarrow = 2048;
-inline bool dense_narrow(int64_t n, int slots) { return n * ((slots + 31) / 32) <= kDenseNarrow; }
+// Whether dH = s dY B over n weight rows is formed beside the restoring, 16 tokens and
+// 16 slots a workgroup whose lanes read B in strided loads, or behind it from B^T. Whole
+// calls, us, beside / behind, 17 and 2048 tokens:
+//   1040 x 1088, 16 slots  16.5 / 23.3, 31 / 39; 64 slots 19.0 / 27.3, 43 / 55
+//   2048 x 2048, 16 slots  21.0 / 24.1, 43 / 48; 64 slots 23.0 / 29.2, 57 / 68
+//   4096 x 4096, 16 slots  41.4 / 39.5, 94 / 96; 64 slots 44.9 / 44.1, 118 / 121
+//   6656 x 4544, 16 slots  57.2 / 47.3, 167 / 161; 64 slots 61.0 / 50.8, 204 / 195
+constexpr int64_t kDenseNarrow = 4096;
+inline bool dense_narrow(int64_t n) { return n <= kDenseNarrow; }
 
 // m tokens, `out` weight rows along the outputs (of the stored weight or of its
 // transpose), `con` elements of contraction. A launch has under 2^32 threads, up to

@@ -162,7 +162,7 @@ hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const 
                               const uint16_t* hs, const uint16_t* b, int rpart, int rpad, int act, uint16_t* y,
                               uint16_t* p, hipStream_t st, bool f16);
 // launch_restore_t: wt16 (k x n) unless it is null, and with slots > 0 A^T (at, k x
-// rpad, with wt16) and, where dense_narrow(w.n, slots), dH = s dY B (dh32, and dhs in 16 bits,
+// rpad, with wt16) and, where dense_narrow(w.n), dH = s dY B (dh32, and dhs in 16 bits,
 // zero-padded to rpad); otherwise B^T (bt, rpad x n), for launch_skinny_prefill.
 hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy, int64_t m, const uint16_t* a,
                             const uint16_t* b, int slots, int rpad, const LoraParts* parts, float s, float* dh32,
