@@ -83,9 +83,9 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
   return L;
 }
 
-// The gated forward: H (decode), or H, s H and the partial sums of H; last, from
-// w16 on, the restored weight where restoring it once pays (dense_rule.h). A
-// workspace that ends in front of it is taken as well.
+// The gated forward: H (decode), or s H in three 16-bit terms and the partial sums of
+// H; last, from w16 on, the restored weight where restoring it once pays
+// (dense_rule.h). A workspace that ends in front of it is taken as well.
 FwdLayout gated_layout(int64_t m, int64_t n, int64_t k, int slots) {
   Carve c;
   FwdLayout L{};
@@ -95,21 +95,27 @@ FwdLayout gated_layout(int64_t m, int64_t n, int64_t k, int slots) {
     L.total = c.off;
     return L;
   }
-  L = fwd_layout(m, n, k, slots, true);
-  c.off = L.total;
+  L.hs = c.take(m * 3 * rank_pad(slots) * 2);
+  L.part = c.take(static_cast<int64_t>(qlora::skinny_prefill_splits(m, k, slots)) * m * slots * 4);
   L.w16 = c.take(qlora::dense_pays(m, n, k) ? n * k * 2 : 0);
   L.total = c.off;
   return L;
 }
 
-// The backward from 8-bit rows: the plain one's buffers but for the partial sums
-// of dA and dB, which go last, in front of the restored weight (w16, as above).
+// The backward from 8-bit rows: dH, also in three 16-bit terms, the adapter's
+// transposes, the partial sums of dH and of dA and dB; last the restored weight (w16,
+// as above).
 BwdLayout x8_layout(int64_t m, int64_t n, int64_t k, int r, int rpart) {
-  BwdLayout L = bwd_layout(m, n, k, r, rpart);
   Carve c;
-  c.off = L.part;
+  BwdLayout L{};
+  const int rp = rank_pad(r);
+  L.dh32 = c.take(m * r * 4);
+  L.dhs = c.take(m * 3 * rp * 2);
+  L.at = c.take(k * rp * 2);
+  L.bt = c.take(n * rp * 2);
+  L.spart = c.take(static_cast<int64_t>(qlora::skinny_prefill_splits(m, n, r)) * m * r * 4);
   const int splits = r == 0 ? 1 : qlora::rank_grad8_splits(m, n, k, r, rpart);
-  c.take(splits == 1 ? 0 : splits * (r * k + rpart * n) * 4);
+  L.part = c.take(splits == 1 ? 0 : splits * (r * k + rpart * n) * 4);
   L.w16 = c.take(qlora::dense_pays(m, k, n) ? n * k * 2 : 0);
   L.total = c.off;
   return L;
@@ -479,7 +485,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
     if (drop != nullptr) dhs = nullptr;
     if (!restores || !qlora::dense_narrow(n))
       QLORA_TRY(qlora::launch_skinny_prefill(dy, bt, m, n, r, rp, drop != nullptr ? s * inv_keep : s, 1.0f, spart, dh32,
-                                             dhs, stream, f16));
+                                             dhs, stream, f16, x8 != nullptr));
     if (x8 != nullptr) {
       QLORA_TRY(qlora::launch_rank_grads8(dh32, x8->codes, x8->ld, x8->scale, k, h, dy, n, m, r, grp, s, part, da, db,
                                           stream, f16));
@@ -504,6 +510,8 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
                                               r, stream, f16));
     } else if (restores) {
       QLORA_TRY(qlora::launch_dense_dx(wt16, n, k, dy, m, dhs, at, rp, dx, stream, f16));
+    } else if (x8 != nullptr) {
+      QLORA_TRY(qlora::launch_gemm_dx_terms(pw, dy, m, dhs, at, rp, dx, stream, f16));
     } else {
       QLORA_TRY(qlora::launch_gemm_dx(pw, dy, m, dhs, at, rp, dx, stream, f16));
     }
@@ -717,7 +725,7 @@ static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int6
   }
   if (r > 0)
     QLORA_TRY(qlora::launch_skinny_prefill(x, a, m, k, slots, rp, 1.0f, s, reinterpret_cast<float*>(base + L.part),
-                                           h_out, hs, stream, f16));
+                                           h_out, hs, stream, f16, true));
   return hip_status(qlora::launch_gemm_gated(pw, x, m, hs, b, r, rp, act, y, p, stream, f16));
 }
 

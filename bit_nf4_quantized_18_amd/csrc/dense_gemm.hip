@@ -29,7 +29,7 @@ struct DenseArgs {
   const uint8_t* x;  // m rows of kb bytes
   int64_t m, n, kb;
   int64_t up;         // gated: weight rows from an output's gate row to its up row
-  const uint16_t* ha;  // m x rpad adapter slots
+  const uint16_t* ha;  // m x 3 rpad: the adapter's slots as terms (put_terms, mfma.h)
   const uint16_t* hb;  // their rows of a channel: hb_lim slots at hb_ld, up's after `shift` others
   int64_t hb_ld;
   int hb_lim, rpad, shift;
@@ -255,29 +255,46 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void dense_kernel(DenseArgs g, i
     }
   }
 
-  // The adapter's slots as more contraction, operands straight from memory.
-  // Fragment rows as in the ring; tokens past the last are not stored, channels
-  // past it are zeros.
+  // The adapter's slots as more contraction, in terms that hold all bits of the float32
+  // H or dH, operands straight from memory. Fragment rows as in the ring; tokens past the
+  // last are not stored, channels past it are zeros.
   for (int ks = 0; ks < g.rpad / 32; ++ks) {
-    u32x4 xa[TM], wb[TN];
+    // two terms in registers at a time, a part of one beside a widened fp16 B: more spill in the largest tiles
+    constexpr int kFirst = kF16 && TM == 8 ? 4 : TM;
+    u32x4 xa[TM], xc[TM];
+    auto load = [&](u32x4(&to)[TM], int q, int first, int last) {
 #pragma unroll
-    for (int a = 0; a < TM; ++a) {
-      const int64_t m = m0 + wm * TM * 16 + 16 * a + i;
-      xa[a] = ld16(g.ha + (m < g.m ? m : g.m - 1) * g.rpad + 32 * ks + 8 * h);
-    }
+      for (int a = first; a < last; ++a) {
+        const int64_t m = m0 + wm * TM * 16 + 16 * a + i;
+        to[a] = ld16(g.ha + (m < g.m ? m : g.m - 1) * (3 * g.rpad) + q * g.rpad + 32 * ks + 8 * h);
+      }
+    };
+    load(xa, 0, 0, TM);
+    Wide<kF16> wb[TN];
 #pragma unroll
     for (int b = 0; b < TN; ++b) {
       const int row = wn * TN * 16 + 64 * (b >> 2) + 16 * (i >> 2) + 4 * (b & 3) + (i & 3);
       const bool up = kGated && (row & 8) != 0;
       const int64_t n = n0 + (kGated ? 8 * (row >> 4) + (row & 7) : row);
-      wb[b] = n < g.n ? ld8_bf16_window(g.hb + (n + (up ? g.up : 0)) * g.hb_ld, 32 * ks + 8 * h - (up ? g.shift : 0),
-                                        g.hb_lim, (g.hb_ld % 8) == 0)
-                      : u32x4{0, 0, 0, 0};
+      wb[b].t[0] = n < g.n ? ld8_bf16_window(g.hb + (n + (up ? g.up : 0)) * g.hb_ld, 32 * ks + 8 * h - (up ? g.shift : 0),
+                                             g.hb_lim, (g.hb_ld % 8) == 0)
+                           : u32x4{0, 0, 0, 0};
     }
+    load(xc, 1, 0, kFirst);
 #pragma unroll
-    for (int a = 0; a < TM; ++a)
+    for (int b = 0; b < TN; ++b) wb[b] = widen<kF16>(wb[b].t[0]);
+    auto multiply = [&](const u32x4(&x)[TM], int q) {
 #pragma unroll
-      for (int b = 0; b < TN; ++b) acc[a][b] = mma16<kF16>(wb[b], xa[a], acc[a][b]);
+      for (int b = 0; b < TN; ++b)
+#pragma unroll
+        for (int a = 0; a < TM; ++a) acc[a][b] = mma_term<kF16>(wb[b], x[a], q, acc[a][b]);
+    };
+    multiply(xa, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load(xc, 1, kFirst, TM);
+    load(xa, 2, 0, TM);
+    multiply(xc, 1);
+    multiply(xa, 2);
   }
 
   // Lane: tokens 16 a + i, channels 64 (b / 4) + 16 h + 4 (b % 4) + v: runs of 16
@@ -376,8 +393,8 @@ hipError_t launch_product(DenseArgs g, bool f16, hipStream_t s) {
 constexpr int kThreads = 256;    // with the transpose
 constexpr int kRowThreads = 1024;  // of the weight as it is stored
 
-// out32[i][j] = scale sum_q p[i][q] w(j, q), out16 = 16 bits of scale2 out32 with zeros
-// behind the slots. w: slots x q, or (kCols) q x rpart, where slot j is column j mod
+// out32[i][j] = scale sum_q p[i][q] w(j, q), terms (m x 3 rpad) = scale2 out32 as terms
+// with zeros behind the slots. w: slots x q, or (kCols) q x rpart, where slot j is column j mod
 // rpart of part j / rpart's rows and zero in the others'.
 struct Narrow {
   const uint16_t* p;
@@ -387,7 +404,7 @@ struct Narrow {
   LoraParts parts;
   float scale, scale2;
   float* out32;
-  uint16_t* out16;
+  uint16_t* terms;
 };
 
 // 16 tokens and 16 slots by a workgroup: its kW waves take units of 64 of the
@@ -404,7 +421,7 @@ __device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x
   const int slot = static_cast<int>(block % tiles) * 16 + i;
   if (slot - i >= g.slots) {  // zeros alone
     for (int o = wave; o < 4; o += kW)
-      if (m0 + 4 * h + o < g.m) g.out16[(m0 + 4 * h + o) * g.rpad + slot] = 0;
+      if (m0 + 4 * h + o < g.m) put_terms(g.terms + (m0 + 4 * h + o) * (3 * g.rpad), g.rpad, slot, 0.0f);
     return;
   }
   const uint16_t* prow = g.p + (m0 + i < g.m ? m0 + i : g.m - 1) * g.q;
@@ -449,7 +466,7 @@ __device__ __forceinline__ void narrow_tile(const Narrow& g, int64_t block, f32x
     for (int w = 0; w < kW; ++w) sum += rf[(w * 64 + lane) * 4 + v];
     sum = slot < g.slots ? g.scale * sum : 0.0f;
     if (g.out32 != nullptr && slot < g.slots) g.out32[m * g.slots + slot] = sum;
-    g.out16[m * g.rpad + slot] = to16<kF16>(g.scale2 * sum);
+    put_terms(g.terms + m * (3 * g.rpad), g.rpad, slot, g.scale2 * sum);
   }
 }
 

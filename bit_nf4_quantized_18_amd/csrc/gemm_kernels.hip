@@ -117,7 +117,8 @@ __device__ __forceinline__ int64_t gated_row(int64_t p0, int row, int64_t half) 
   return p0 / 2 + 32 * (row >> 6) + (row & 31) + ((row & 32) != 0 ? half : 0);
 }
 
-template <bool kTransW, bool kDQ, bool kF16, bool kGated = false>
+// kTerms: ep_a holds the adapter's slots as terms of their float32 (put_terms, mfma.h).
+template <bool kTransW, bool kDQ, bool kF16, bool kGated = false, bool kTerms = kGated>
 __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t* __restrict__ A, int64_t M,
                                                        int64_t P, int64_t Qn, const uint16_t* __restrict__ ep_a,
                                                        const uint16_t* __restrict__ ep_b, int64_t ep_ld, int ep_lim,
@@ -404,13 +405,17 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t
     for (int l = 0; l < 3; ++l) part += (l + 1 < lp.g && p0 >= lp.end[l]) ? 1 : 0;
     slot_shift = part * lp.rpart;
   }
+  constexpr int kOf = kTerms ? 3 : 1;
   for (int ks = 0; ks < rpad / 32; ++ks) {
     u32x4 xa[8], xb[4];
+    auto load = [&](u32x4(&to)[8], int q, int first = 0, int last = 8) {
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const int64_t m = m0 + wm * 128 + 16 * mt + i;
-      xa[mt] = ld16(ep_a + (m < M ? m : M - 1) * rpad + 32 * ks + 8 * g);  // rows past M are never stored
-    }
+      for (int mt = first; mt < last; ++mt) {
+        const int64_t m = m0 + wm * 128 + 16 * mt + i;  // rows past M are never stored
+        to[mt] = ld16(ep_a + (m < M ? m : M - 1) * (kOf * rpad) + q * rpad + 32 * ks + 8 * g);
+      }
+    };
+    load(xa, 0);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       const int64_t p = kGated ? gated_row(p0, wp * 64 + 16 * nt + i, P / 2) : p0 + wp * 64 + 16 * nt + i;
@@ -418,7 +423,28 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(PackedW w, const uint16_t
       xb[nt] = (p < P) ? ld8_bf16_window(ep_b + p * ep_ld, 32 * ks + 8 * g - shift, ep_lim, (ep_ld % 8) == 0)
                        : u32x4{0, 0, 0, 0};
     }
-    mma(xa, xb);
+    if constexpr (kTerms) {
+      // two terms in registers at a time, a part of one beside a widened fp16 B: more spill
+      u32x4 xc[8];
+      load(xc, 1, 0, kF16 ? 4 : 8);
+      Wide<kF16> w16[4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) w16[nt] = widen<kF16>(xb[nt]);
+      auto multiply = [&](const u32x4(&x)[8], int q) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) acc[nt][mt] = mma_term<kF16>(w16[nt], x[mt], q, acc[nt][mt]);
+      };
+      multiply(xa, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kF16) load(xc, 1, 4);
+      load(xa, 2);
+      multiply(xc, 1);
+      multiply(xa, 2);
+    } else {
+      mma(xa, xb);
+    }
   }
 
   // Output through LDS: the ring is free after the last step's barrier (no
@@ -509,6 +535,15 @@ hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, con
   lp.rpart = rpart;
   hipLaunchKernelGGL(kern, dim3(tiles(m, w.n)), dim3(512), 0, st, w, x, m, w.n, w.k, hs, b,
                      static_cast<int64_t>(rpart), rpart, rpad, lp, y, codebook_table(w.codebook), GateOut{p, act});
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_dx_terms(const PackedW& w, const uint16_t* dy, int64_t m, const uint16_t* dhs,
+                                const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16) {
+  auto kern = f16 ? (w.dq ? nf4_gemm_kernel<true, true, true, false, true> : nf4_gemm_kernel<true, false, true, false, true>)
+                  : (w.dq ? nf4_gemm_kernel<true, true, false, false, true> : nf4_gemm_kernel<true, false, false, false, true>);
+  hipLaunchKernelGGL(kern, dim3(tiles(m, w.k)), dim3(512), 0, st, w, dy, m, w.k, w.n, dhs, at,
+                     static_cast<int64_t>(rpad), rpad, rpad, LoraParts{}, dx, codebook_table(w.codebook), GateOut{});
   return hipGetLastError();
 }
 

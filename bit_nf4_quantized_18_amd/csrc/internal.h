@@ -82,12 +82,13 @@ hipError_t launch_skinny_decode(const uint16_t* P, const uint16_t* Q, int64_t m,
 // Prefill (m > 16) form of the same projection, split over the contraction
 // for parallelism: raw partials in part (skinny_prefill_splits(m, qn, r) x m x r
 // float32), then out_f32 (m x r, may be null) = scale * sum and out_bf16
-// (m x rpad, may be null) = bf16(scale2 * scale * sum), zero-padded. For
+// (m x rpad, may be null) = bf16(scale2 * scale * sum), zero-padded; with `terms`
+// (m x 3 rpad) those float32 values as three bf16 terms (put_terms, mfma.h). For
 // r <= 16 the partials come from a streaming kernel (LDS ring, MFMA).
 int skinny_prefill_splits(int64_t m, int64_t qn, int r);
 hipError_t launch_skinny_prefill(const uint16_t* P, const uint16_t* Q, int64_t m, int64_t qn, int r, int rpad,
                                  float scale, float scale2, float* part, float* out_f32, uint16_t* out_bf16,
-                                 hipStream_t st, bool f16 = false);
+                                 hipStream_t st, bool f16 = false, bool terms = false);
 
 // A weight made of g row blocks (grouped linears sharing their input): part
 // l covers output rows end[l-1] .. end[l]-1 (end[-1] = 0) and owns adapter
@@ -142,7 +143,7 @@ hipError_t launch_gemm_fwd(const PackedW& w, const uint16_t* x, int64_t m, const
 
 // The same for a gated block (w: gate's rows above up's, each a multiple of 64):
 // p = act(gate) up from the float32 sums, and y, the pre-activations, unless it
-// is null.
+// is null. hs: s H of both parts as terms, m x 3 rpad.
 hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, const uint16_t* hs, const uint16_t* b,
                              int rpart, int rpad, int act, uint16_t* y, uint16_t* p, hipStream_t st, bool f16);
 
@@ -150,20 +151,23 @@ hipError_t launch_gemm_gated(const PackedW& w, const uint16_t* x, int64_t m, con
 // m x rpad and at is bf16 k x rpad (A transposed, zero padded).
 hipError_t launch_gemm_dx(const PackedW& w, const uint16_t* dy, int64_t m, const uint16_t* dhs,
                           const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16 = false);
+// The same with dH as terms, m x 3 rpad.
+hipError_t launch_gemm_dx_terms(const PackedW& w, const uint16_t* dy, int64_t m, const uint16_t* dhs,
+                                const uint16_t* at, int rpad, uint16_t* dx, hipStream_t st, bool f16);
 
 // The product over a weight restored to 16 bits in the workspace (dense_gemm.hip),
 // for sizes that dense_fits (dense_rule.h); other arguments as launch_gemm_gated and
-// launch_gemm_dx.
+// launch_gemm_dx_terms.
 // launch_restore: w16 (n x k), and with slots > 0 H = X A^T (h32, m x slots, may be
-// null) and hs (m x rpad, 16 bits of s H, zero-padded).
+// null) and hs (m x 3 rpad, s H as terms, zero-padded).
 hipError_t launch_restore(const PackedW& w, uint16_t* w16, const uint16_t* x, int64_t m, const uint16_t* a, int slots,
                           int rpad, float s, float* h32, uint16_t* hs, hipStream_t st, bool f16);
 hipError_t launch_dense_gated(const uint16_t* w16, int64_t n2, int64_t k, const uint16_t* x, int64_t m,
                               const uint16_t* hs, const uint16_t* b, int rpart, int rpad, int act, uint16_t* y,
                               uint16_t* p, hipStream_t st, bool f16);
 // launch_restore_t: wt16 (k x n) unless it is null, and with slots > 0 A^T (at, k x
-// rpad, with wt16) and, where dense_narrow(w.n), dH = s dY B (dh32, and dhs in 16 bits,
-// zero-padded to rpad); otherwise B^T (bt, rpad x n), for launch_skinny_prefill.
+// rpad, with wt16) and, where dense_narrow(w.n), dH = s dY B (dh32, and dhs as terms,
+// m x 3 rpad, zero-padded); otherwise B^T (bt, rpad x n), for launch_skinny_prefill.
 hipError_t launch_restore_t(const PackedW& w, uint16_t* wt16, const uint16_t* dy, int64_t m, const uint16_t* a,
                             const uint16_t* b, int slots, int rpad, const LoraParts* parts, float s, float* dh32,
                             uint16_t* dhs, uint16_t* at, uint16_t* bt, hipStream_t st, bool f16);

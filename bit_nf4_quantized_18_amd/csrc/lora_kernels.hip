@@ -223,8 +223,8 @@ __device__ __forceinline__ float sum_splits(const float* __restrict__ p, int64_t
 
 // Second half of the split prefill projection: out_f32 = scale * sum of the
 // split partials (summed in split order), out_bf16 = bf16(scale2 * that),
-// zero-padded from r to rpad columns.
-template <bool kF16>
+// zero-padded from r to rpad columns. kTerms: that in three bf16 terms.
+template <bool kF16, bool kTerms = false>
 __global__ void skinny_final_kernel(const float* __restrict__ part, int64_t M, int r, int rpad, int splits,
                                     float scale, float scale2, float* __restrict__ out_f32,
                                     uint16_t* __restrict__ out_bf16) {
@@ -235,7 +235,9 @@ __global__ void skinny_final_kernel(const float* __restrict__ part, int64_t M, i
   const float sum = j < r ? sum_splits(part + mo * r + j, M * r, splits) : 0.0f;
   const float val = scale * sum;
   if (out_f32 != nullptr && j < r) out_f32[mo * r + j] = val;
-  if (out_bf16 != nullptr) out_bf16[idx] = to16<kF16>(scale2 * val);
+  if (out_bf16 == nullptr) return;
+  if (kTerms) put_terms(out_bf16 + mo * 3 * rpad, rpad, j, scale2 * val);
+  else out_bf16[idx] = to16<kF16>(scale2 * val);
 }
 
 __global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ a,
@@ -677,7 +679,7 @@ int skinny_prefill_splits(int64_t m, int64_t qn, int r) {
 
 hipError_t launch_skinny_prefill(const uint16_t* P, const uint16_t* Q, int64_t m, int64_t qn, int r, int rpad,
                                  float scale, float scale2, float* part, float* out_f32, uint16_t* out_bf16,
-                                 hipStream_t st, bool f16) {
+                                 hipStream_t st, bool f16, bool terms) {
   const int splits = skinny_prefill_splits(m, qn, r);
   if (proj_fast(r)) {
     // columns per split: a multiple of the 128-column chunk
@@ -694,7 +696,10 @@ hipError_t launch_skinny_prefill(const uint16_t* P, const uint16_t* Q, int64_t m
   }
   const int64_t total = m * rpad;
   const dim3 fgrid(static_cast<unsigned>((total + 255) / 256));
-  if (f16) {
+  if (terms) {
+    hipLaunchKernelGGL((skinny_final_kernel<false, true>), fgrid, dim3(256), 0, st, part, m, r, rpad, splits, scale,
+                       scale2, out_f32, out_bf16);
+  } else if (f16) {
     hipLaunchKernelGGL(skinny_final_kernel<true>, fgrid, dim3(256), 0, st, part, m, r, rpad, splits, scale, scale2,
                        out_f32, out_bf16);
   } else {

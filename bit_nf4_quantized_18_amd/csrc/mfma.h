@@ -88,4 +88,53 @@ __device__ __forceinline__ uint16_t to16(float f) {
   return f32_to_bf16_rne(f);
 }
 
+// A float32 as three bf16 terms, which hold all of its 24 bits, in rows of 3 rpad: term t
+// of slot j at t rpad + j. Products of bf16 terms on the matrix cores are exact, so a sum
+// over the terms is one over unrounded float32 values. The first is cut off (a value
+// next to float32's end must not round to infinity), the others are rounded, the last
+// without a rest. Infinities become NaN.
+__device__ __forceinline__ void put_terms(uint16_t* row, int rpad, int j, float v) {
+  const uint32_t t0 = __float_as_uint(v) >> 16;
+  v -= __uint_as_float(t0 << 16);
+  const uint16_t t1 = f32_to_bf16_rne(v);
+  row[j] = static_cast<uint16_t>(t0);
+  row[rpad + j] = t1;
+  row[2 * rpad + j] = f32_to_bf16_rne(v - __uint_as_float(static_cast<uint32_t>(t1) << 16));
+}
+
+// Eight 16-bit elements as bf16 terms, whose sum they are: bf16 ones as they are, fp16
+// ones as their rounding and the rest, at most 2^-9 of it.
+template <bool kF16>
+struct Wide {
+  u32x4 t[kF16 ? 2 : 1];
+};
+template <bool kF16>
+__device__ __forceinline__ Wide<kF16> widen(u32x4 v) {
+  Wide<kF16> r;
+  r.t[0] = v;
+  if constexpr (kF16) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float f0 = lo16<true>(v[e]), f1 = hi16<true>(v[e]);
+      const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{f0, f1}, bf16x2));
+      r.t[0][e] = hi;
+      r.t[1][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                                                   f32x2{f0 - lo16<false>(hi), f1 - hi16<false>(hi)}, bf16x2));
+    }
+  }
+  return r;
+}
+
+// acc += term q (of put_terms) times the elements. The rest of an fp16 element with the
+// last term, below 2^-25 of the product, is left out.
+template <bool kF16>
+__device__ __forceinline__ f32x4 mma_term(const Wide<kF16>& w, u32x4 term, int q, f32x4 acc) {
+  acc = mma16<false>(w.t[0], term, acc);
+  if constexpr (kF16)
+    if (q < 2) acc = mma16<false>(w.t[1], term, acc);
+  return acc;
+}
+
 }  // namespace qlora

@@ -379,7 +379,8 @@ size_t qlora_linear_grouped_workspace_bytes(int64_t m, int64_t n, int64_t k, int
  *   y     : m x (2 np) output of [G | U] rounded to 16 bits, for the backward;
  *           NULL where it is not wanted.
  *   p     : m x np output, formed from the float32 sums of G and U and rounded
- *           once.
+ *           once. H enters these sums as float32 at every m (the linear calls
+ *           round s H to 16 bits above 16 tokens).
  *   h_out : float32 m x (2 r), [H_1 | H_2]; may be NULL.
  *   ws    : qlora_linear_gated_workspace_bytes(m, w->n, k, r) bytes. Their last
  *           2 w->n k are, where the size counts them, for the weight restored to
@@ -433,7 +434,8 @@ qlora_status qlora_gated_bwd_x8(const int8_t* codes, int64_t ld, const float* sc
  * X[i][q] = x[i][q] x_scale[i]:
  *   dA = dH^T X, dB = s dY^T H, dX = dY W16 + dH A
  * as in qlora_linear_bwd (qlora_linear_bwd_grouped), the products of dA and dB
- * in float32 sums of unrounded products.
+ * in float32 sums of unrounded products, and dH in float32 in dX (the calls with a
+ * 16-bit input round it to 16 bits there).
  *   x, ldx, x_scale : m rows of k codes, ldx the row length (ldx % 64 == 0, k ..
  *                     QLORA_INT8_MAX_COLS), and their scales. A row whose scale
  *                     is NaN makes dA NaN.
