@@ -137,6 +137,10 @@ bool linear_sizes_ok(int64_t m, int64_t n, int64_t k) {
   return m > 0 && n > 0 && k > 0 && m <= (INT64_C(1) << 31) && n <= (INT64_C(1) << 22) && k <= (INT64_C(1) << 22);
 }
 
+// The slots of g parts of rank r (g in 1 .. QLORA_MAX_PARTS), g r, are at most
+// QLORA_MAX_RANK; the product itself may leave an int.
+bool rank_fits(int g, int r) { return r <= QLORA_MAX_RANK / g; }
+
 // A linear's input kept as 8-bit rows.
 struct Rows8 {
   const int8_t* codes;
@@ -261,7 +265,7 @@ size_t qlora_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int r) {
 }
 
 size_t qlora_linear_grouped_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r) {
-  if (!linear_sizes_ok(m, n, k) || g < 1 || g > QLORA_MAX_PARTS || r < 1 || g * r > QLORA_MAX_RANK) return 0;
+  if (!linear_sizes_ok(m, n, k) || g < 1 || g > QLORA_MAX_PARTS || r < 1 || !rank_fits(g, r)) return 0;
   const int64_t f = fwd_layout(m, n, k, g * r).total;
   const int64_t b = bwd_layout(m, n, k, g * r, r).total;
   return static_cast<size_t>(f > b ? f : b);
@@ -524,7 +528,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
 qlora_status group_parts(const qlora_nf4_weight* w, int g, const int64_t* parts, int r, qlora::LoraParts* out) {
   if (w == nullptr || parts == nullptr) return QLORA_ERR_NULL;
   if (g < 1 || g > QLORA_MAX_PARTS || r < 1) return QLORA_ERR_SHAPE;
-  if (g * r > QLORA_MAX_RANK) return QLORA_ERR_UNSUPPORTED;
+  if (!rank_fits(g, r)) return QLORA_ERR_UNSUPPORTED;
   int64_t end = 0;
   out->g = g;
   out->rpart = r;
@@ -626,7 +630,7 @@ qlora_status qlora_linear_bwd_grouped_f16(const qlora_nf4_weight* w, int g, cons
 // Backward from an input kept as 8-bit rows
 // ---------------------------------------------------------------------------
 size_t qlora_linear_x8_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r) {
-  if (!linear_sizes_ok(m, n, k) || g < 1 || g > QLORA_MAX_PARTS || r < 0 || g * r > QLORA_MAX_RANK) return 0;
+  if (!linear_sizes_ok(m, n, k) || g < 1 || g > QLORA_MAX_PARTS || r < 0 || !rank_fits(g, r)) return 0;
   return static_cast<size_t>(x8_layout(m, n, k, g * r, r).total);
 }
 
@@ -681,14 +685,14 @@ qlora_status qlora_linear_bwd_grouped_x8_f16(const qlora_nf4_weight* w, int g, c
 // Gated feed-forward block
 // ---------------------------------------------------------------------------
 size_t qlora_linear_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int r) {
-  if (!linear_sizes_ok(m, n, k) || r < 0 || 2 * r > QLORA_MAX_RANK) return 0;
+  if (!linear_sizes_ok(m, n, k) || r < 0 || !rank_fits(2, r)) return 0;
   return static_cast<size_t>(gated_layout(m, n, k, 2 * r).total);
 }
 
 static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int64_t m, const uint16_t* a,
                               const uint16_t* b, int r, float alpha, int act, uint16_t* y, uint16_t* p, float* h_out,
                               void* ws, size_t ws_bytes, hipStream_t stream, bool f16) {
-  if (!known_act(act) || r > QLORA_MAX_RANK / 2) return QLORA_ERR_UNSUPPORTED;
+  if (!known_act(act) || !rank_fits(2, r)) return QLORA_ERR_UNSUPPORTED;
   if (r < 0) return QLORA_ERR_SHAPE;
   const int slots = 2 * r;
   const qlora_status st = check_fwd_args(w, x, m, a, b, slots, p, h_out);
