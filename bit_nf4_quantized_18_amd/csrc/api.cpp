@@ -437,7 +437,7 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
   if (x8 != nullptr &&
       !apart({span(dx, 2 * m * k), span(da, 4 * r * k), span(db, 4 * n * rpart),
               span(ws, restores ? L.total : static_cast<int64_t>(need))},
-             {span(r > 0 ? x8->codes : nullptr, m * x8->ld), span(r > 0 ? x8->scale : nullptr, 4 * m),
+             {span(r > 0 ? x8->codes : nullptr, r > 0 ? m * x8->ld : 0), span(r > 0 ? x8->scale : nullptr, 4 * m),
               span(dy, 2 * m * n), span(h_saved, 4 * m * r), span(a, 2 * r * k), span(b, 2 * n * rpart),
               span(w->codes, n * k / 2), span(w->scale_codes, n * k / 64), span(w->group_scale, group_bytes(n, k)),
               span(w->absmax, n * k / 16)}))

@@ -1,7 +1,7 @@
 // Host driver for arguments far outside their ranges in the grouped, gated-block and
 // 8-bit backward calls: api.cpp is built with AddressSanitizer and
 // UndefinedBehaviorSanitizer on the host side and linked with the library's kernel
-// objects. Every call is refused before a launch. Prints "abi_ranges_sanitize: all
+// objects, with every device hidden. Prints "abi_ranges_sanitize: all
 // checks passed" and exits 0, or names every failed check and exits 1.
 #include <hip/hip_runtime_api.h>
 
@@ -52,6 +52,16 @@ int main() {
     CHECK_EQ(qlora_linear_fwd_grouped(&w, 4, parts, u16(3), 20, u16(4), u16(5), r, 32.0f, u16(6), f32(8), at(9), many, nullptr),
              QLORA_ERR_UNSUPPORTED);
   }
+
+  // row lengths of inputs that are not read (no adapter) are not multiplied either; the
+  // call itself is fine and ends at its first launch, no device being visible
+  for (int64_t ld : {INT64_MIN, int64_t{-64}, int64_t{0}, INT64_MAX - 63, INT64_MAX})
+    for (int8_t* x : {static_cast<int8_t*>(nullptr), i8(10)}) {
+      CHECK_EQ(qlora_linear_bwd_x8(&w, x, ld, f32(11), u16(12), 20, nullptr, nullptr, 0, 32.0f, nullptr, u16(14), nullptr,
+                                   nullptr, at(17), many, nullptr), QLORA_ERR_HIP);
+      CHECK_EQ(qlora_linear_bwd_x8(&w, x, ld, f32(11), u16(12), 20, u16(4), u16(5), 16, 32.0f, f32(13), u16(14), f32(15),
+                                   f32(16), at(17), many, nullptr), x == nullptr ? QLORA_ERR_NULL : QLORA_ERR_SHAPE);
+    }
   if (g_failures == 0) std::printf("abi_ranges_sanitize: all checks passed\n");
   return g_failures == 0 ? 0 : 1;
 }
