@@ -95,7 +95,11 @@ struct Run {
       for (int e = 0; e < 8; ++e) {
         float slope;
         const float v = act_both<kFine>(a[e], g.act, &slope);
-        a[e] = d[e] * (u[e] * slope);  // |slope| < 1.13: no overflow that the result has not
+        // |slope| < 1.13: halved next to float32's end, where U act' may pass it and the
+        // result need not
+        const bool far = fabsf(u[e]) > 0x1p127f;
+        const float part = d[e] * (u[e] * (far ? 0.5f * slope : slope));
+        a[e] = far ? 2.0f * part : part;
         u[e] = d[e] * v;
       }
     } else {
