@@ -38,7 +38,8 @@ EXPORTS = ("qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd", "ql
            "qlora_linear_fwd_gated_f16", "qlora_linear_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_fwd_x8",
            "qlora_gated_bwd", "qlora_gated_bwd_x8", "qlora_int8_linear_fwd_gated", "qlora_linear_bwd_x8",
            "qlora_linear_bwd_x8_f16", "qlora_linear_bwd_grouped_x8", "qlora_linear_bwd_grouped_x8_f16",
-           "qlora_linear_x8_workspace_bytes")
+           "qlora_linear_x8_workspace_bytes", "qlora_linear_gated_least_workspace_bytes",
+           "qlora_linear_x8_least_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 16 << 20  # QLORA_NOALLOC_SCRATCH_BYTES
 
 CODEBOOK_NF4 = 0   # normal-quantile levels
@@ -137,7 +138,10 @@ def load():
     lib.qlora_linear_bwd_grouped_x8.argtypes = [wp, i32, p64, vp, i64, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp,
                                                 vp, sz, vp]
     lib.qlora_linear_x8_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
-    lib.qlora_linear_gated_workspace_bytes.restype = lib.qlora_linear_x8_workspace_bytes.restype = sz
+    for name in ("gated", "x8"):
+        full, least = (getattr(lib, f"qlora_linear_{name}_{s}workspace_bytes") for s in ("", "least_"))
+        least.argtypes = full.argtypes
+        full.restype = least.restype = sz
     for name in ("linear_fwd_gated", "linear_bwd_x8", "linear_bwd_grouped_x8"):
         fn, f16 = getattr(lib, f"qlora_{name}"), getattr(lib, f"qlora_{name}_f16")
         f16.argtypes = fn.argtypes
@@ -868,8 +872,13 @@ def int8_linear_fwd(q: PackedInt8, x: PackedInt8, dtype=None, out=None):
     return out
 
 
-def x8_workspace_bytes(m: int, n: int, k: int, g: int, r: int) -> int:
-    return int(load().qlora_linear_x8_workspace_bytes(m, n, k, g, r))
+def x8_workspace_bytes(m: int, n: int, k: int, g: int, r: int, restored: bool = True) -> int:
+    """For linear_bwd (g = 1) and linear_bwd_grouped from 8-bit rows. ``restored``: with the
+    weight restored to 16 bits where the call uses it, 2 n k bytes; without it a call takes
+    longer, but for one that needs no dX."""
+    lib = load()
+    fn = lib.qlora_linear_x8_workspace_bytes if restored else lib.qlora_linear_x8_least_workspace_bytes
+    return int(fn(m, n, k, g, r))
 
 
 def _linear_bwd_x8(q, parts, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws):
@@ -905,7 +914,7 @@ def _linear_bwd_x8(q, parts, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws):
     elif need_dx:
         dx = dy.new_empty(m, k)
     if ws is None:
-        nbytes = _LIB.qlora_linear_x8_workspace_bytes(m, n, k, g, r)
+        nbytes = x8_workspace_bytes(m, n, k, g, r, restored=dx is not None)
         ws = dy.new_empty(nbytes, dtype=_torch.uint8) if nbytes else None
     else:
         _need_ws(ws, dev)
@@ -923,9 +932,13 @@ def _linear_bwd_x8(q, parts, x, dy, a, b, alpha, h, need_dx, dx, da, db, ws):
 
 
 # ---------------------------------------------------------------- gated block
-def gated_workspace_bytes(m: int, n: int, k: int, r: int) -> int:
-    """For linear_fwd_gated over a stacked weight of n rows (gate's and up's)."""
-    return int(load().qlora_linear_gated_workspace_bytes(m, n, k, r))
+def gated_workspace_bytes(m: int, n: int, k: int, r: int, restored: bool = True) -> int:
+    """For linear_fwd_gated over a stacked weight of n rows (gate's and up's). ``restored``:
+    with the weight restored to 16 bits where the call uses it, 2 n k bytes; without it the
+    call takes longer."""
+    lib = load()
+    fn = lib.qlora_linear_gated_workspace_bytes if restored else lib.qlora_linear_gated_least_workspace_bytes
+    return int(fn(m, n, k, r))
 
 
 def linear_fwd_gated(q: PackedNF4, x, a=None, b=None, alpha: float = 0.0, act: int = ACT_SILU, want_y: bool = True,

@@ -432,11 +432,13 @@ qlora_status linear_bwd_impl(const qlora_nf4_weight* w, const qlora::LoraParts* 
 
   const BwdLayout L = x8 != nullptr ? x8_layout(m, n, k, r, rpart) : bwd_layout(m, n, k, r, rpart);
   // From 8-bit rows: the weight is restored once where that pays and the workspace
-  // holds it (without dX not at all, but dH is then formed as it is beside it).
-  const bool restores = x8 != nullptr && L.total > L.w16 && ws != nullptr && ws_bytes >= static_cast<size_t>(L.total);
+  // holds it (without dX not at all, and nothing has to hold it, but dH is then formed
+  // as it is beside it).
+  const bool restores = x8 != nullptr && L.total > L.w16 &&
+                        (dx == nullptr || (ws != nullptr && ws_bytes >= static_cast<size_t>(L.total)));
   if (x8 != nullptr &&
       !apart({span(dx, 2 * m * k), span(da, 4 * r * k), span(db, 4 * n * rpart),
-              span(ws, restores ? L.total : static_cast<int64_t>(need))},
+              span(ws, restores && dx != nullptr ? L.total : static_cast<int64_t>(need))},
              {span(r > 0 ? x8->codes : nullptr, r > 0 ? m * x8->ld : 0), span(r > 0 ? x8->scale : nullptr, 4 * m),
               span(dy, 2 * m * n), span(h_saved, 4 * m * r), span(a, 2 * r * k), span(b, 2 * n * rpart),
               span(w->codes, n * k / 2), span(w->scale_codes, n * k / 64), span(w->group_scale, group_bytes(n, k)),
@@ -629,9 +631,16 @@ qlora_status qlora_linear_bwd_grouped_f16(const qlora_nf4_weight* w, int g, cons
 // ---------------------------------------------------------------------------
 // Backward from an input kept as 8-bit rows
 // ---------------------------------------------------------------------------
+static bool x8_sizes_ok(int64_t m, int64_t n, int64_t k, int g, int r) {
+  return linear_sizes_ok(m, n, k) && g >= 1 && g <= QLORA_MAX_PARTS && r >= 0 && rank_fits(g, r);
+}
+
 size_t qlora_linear_x8_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r) {
-  if (!linear_sizes_ok(m, n, k) || g < 1 || g > QLORA_MAX_PARTS || r < 0 || !rank_fits(g, r)) return 0;
-  return static_cast<size_t>(x8_layout(m, n, k, g * r, r).total);
+  return x8_sizes_ok(m, n, k, g, r) ? static_cast<size_t>(x8_layout(m, n, k, g * r, r).total) : 0;
+}
+
+size_t qlora_linear_x8_least_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r) {
+  return x8_sizes_ok(m, n, k, g, r) ? static_cast<size_t>(x8_layout(m, n, k, g * r, r).w16) : 0;
 }
 
 static qlora_status bwd_x8(const qlora_nf4_weight* w, int g, const int64_t* parts, const int8_t* x, int64_t ldx,
@@ -684,9 +693,16 @@ qlora_status qlora_linear_bwd_grouped_x8_f16(const qlora_nf4_weight* w, int g, c
 // ---------------------------------------------------------------------------
 // Gated feed-forward block
 // ---------------------------------------------------------------------------
+static bool gated_sizes_ok(int64_t m, int64_t n, int64_t k, int r) {
+  return linear_sizes_ok(m, n, k) && r >= 0 && rank_fits(2, r);
+}
+
 size_t qlora_linear_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int r) {
-  if (!linear_sizes_ok(m, n, k) || r < 0 || !rank_fits(2, r)) return 0;
-  return static_cast<size_t>(gated_layout(m, n, k, 2 * r).total);
+  return gated_sizes_ok(m, n, k, r) ? static_cast<size_t>(gated_layout(m, n, k, 2 * r).total) : 0;
+}
+
+size_t qlora_linear_gated_least_workspace_bytes(int64_t m, int64_t n, int64_t k, int r) {
+  return gated_sizes_ok(m, n, k, r) ? static_cast<size_t>(gated_layout(m, n, k, 2 * r).w16) : 0;
 }
 
 static qlora_status fwd_gated(const qlora_nf4_weight* w, const uint16_t* x, int64_t m, const uint16_t* a,

@@ -382,11 +382,12 @@ size_t qlora_linear_grouped_workspace_bytes(int64_t m, int64_t n, int64_t k, int
  *           once. H enters these sums as float32 at every m (the linear calls
  *           round s H to 16 bits above 16 tokens).
  *   h_out : float32 m x (2 r), [H_1 | H_2]; may be NULL.
- *   ws    : qlora_linear_gated_workspace_bytes(m, w->n, k, r) bytes. Their last
- *           2 w->n k are, where the size counts them, for the weight restored to
- *           16 bits; a workspace without them is taken too, and the weight then
- *           restored as it is multiplied (the same bounds, more time; sums in
- *           another order).
+ *   ws    : qlora_linear_gated_workspace_bytes(m, w->n, k, r) bytes, which hold the
+ *           weight restored to 16 bits (2 w->n k, four times the packed weight)
+ *           where that is faster. Less is taken too, down to
+ *           qlora_linear_gated_least_workspace_bytes(m, w->n, k, r); the weight is
+ *           then restored as it is multiplied (the same bounds; sums in another
+ *           order).
  * Outputs and workspace overlap neither an input nor each other. The backward is
  * qlora_gated_bwd for d[G | U], then qlora_linear_bwd_grouped. m = 0 is a no-op.
  * Errors: NULL / ALIGN / SHAPE (as qlora_linear_fwd; w->n % 512 != 0) / UNSUPPORTED
@@ -401,9 +402,11 @@ qlora_status qlora_linear_fwd_gated_f16(const qlora_nf4_weight* w, const uint16_
                                         int act, uint16_t* y, uint16_t* p, float* h_out, void* ws,
                                         size_t ws_bytes, hipStream_t stream);
 
-/* Workspace bytes of the two calls above (n = w->n, both parts' rows); 0 if none
- * is needed and for invalid sizes. Host only, no GPU use. */
+/* Workspace bytes of the two calls above (n = w->n, both parts' rows), with the
+ * restored weight where the calls use it, and without; 0 if none is needed and for
+ * invalid sizes. Host only, no GPU use. */
 size_t qlora_linear_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int r);
+size_t qlora_linear_gated_least_workspace_bytes(int64_t m, int64_t n, int64_t k, int r);
 
 /* The block's product alone and its gradient, element by element in float32:
  *   P = act(G) U;    dG = dP U act'(G),  dU = dP act(G).
@@ -442,8 +445,9 @@ qlora_status qlora_gated_bwd_x8(const int8_t* codes, int64_t ld, const float* sc
  *   h               : float32 m x r (m x (g r)), from the forward's h_out;
  *                     required (H is not formed again from rounded rows).
  *   ws              : qlora_linear_x8_workspace_bytes(m, n, k, g, r) bytes (g = 1
- *                     for the plain calls); the last 2 n k, where the size counts
- *                     them, may be left out as in qlora_linear_fwd_gated.
+ *                     for the plain calls), or less, down to
+ *                     qlora_linear_x8_least_workspace_bytes, as in
+ *                     qlora_linear_fwd_gated. With dx NULL no more than that is used.
  * The other arguments, limits and errors are those of the calls with a 16-bit
  * input; UNSUPPORTED also for outputs or a workspace that overlap an input or
  * each other, SHAPE for a bad ldx. With r = 0 the rows are not read. */
@@ -470,8 +474,10 @@ qlora_status qlora_linear_bwd_grouped_x8_f16(const qlora_nf4_weight* w, int g, c
                                              uint16_t* dx, float* da, float* db, void* ws,
                                              size_t ws_bytes, hipStream_t stream);
 
-/* Workspace bytes of the four calls above; 0 for invalid sizes. Host only. */
+/* Workspace bytes of the four calls above, with the restored weight where the calls
+ * use it, and without; 0 for invalid sizes. Host only. */
 size_t qlora_linear_x8_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r);
+size_t qlora_linear_x8_least_workspace_bytes(int64_t m, int64_t n, int64_t k, int g, int r);
 
 /* Merge a trained adapter into the weight: out (n x k, row-major) =
  * fl32(W16 + t), where W16 is the bf16 dequantized weight (as
