@@ -8,6 +8,10 @@
 // 4096 holds 39 MB and takes 13.7 us (2.9 TB/s), and 5 for the sums of two splits; k =
 // 4096, n = 22016 in two parts 99 MB in 32 us (3.1 TB/s). With what a step computes from
 // its loads in front of the step before it, whose loads then wait for it, 25 us for 14.
+// Above rank 16 V is read once for every 32 slots of a part (codes for every 32 of all):
+// the first size takes 19 us at rank 32, 30 at 64 and 56 at 128, the second 31 and 54 at
+// 32 and 64; with both steps' U in registers, which spills, 27, 45, 86, 48 and 66, and 16
+// slots at a time 21, 39, 75, 42 and 86.
 //
 // Matrix cores in bf16 with float32 sums (v_mfma_f32_16x16x32_bf16), every
 // float32 U split into three bf16 terms that hold all of its 24 bits (the low 16
@@ -127,19 +131,26 @@ __device__ __forceinline__ void solve(const Problem& p, int64_t M, int id, int s
 
   // A step's operands as loaded; nothing is computed from them before the step, so
   // that the next one's loads are in flight under it. Rows past the last are read
-  // from it and multiplied by zeros.
+  // from it and multiplied by zeros. With 32 slots U, which stays in L2, is loaded at the
+  // step itself: two steps of it leave no registers, and a spilled load has to arrive
+  // before it can be stored, in front of the step that it should be in flight under.
   typedef typename Block<kKind>::Word Word;
-  struct Step {
-    Block<kKind> b;
+  struct Slots {
     float u[RT][8], scale[kKind == kCodes ? 8 : 1];
   };
-  auto load = [&](int64_t m0, Step& s) {
+  struct Step {
+    Block<kKind> b;
+    Slots s;
+  };
+  constexpr bool kAhead = RT == 1;
+  auto row_of = [&](int64_t m0, int e) {
+    const int64_t m = m0 + 8 * g + e;
+    return m < M ? m : M - 1;
+  };
+  auto load_slots = [&](int64_t m0, Slots& s) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t m = m0 + 8 * g + e;
-      const int64_t mr = m < M ? m : M - 1;
-      const char* row = static_cast<const char*>(p.v) + (mr * p.ldv + col) * (kKind == kCodes ? 1 : 2);
-      s.b.w[e] = *reinterpret_cast<const Word*>(row);
+      const int64_t mr = row_of(m0, e);
       if (kKind == kCodes) s.scale[e] = p.uscale[mr];
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
@@ -148,15 +159,25 @@ __device__ __forceinline__ void solve(const Problem& p, int64_t M, int id, int s
       }
     }
   };
-  auto multiply = [&](int64_t m0, const Step& s) {
+  auto load = [&](int64_t m0, Step& s) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const char* row = static_cast<const char*>(p.v) + (row_of(m0, e) * p.ldv + col) * (kKind == kCodes ? 1 : 2);
+      s.b.w[e] = *reinterpret_cast<const Word*>(row);
+    }
+    if (kAhead) load_slots(m0, s.s);
+  };
+  auto multiply = [&](int64_t m0, Step& s) {
+    if (!kAhead) load_slots(m0, s.s);
     Terms terms[RT];
 #pragma unroll
     for (int a = 0; a < RT; ++a) {
       float uv[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        uv[e] = m0 + 8 * g + e < me && j0 + 16 * a + i < p.slots ? (kKind == kCodes ? s.u[a][e] * s.scale[e] : s.u[a][e])
-                                                                 : 0.0f;
+        uv[e] = m0 + 8 * g + e < me && j0 + 16 * a + i < p.slots
+                    ? (kKind == kCodes ? s.s.u[a][e] * s.s.scale[e] : s.s.u[a][e])
+                    : 0.0f;
       terms[a] = split3(uv);
     }
 #pragma unroll
