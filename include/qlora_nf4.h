@@ -390,6 +390,11 @@ size_t qlora_linear_grouped_workspace_bytes(int64_t m, int64_t n, int64_t k, int
  *           order).
  * Outputs and workspace overlap neither an input nor each other. The backward is
  * qlora_gated_bwd for d[G | U], then qlora_linear_bwd_grouped. m = 0 is a no-op.
+ * There is no form with dropout on the adapters' input (qlora_linear_fwd_dropout).
+ * x, a and b are finite, as in every linear call. What is not comes out as NaN or
+ * infinity (an infinity as either) where it enters: a token in its own rows of y, p
+ * and h_out, a row of a in its slot of h_out and, through it, in y and p of both
+ * parts, a row of b in its own output; nowhere else.
  * Errors: NULL / ALIGN / SHAPE (as qlora_linear_fwd; w->n % 512 != 0) / UNSUPPORTED
  * (act, r, overlapping buffers) / WORKSPACE / HIP. The _f16 call has IEEE half
  * as its 16-bit type. */
@@ -448,6 +453,10 @@ qlora_status qlora_gated_bwd_x8(const int8_t* codes, int64_t ld, const float* sc
  *                     for the plain calls), or less, down to
  *                     qlora_linear_x8_least_workspace_bytes, as in
  *                     qlora_linear_fwd_gated. With dx NULL no more than that is used.
+ * There is no form with dropout (qlora_linear_bwd_dropout). dy, a, b and h are
+ * finite. What is not comes out as NaN or infinity (an infinity as either) in the
+ * outputs that depend on it, of every part; elsewhere only as the linear calls do it,
+ * from dy at a ragged edge.
  * The other arguments, limits and errors are those of the calls with a 16-bit
  * input; UNSUPPORTED also for outputs or a workspace that overlap an input or
  * each other, SHAPE for a bad ldx. With r = 0 the rows are not read. */
