@@ -10,9 +10,10 @@
 // Rows of bytes as in the 8-bit product: both operands are copied from memory into
 // a ring of units (128 bytes of the tile's rows, 64 elements), read as fragments
 // half a unit ahead and multiplied by v_mfma_f32_16x16x32. The adapter's slots
-// follow as more contraction, with operands straight from memory. 2048 x 22016 x 4096,
-// gated: 275 to 300 us (1.23 to 1.34 PFLOP/s; the library's 8192^3 product reaches 1.52)
-// behind 44 to 48 us of restoring (5.8 TB/s); the fused product takes 392 in all.
+// follow as more contraction, with operands straight from memory and H or dH in three
+// 16-bit terms (0.6% of this call at rank 16, 9% at 64). 2048 x 22016 x 4096, gated: 275 to 300
+// us (1.23 to 1.34 PFLOP/s; the library's 8192^3 product reaches 1.52) behind 44 to 48 us
+// of restoring (5.8 TB/s); the fused product takes 396 in all.
 #include "bufmem.h"
 #include "dense_rule.h"
 #include "gate.h"

@@ -13,10 +13,10 @@ constexpr int64_t kDenseMaxK = 65536;
 // Whether dH = s dY B over n weight rows is formed beside the restoring, 16 tokens and
 // 16 slots a workgroup whose lanes read B in strided loads, or behind it from B^T. Whole
 // calls, us, beside / behind, 17 and 2048 tokens:
-//   1040 x 1088, 16 slots  16.5 / 23.3, 31 / 39; 64 slots 19.0 / 27.3, 43 / 55
-//   2048 x 2048, 16 slots  21.0 / 24.1, 43 / 48; 64 slots 23.0 / 29.2, 57 / 68
-//   4096 x 4096, 16 slots  41.4 / 39.5, 94 / 96; 64 slots 44.9 / 44.1, 118 / 121
-//   6656 x 4544, 16 slots  57.2 / 47.3, 167 / 161; 64 slots 61.0 / 50.8, 204 / 195
+//   1040 x 1088, 16 slots  18.3 / 23.6, 35 / 41; 64 slots 21.0 / 29.1, 44 / 56
+//   2048 x 2048, 16 slots  22.6 / 25.3, 45 / 50; 64 slots 24.6 / 30.9, 55 / 63
+//   4096 x 4096, 16 slots  42.4 / 40.8, 94 / 95; 64 slots 46.5 / 45.8, 111 / 114
+//   6656 x 4544, 16 slots  59.2 / 48.3, 170 / 164; 64 slots 62.8 / 52.6, 198 / 189
 constexpr int64_t kDenseNarrow = 4096;
 inline bool dense_narrow(int64_t n) { return n <= kDenseNarrow; }
 
@@ -27,22 +27,25 @@ inline bool dense_fits(int64_t m, int64_t out, int64_t con) {
   return con <= kDenseMaxK && m < (INT64_C(1) << 22) && pick_shape(m, out, 2 * con).shape >= 0;
 }
 
-// The two sides' microseconds, fitted to 114 measured calls (17 .. 4096 tokens, 0.5 M
-// .. 360 M weights, forward and backward, rank 16), where the smaller estimate names the
-// slower side by more than 2% twice (3% and 4%). Fused: rounds of the 256 CUs over 256 x
-// 128 tiles, in steps of 64, and H or dH in launches of their own. Dense: 2.5 bytes a
-// weight to restore it, then the tiles of the 8-bit product, whose units of 128 bytes
-// take about as long, or reading 2 bytes a weight.
+// The two sides' microseconds, to choose by and no more: fitted to 114 measured calls (17
+// .. 4096 tokens, 0.5 M .. 360 M weights, forward and backward, rank 16), where the
+// smaller estimate names the slower side by more than 2% twice (3% and 4%). Fused: rounds
+// of the 256 CUs over 256 x 128 tiles, in steps of 64, and H or dH in launches of their
+// own. Dense: 2.5 bytes a weight to restore it, then the tiles of the 8-bit product, whose
+// units of 128 bytes take about as long, or reading 2 bytes a weight. Few tokens of a
+// large weight are estimated high on that side (64 x 22016 x 4096: 105 us, 71 measured: the
+// restored weight is read back faster than counted), where the fused side still is the
+// faster one. A side that gets faster needs the fit again.
 // Some of the calls, fused / dense, us:
 //   tokens                            64           333          2048         4096
-//   forward 22016 x 4096          65 / 71     123 / 121     392 / 350    745 / 647
-//   forward 44032 x 8192        221 / 350                 1389 / 1279
-//   forward 2560 x 5120           75 / 41       79 / 42       81 / 78    158 / 121
-//   forward 5120 x 1088           30 / 18       31 / 23       55 / 43      83 / 73
+//   forward 22016 x 4096          67 / 71     125 / 122     396 / 346    739 / 635
+//   forward 44032 x 8192        222 / 340     345 / 526   1366 / 1285  2733 / 2327
+//   forward 2560 x 5120           75 / 38       81 / 40       83 / 79    161 / 129
+//   forward 5120 x 1088           31 / 19       33 / 22       59 / 45      87 / 80
 //   tokens                            64           256          1024         4096
-//   backward 22016 x 4096       278 / 108     282 / 136     294 / 258    735 / 650
-//   backward 4096 x 11008         72 / 53       74 / 66     141 / 121    409 / 347
-//   backward 8192 x 22016       119 / 222     123 / 253     382 / 462
+//   backward 22016 x 4096       282 / 113     287 / 142     295 / 251    711 / 637
+//   backward 4096 x 11008         74 / 54       76 / 68     141 / 121    412 / 350
+//   backward 8192 x 22016       121 / 221     127 / 254     378 / 463  1373 / 1209
 inline double fused_us(int64_t m, int64_t out, int64_t con) {
   const int64_t tiles = ((m + 255) / 256) * ((out + 127) / 128);
   return 6 + static_cast<double>((tiles + 255) / 256) * (6 + 0.9 * static_cast<double>((con + 63) / 64));

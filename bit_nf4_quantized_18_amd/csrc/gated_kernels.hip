@@ -8,8 +8,9 @@
 // gradients. A thread takes kRuns runs of eight columns, all of whose loads are
 // issued before the first is waited for; a run that the row's end cuts goes
 // element by element. Measured: the product of 2048 x 11008 from 8-bit rows 21.6 us
-// (4.2 TB/s), the gradient of 4096 x 22016 from them 126 us (5.7 TB/s); 37 x 5001 4.8 us,
-// nearly all of it start and end.
+// (4.2 TB/s), the gradient of 4096 x 22016 from them 126 us (5.7 TB/s); from bf16 rows
+// 24 us (5.6) and 166 (5.5), from float32 46 (5.9) and 340 (5.3). The gradient of 37 x
+// 5001 in float32 5.0 us, nearly all of it start and end.
 #include "elem.h"
 #include "gate.h"
 

@@ -41,6 +41,8 @@
 // output columns of one token row and stores 8 contiguous bytes. Tiles are
 // ordered so that the workgroups on one XCD (ids congruent mod 8) share token
 // rows in that XCD's L2. The rank-r LoRA term is one more pass of MFMAs.
+// kTerms (the gated block, and dX from 8-bit rows): Hs or dHs is float32, in three bf16 terms,
+// so two more passes (fp16, whose B or At has two terms itself: four more).
 // kF16 builds the same kernel for IEEE-half compute: half lookup tables, the
 // f16 MFMA and a half output; everything else is bit-pattern movement.
 //
@@ -49,7 +51,7 @@
 // rows of the same outputs, 16 of each in turn, so that a lane's accumulators
 // hold both pre-activations of an output and the product act(gate) up is formed
 // from them unrounded: 256 x 64 outputs a tile, and the pre-activations are
-// written only where the backward pass wants them. 64 x 22016 x 4096 takes 64 us, bound
+// written only where the backward pass wants them. 64 x 22016 x 4096 takes 67 us, bound
 // by the steps of its one round; dense_rule.h has the sizes that go another way.
 #include <type_traits>
 

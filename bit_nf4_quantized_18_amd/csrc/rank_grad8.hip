@@ -6,7 +6,7 @@
 //
 // Bound by reading V once: k + 2 n bytes a token. 2048 tokens, rank 16: k = 11008, n =
 // 4096 holds 39 MB and takes 13.7 us (2.9 TB/s), and 5 for the sums of two splits; k =
-// 4096, n = 22016 in two parts 99 MB in 32 us (3.1 TB/s). With what a step computes from
+// 4096, n = 22016 in two parts 99 MB in 25 us (4.0 TB/s). With what a step computes from
 // its loads in front of the step before it, whose loads then wait for it, 25 us for 14.
 // Above rank 16 V is read once for every 32 slots of a part (codes for every 32 of all):
 // the first size takes 19 us at rank 32, 30 at 64 and 56 at 128, the second 31 and 54 at
@@ -282,8 +282,8 @@ int64_t workgroups(int64_t n, int64_t k, int slots, int r) {
 
 int rank_grad8_splits(int64_t m, int64_t n, int64_t k, int slots, int r) {
   // About a workgroup a CU, a step at least for each of its waves. 2048 tokens, n = 4096,
-  // k = 11008: 13.7 us with two splits, 16.0 with four; k = 4096, n = 22016 in two parts:
-  // 32 us and no second launch with one, 33 and 6 with two.
+  // k = 11008: 13.7 us with two splits, 16.1 with four; k = 4096, n = 22016 in two parts:
+  // 25 us and no second launch with one, 26 and 6 with two.
   int64_t s = 256 / workgroups(n, k, slots, r);
   const int64_t by_rows = m / (kWaves * kRows);
   if (s > by_rows) s = by_rows;
